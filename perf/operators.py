@@ -372,7 +372,7 @@ def _product(s, a, w):
 
 
 def _plain_fprop(s):
-    I, O, total = s["I"], s["O"], s["total"]
+    E, I, O, total = s["E"], s["I"], s["O"], s["total"]
     x = _gathered(s)
     a, sa = _quantized(x, x.abs().amax())
     codes, scales, amax = s["w"]
