@@ -170,7 +170,7 @@ def _weights(case, gen, transposed):
         w = (0.02 * torch.randn(n, I, generator=gen, device="cuda")).clamp(-0.125, 0.125)
         w = w.bfloat16().float()
         b = w.abs().view(n // 16, 16, I // 16, 16).amax(dim=(1, 3)).repeat_interleave(16, 0)
-        sf = ((b / 6) * s_enc).clamp(max=448).to(torch.float8_e4m3fn)
+        sf = _scale_code(b, s_enc)
         r = _element_factor(sf.float(), s_enc).repeat_interleave(16, 1)
         index = _nearest(w.abs() * r)
         nib = (index + 8 * (w < 0)).to(torch.uint8).view(n, I // 2, 2)
@@ -270,8 +270,19 @@ def _run_own(s):
 
 # ---- the plain forms -------------------------------------------------------------------------
 
+def _over(a, b):
+    """a / b rounded to nearest: torch divides two tensors, but takes the quotient of a tensor and
+    a number as a product with a rounded reciprocal."""
+    return torch.as_tensor(a, dtype=b.dtype, device=b.device).expand_as(b) / b
+
+
 def _tensor_scale(amax):
-    return torch.where(amax == 0, 1.0, (2688.0 / amax).clamp(max=FLT_MAX))
+    return torch.where(amax == 0, 1.0, _over(2688.0, amax).clamp(max=FLT_MAX))
+
+
+def _scale_code(b, s_enc):
+    """E4M3 code of (b / 6) s_enc."""
+    return ((b / torch.full_like(b, 6.0)) * s_enc).clamp(max=448).to(torch.float8_e4m3fn)
 
 
 def _element_factor(sf, s_enc):
@@ -315,7 +326,7 @@ def _quantized(y, amax, seed=None, offset=0):
     R, C = y.shape
     s_enc = _tensor_scale(amax)
     b = y.abs().view(R, C // 16, 16).amax(-1)
-    sf = ((b / 6) * s_enc).clamp(max=448).to(torch.float8_e4m3fn).float()
+    sf = _scale_code(b, s_enc).float()
     v = y.abs() * _element_factor(sf, s_enc).repeat_interleave(16, 1)
     if seed is None:
         index = _nearest(v)
