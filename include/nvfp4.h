@@ -77,9 +77,11 @@ enum {
     NVFP4_DEVSTAT_NONFINITE = 1, /* a quantizer input (or its transform) held NaN/Inf     */
     NVFP4_DEVSTAT_TIMEOUT = 2,   /* a GEMM pipeline wait exceeded its time limit; the
                                     output of that GEMM is undefined                     */
-    NVFP4_DEVSTAT_BOUNDS = 4     /* (debug build only, see nvfp4_bounds_checked) a kernel
+    NVFP4_DEVSTAT_BOUNDS = 4,    /* (debug build only, see nvfp4_bounds_checked) a kernel
                                     computed a global access outside its buffer and
                                     skipped it; the outputs of that call are undefined   */
+    NVFP4_DEVSTAT_INDEX = 8      /* a routing named an expert outside [-1, E); the pair was
+                                    treated as having no expert                          */
 };
 
 /* Quantizer flags. */
@@ -91,7 +93,8 @@ enum {
     NVFP4_AMAX_GIVEN = 16,/* skip the amax pass: read the tensor amax from the output
                              operand's `amax` (out_row's if present, else out_col's); the
                              data must then be finite                                    */
-    NVFP4_MX = 32         /* MXFP4 instead of NVFP4 (see below); not with NVFP4_BLOCK2D  */
+    NVFP4_MX = 32,        /* MXFP4 instead of NVFP4 (see below); not with NVFP4_BLOCK2D  */
+    NVFP4_GATHER = 64     /* nvfp4_quantize_grouped only: x has a row per token          */
 };
 
 /* MXFP4, the comparison format of [P1 Formato NVFP4; Nuevo Formato NVFP4] (OCP MX):
@@ -357,6 +360,194 @@ nvfp4_status nvfp4_quantize_noalloc(const void* x_bf16, int64_t rows, int64_t co
                                     unsigned flags, uint64_t seed, uint64_t offset,
                                     const nvfp4_operand* out_row, const nvfp4_operand* out_col,
                                     int* dev_status, void* stream);
+
+/*
+ * ---- Mixture-of-experts layers ---------------------------------------------------------
+ * A layer with E experts whose weights are E matrices W_e [O x I]; every token is multiplied by
+ * those of its k experts.  The pages have no counterpart to these calls: they carry the recipe's
+ * quantization and GEMMs of a linear layer over to a layer of experts.
+ *
+ *   nvfp4_route -> nvfp4_plan_experts -> nvfp4_experts_fprop (up, gathering the tokens) ->
+ *   activation -> nvfp4_experts_fprop (down) -> nvfp4_combine
+ *   and back: nvfp4_combine_backward -> nvfp4_experts_{dgrad,wgrad} (down) -> activation's
+ *   gradient -> nvfp4_experts_{dgrad,wgrad} (up) -> nvfp4_combine without weights (the gradient
+ *   of the gather), nvfp4_route_backward
+ *
+ * Expert order.  A pair is (token t, slot j), its index t * k + j.  An expert-ordered matrix has
+ * `rows` rows; expert e owns the region offsets[e] .. offsets[e + 1], whose length is the number of
+ * its pairs rounded up to a multiple of 128: one row per pair in the order of the pairs' indices,
+ * then rows without a token, which count as zeros.  Rows behind offsets[E] are neither read nor
+ * written by any call here.
+ * All sizes that depend on the routing stay on the device: every call may be captured in a graph
+ * and replayed for another routing.
+ * The indices in a plan are checked where they are used (a token outside [0, tokens), a row beyond
+ * `rows` count as absent), so that a plan of another routing gives wrong results but no access
+ * outside the buffers.
+ */
+enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
+
+/* The expert-ordered rows of a routing of `tokens` tokens to k of `experts` experts each.  Device
+ * pointers (4-byte aligned), written by nvfp4_plan_experts:
+ *   offsets   : experts + 1 int32, the regions
+ *   pair_row  : tokens * k int32, the row of every pair (-1: the pair has no expert)
+ *   row_token : rows int32, the token of every row (-1: none)
+ * Limits: 1 <= k <= 32, 1 <= experts <= 512, tokens * k < 2^31; rows a multiple of 128, at least
+ * nvfp4_expert_rows(tokens, k, experts) and at most 8388480. */
+typedef struct {
+    int32_t* offsets;
+    int32_t* pair_row;
+    int32_t* row_token;
+    int64_t tokens;
+    int64_t k;
+    int64_t experts;
+    int64_t rows;
+} nvfp4_expert_plan;
+
+/* Rows that hold every routing of T tokens to k of E experts; 0 for sizes outside the limits. */
+int64_t nvfp4_expert_rows(int64_t T, int64_t k, int64_t E);
+
+/* Device workspace of nvfp4_plan_experts (0 for few pairs: no workspace is needed). */
+size_t nvfp4_expert_plan_workspace_bytes(int64_t T, int64_t k, int64_t E);
+
+/*
+ * Experts and weights of every token from its router logits.
+ *   logits  : T x E, FP32 or bf16 (dtype: NVFP4_OUT_F32 / NVFP4_OUT_BF16), row stride ld elements.
+ *             -inf excludes an expert.  A row with NaN or +inf is routed nowhere (indices -1,
+ *             weights 0) and sets NVFP4_DEVSTAT_NONFINITE.
+ *   score   : NVFP4_SCORE_SOFTMAX over the E logits, or NVFP4_SCORE_SIGMOID of each.
+ *   bias    : E FP32 added to the scores for the choice only (not to the weights), or NULL.  -inf
+ *             excludes an expert; NaN and +inf are treated as in logits.
+ *   groups, top_groups : with groups > 1 the experts form `groups` equal ranges, and only those in
+ *             the top_groups ranges with the largest sum of their two best values (score + bias; of
+ *             the one if only one is not excluded) are candidates.  groups <= 32.
+ *   k       : experts per token, k <= E / groups * top_groups; chosen in falling order of score +
+ *             bias.  Equal values go to the lower index.  The choice is that of scores in FP64
+ *             (comparisons closer than FP32's error are decided there).
+ *   experts : T x k int32 out; -1 where fewer than k experts can be chosen.
+ *   weights : T x k FP32 out: scale * score, divided by the sum of the chosen scores with
+ *             `renormalize`; 0 where the expert is -1.
+ */
+nvfp4_status nvfp4_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                         const float* bias, int score, int groups, int top_groups, int k,
+                         int renormalize, float scale, int32_t* experts, float* weights,
+                         int* dev_status, void* stream);
+
+/*
+ * Gradient of nvfp4_route's weights with respect to the logits (the choice itself has none).
+ *   experts, dweights : T x k; pairs with expert -1 have no part.  An expert named twice counts
+ *             twice.  Other indices outside [0, E) count as -1 and set NVFP4_DEVSTAT_INDEX.
+ *   dlogits : T x E of the logits' type, row stride ldd, all written (zeros where no gradient
+ *             arrives, and for rows without an expert).
+ */
+nvfp4_status nvfp4_route_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,
+                                  const int32_t* experts, const float* dweights, int score, int k,
+                                  int renormalize, float scale, void* dlogits, int64_t ldd,
+                                  int* dev_status, void* stream);
+
+/*
+ * The plan of a routing: fills plan->offsets, pair_row and row_token (all rows) from
+ * experts (tokens x k).  Indices outside [-1, E) count as -1 and set NVFP4_DEVSTAT_INDEX; an
+ * expert named twice by a token gets two rows.
+ *   workspace : nvfp4_expert_plan_workspace_bytes(...) device bytes (NULL if 0).
+ */
+nvfp4_status nvfp4_plan_experts(const int32_t* experts, const nvfp4_expert_plan* plan,
+                                void* workspace, int* dev_status, void* stream);
+
+/*
+ * Quantize an expert-ordered matrix (rows x cols) to NVFP4: what nvfp4_quantize(NVFP4_ROWWISE) and
+ * nvfp4_rht_quantize give of it, in its regions; the amax is taken over them too.
+ *   x       : bf16, row stride ld.  With NVFP4_GATHER a matrix with a row per token (tokens x
+ *             cols): row r of the quantized matrix is x[row_token[r]].  Otherwise a matrix in
+ *             expert order (rows x cols).  Rows of x that no pair takes are not looked at.
+ *   flags   : NVFP4_ROWWISE (out_row, rows x cols) and/or NVFP4_COLWISE (out_col, cols x rows,
+ *             random-Hadamard-transformed along the rows with sign_mask); NVFP4_SR,
+ *             NVFP4_AMAX_GIVEN (each output's amax is read from it), NVFP4_GATHER.
+ *   seed, offset : NVFP4_SR draws stream `offset` for out_row and `offset` + 1 for out_col, with the
+ *             element indices of the rows x cols (cols x rows) matrix.
+ *   workspace : nvfp4_workspace_bytes(rows, cols, flags) device bytes (NULL if 0).
+ * Shape rules: cols a multiple of 64 (16 with NVFP4_COLWISE alone), ld >= cols, ld % 8 == 0.
+ */
+nvfp4_status nvfp4_quantize_grouped(const void* x_bf16, int64_t cols, int64_t ld,
+                                    const nvfp4_expert_plan* plan, uint16_t sign_mask,
+                                    unsigned flags, uint64_t seed, uint64_t offset,
+                                    const nvfp4_operand* out_row, const nvfp4_operand* out_col,
+                                    void* workspace, int* dev_status, void* stream);
+
+/*
+ * Every expert's rows times its matrix: D[r, :] = A[r, :] . B_e^T for the rows r of expert e
+ * (rows without a token give zeros, rows behind the last region are not written).
+ *   A : rows x K operand in expert order.
+ *   B : the E matrices B_e [N x K], stacked (an (E * N) x K operand; N a multiple of 128 if E > 1)
+ *       or side by side (an N x (E * K) operand).  For a layer's weights W_e [O x I] stacked in one
+ *       (E * O) x I matrix these are the row-wise output of nvfp4_quantize (forward) and its
+ *       column-wise output (data gradient).
+ *   D : device, rows x N, row stride ldd, FP32 or bf16.
+ * Shape rules: K a multiple of 64, N of 16; ldd as in nvfp4_gemm.
+ */
+nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* A, const nvfp4_operand* B,
+                                const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
+                                int* dev_status, void* stream);
+
+/*
+ * One product per expert along its rows: D_e = A[:, e's rows] . B[:, e's rows]^T, zeros for an
+ * expert without pairs.
+ *   A : M x rows operand, B : N x rows operand (column-wise outputs of nvfp4_quantize_grouped).
+ *   D : device, (E * M) x N, row stride ldd, FP32 or bf16; D_e starts at row e * M.
+ * Shape rules: M a multiple of 128, N of 16.
+ */
+nvfp4_status nvfp4_gemm_grouped_k(const nvfp4_operand* A, const nvfp4_operand* B,
+                                  const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
+                                  int* dev_status, void* stream);
+
+/* Device workspace of each nvfp4_experts_* call (rows: the plan's). */
+size_t nvfp4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t rows, int64_t I,
+                                     int64_t O);
+
+/*
+ * The three training GEMMs of a layer of experts, as nvfp4_linear_*, with the weights quantized
+ * once by the caller: W is the (E * O) x I row-wise, Wt the I x (E * O) column-wise output of
+ * nvfp4_quantize(NVFP4_BLOCK2D) of the stacked weights.
+ *   fprop: Y[rows x O] = X . W_e^T; X 1x16 RTN, a row per token (gather != 0) or in expert order.
+ *   dgrad: dX[rows x I] = dY . W_e; dY [rows x O] 1x16 SR (stream `offset`).
+ *   wgrad: dW[(E * O) x I], dW_e = dY_e^T . X_e; dY RHT + SR (stream `offset` + 1), X RHT + RTN.
+ * Shape rules: I a multiple of 64, O of 128, E * O < 2^31.
+ */
+nvfp4_status nvfp4_experts_fprop(const void* X, int64_t ldx, int gather, const nvfp4_operand* W,
+                                 const nvfp4_expert_plan* plan, int64_t I, int64_t O, void* Y,
+                                 int y_dtype, int64_t ldy, void* workspace, int* dev_status,
+                                 void* stream);
+nvfp4_status nvfp4_experts_dgrad(const void* dY, int64_t lddy, const nvfp4_operand* Wt,
+                                 const nvfp4_expert_plan* plan, int64_t I, int64_t O, uint64_t seed,
+                                 uint64_t offset, void* dX, int dx_dtype, int64_t lddx,
+                                 void* workspace, int* dev_status, void* stream);
+nvfp4_status nvfp4_experts_wgrad(const void* dY, int64_t lddy, const void* X, int64_t ldx, int gather,
+                                 const nvfp4_expert_plan* plan, int64_t I, int64_t O,
+                                 uint16_t sign_mask, uint64_t seed, uint64_t offset, void* dW,
+                                 int dw_dtype, int64_t lddw, void* workspace, int* dev_status,
+                                 void* stream);
+
+/*
+ * The rows of a layer of experts back to tokens: out[t] = sum_j weights[t, j] Y[pair_row[t, j]],
+ * summed in FP32 in slot order (pairs without a row add nothing).  weights NULL: all 1, the
+ * gradient of the gather.
+ *   Y   : rows x cols bf16 in expert order, row stride ldy.
+ *   out : tokens x cols FP32 or bf16, row stride ldo.
+ * Shape rules: cols a multiple of 8; row strides multiples of 16 bytes.
+ */
+nvfp4_status nvfp4_combine(const void* Y_bf16, int64_t cols, int64_t ldy,
+                           const nvfp4_expert_plan* plan, const float* weights, void* out,
+                           int out_dtype, int64_t ldo, int* dev_status, void* stream);
+
+/*
+ * Gradients of nvfp4_combine: dY[pair_row[t, j]] = weights[t, j] dout[t] (zeros in the rows without a
+ * token; rows behind the last region are not written) and dweights[t, j] = sum_c dout[t, c]
+ * Y[pair_row[t, j], c] (0 for pairs without a row).  dout FP32 or bf16, Y and dY bf16.
+ */
+nvfp4_status nvfp4_combine_backward(const void* dout, int dout_dtype, int64_t ldo,
+                                    const void* Y_bf16, int64_t cols, int64_t ldy,
+                                    const nvfp4_expert_plan* plan, const float* weights,
+                                    void* dY_bf16, int64_t lddy, float* dweights, int* dev_status,
+                                    void* stream);
 
 #ifdef __cplusplus
 }

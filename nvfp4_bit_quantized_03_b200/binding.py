@@ -21,9 +21,10 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "nvfp4.h")
 
 # status codes and flags (include/nvfp4.h)
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DEVICE, ERR_CUDA, ERR_NONFINITE, ERR_TIMEOUT, ERR_ARG = range(9)
-DEVSTAT_NONFINITE, DEVSTAT_TIMEOUT, DEVSTAT_BOUNDS = 1, 2, 4
-ROWWISE, COLWISE, BLOCK2D, SR, AMAX_GIVEN, MX = 1, 2, 4, 8, 16, 32
+DEVSTAT_NONFINITE, DEVSTAT_TIMEOUT, DEVSTAT_BOUNDS, DEVSTAT_INDEX = 1, 2, 4, 8
+ROWWISE, COLWISE, BLOCK2D, SR, AMAX_GIVEN, MX, GATHER = 1, 2, 4, 8, 16, 32, 64
 OUT_F32, OUT_BF16 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 
 class NVFP4Error(RuntimeError):
@@ -35,6 +36,12 @@ class NVFP4Error(RuntimeError):
 class Operand(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("amax", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class PlanStruct(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("pair_row", ctypes.c_void_p),
+                ("row_token", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("experts", ctypes.c_int64), ("rows", ctypes.c_int64)]
 
 
 _libs = {}               # path -> configured CDLL
@@ -132,6 +139,27 @@ def _open(path):
     L.nvfp4_linear_dgrad_quantized.argtypes = [vp, vp, i64, i64, i64, u64, u64, vp, u16, u64,
                                                u64, op, op, vp, vp, vp]
     L.nvfp4_linear_dgrad_quantized.restype = i32
+    pl, u32, f32 = ctypes.POINTER(PlanStruct), ctypes.c_uint, ctypes.c_float
+    L.nvfp4_expert_rows.argtypes, L.nvfp4_expert_rows.restype = [i64, i64, i64], i64
+    L.nvfp4_expert_plan_workspace_bytes.argtypes = [i64, i64, i64]
+    L.nvfp4_expert_plan_workspace_bytes.restype = sz
+    L.nvfp4_experts_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
+    L.nvfp4_experts_workspace_bytes.restype = sz
+    for name, argtypes in {
+            "route": [vp, i32, i64, i64, i64, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp],
+            "route_backward": [vp, i32, i64, i64, i64, vp, vp, i32, i32, i32, f32, vp, i64, vp, vp],
+            "plan_experts": [vp, pl, vp, vp, vp],
+            "quantize_grouped": [vp, i64, i64, pl, u16, u32, u64, u64, op, op, vp, vp, vp],
+            "gemm_grouped": [op, op, pl, vp, i32, i64, vp, vp],
+            "gemm_grouped_k": [op, op, pl, vp, i32, i64, vp, vp],
+            "experts_fprop": [vp, i64, i32, op, pl, i64, i64, vp, i32, i64, vp, vp, vp],
+            "experts_dgrad": [vp, i64, op, pl, i64, i64, u64, u64, vp, i32, i64, vp, vp, vp],
+            "experts_wgrad": [vp, i64, vp, i64, i32, pl, i64, i64, u16, u64, u64, vp, i32, i64, vp,
+                              vp, vp],
+            "combine": [vp, i64, i64, pl, vp, vp, i32, i64, vp, vp],
+            "combine_backward": [vp, i32, i64, vp, i64, i64, pl, vp, vp, i64, vp, vp, vp]}.items():
+        f = getattr(L, "nvfp4_" + name)
+        f.argtypes, f.restype = argtypes, i32
     return L
 
 
@@ -201,6 +229,21 @@ class QuantizedTensor:
         self.scales = _poisoned(torch.empty((scales_bytes(rows, cols),), dtype=torch.uint8,
                                             device=device))
         self.amax = _poisoned(torch.zeros((1,), dtype=torch.float32, device=device))
+
+    @classmethod
+    def from_buffers(cls, codes, scales, amax):
+        """An operand of buffers that hold one already (codes [rows x cols/2])."""
+        if (codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous()
+                or scales.dtype != torch.uint8 or not scales.is_contiguous()
+                or amax.dtype != torch.float32 or amax.numel() != 1):
+            raise ValueError("an operand has contiguous uint8 codes [rows x cols/2], uint8 scales and "
+                             "one float32 amax")
+        q = cls.__new__(cls)
+        q.rows, q.cols = codes.shape[0], 2 * codes.shape[1]
+        if scales.numel() < scales_bytes(q.rows, q.cols):
+            raise ValueError(f"scales: {scales.numel()} bytes are too few for {q.rows} x {q.cols}")
+        q.codes, q.scales, q.amax = codes, scales, amax
+        return q
 
     def operand(self):
         return Operand(self.codes.data_ptr(), self.scales.data_ptr(), self.amax.data_ptr(),
@@ -409,3 +452,301 @@ def linear_wgrad(dY, X, sign_mask, seed, offset, out=None, out_dtype=torch.float
                                   _stream(stream))
     _check(st, "nvfp4_linear_wgrad")
     return out
+
+
+# ---- mixture-of-experts layers -----------------------------------------------------------
+
+def expert_rows(tokens, k, experts):
+    """Rows of an expert-ordered matrix that hold every routing (0: sizes outside the limits)."""
+    return lib().nvfp4_expert_rows(tokens, k, experts)
+
+
+def experts_workspace_bytes(plan, I, O):
+    return lib().nvfp4_experts_workspace_bytes(plan.tokens, plan.k, plan.experts, plan.rows, I, O)
+
+
+def _on_current_device(what, *tensors):
+    """The calls run on the current device: its stream, its kernels.  Refuses tensors elsewhere."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != here):
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {t.device}")
+
+
+def _matrix(what, t, dtypes, rows, cols):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (
+            cols is not None and t.shape[1] != cols) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [{'rows' if rows is None else rows} x "
+                         f"{'cols' if cols is None else cols}] with unit column stride, got "
+                         f"{tuple(t.shape)} strides {t.stride()}")
+
+
+def _dense(what, t, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _row_stride(t):
+    # a one-row view may carry any stride; it is never used
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+_F32_BF16 = (torch.float32, torch.bfloat16)
+_BF16 = (torch.bfloat16,)
+
+
+def _allocating(stream):
+    """Buffers made for a call belong to the stream that uses them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+class ExpertPlan:
+    """The expert-ordered rows of a routing: offsets [experts + 1], pair_row [tokens, k] and
+    row_token [rows], int32 (nvfp4_expert_plan)."""
+
+    def __init__(self, offsets, pair_row, row_token):
+        for name, t, dim in (("offsets", offsets, 1), ("pair_row", pair_row, 2),
+                             ("row_token", row_token, 1)):
+            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+                raise ValueError(f"plan: {name} must be a contiguous int32 tensor of {dim} dimensions")
+        self.offsets, self.pair_row, self.row_token = offsets, pair_row, row_token
+        self.tokens, self.k = pair_row.shape
+        self.experts, self.rows = offsets.shape[0] - 1, row_token.shape[0]
+
+    @classmethod
+    def empty(cls, tokens, k, experts, rows=None, device="cuda"):
+        if rows is None:
+            rows = expert_rows(tokens, k, experts)
+        if rows == 0:
+            raise NVFP4Error(ERR_SHAPE, f"expert plan of {tokens} tokens, {k} of {experts} experts")
+
+        def ints(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=device)
+        return cls(ints(experts + 1), ints(tokens, k), ints(rows))
+
+    def struct(self):
+        return PlanStruct(self.offsets.data_ptr(), self.pair_row.data_ptr(),
+                          self.row_token.data_ptr(), self.tokens, self.k, self.experts, self.rows)
+
+
+def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=True, scale=1.0,
+          experts=None, weights=None, dev_status=None, stream=None):
+    """nvfp4_route: the k experts of every token (int32 [T, k]) and their weights (float32)."""
+    _matrix("logits", logits, _F32_BF16, None, None)
+    T, E = logits.shape
+    if bias is not None:
+        _dense("bias", bias, torch.float32, (E,))
+    with _allocating(stream):
+        if experts is None:
+            experts = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+        if weights is None:
+            weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    _dense("experts", experts, torch.int32, (T, k))
+    _dense("weights", weights, torch.float32, (T, k))
+    _on_current_device("nvfp4_route", logits, bias, experts, weights)
+    _check(lib().nvfp4_route(_ptr(logits), _dtype_code(logits.dtype), T, E, _row_stride(logits),
+                             _ptr(bias), int(bool(sigmoid)), groups, top_groups, k, int(bool(renorm)),
+                             scale, _ptr(experts), _ptr(weights), _ptr(dev_status),
+                             _stream(stream)), "nvfp4_route")
+    return experts, weights
+
+
+def route_backward(logits, experts, dweights, sigmoid=False, renorm=True, scale=1.0, dlogits=None,
+                   dev_status=None, stream=None):
+    """nvfp4_route_backward: gradient of route's weights with respect to the logits."""
+    _matrix("logits", logits, _F32_BF16, None, None)
+    T, E = logits.shape
+    k = experts.shape[-1]
+    _dense("experts", experts, torch.int32, (T, k))
+    _dense("dweights", dweights, torch.float32, (T, k))
+    if dlogits is None:
+        with _allocating(stream):
+            dlogits = _poisoned(torch.empty((T, E), dtype=logits.dtype, device=logits.device))
+    _matrix("dlogits", dlogits, (logits.dtype,), T, E)
+    _on_current_device("nvfp4_route_backward", logits, experts, dweights, dlogits)
+    _check(lib().nvfp4_route_backward(_ptr(logits), _dtype_code(logits.dtype), T, E,
+                                      _row_stride(logits), _ptr(experts), _ptr(dweights),
+                                      int(bool(sigmoid)), k, int(bool(renorm)), scale,
+                                      _ptr(dlogits), _row_stride(dlogits), _ptr(dev_status),
+                                      _stream(stream)), "nvfp4_route_backward")
+    return dlogits
+
+
+def expert_plan(experts, n_experts, plan=None, workspace=None, dev_status=None, stream=None):
+    """nvfp4_plan_experts: the ExpertPlan of a routing experts [T, k] (int32)."""
+    T, k = experts.shape
+    _dense("experts", experts, torch.int32, (T, k))
+    with _allocating(stream):
+        if plan is None:
+            plan = ExpertPlan.empty(T, k, n_experts, device=experts.device)
+        if workspace is None:
+            workspace = _workspace(lib().nvfp4_expert_plan_workspace_bytes(T, k, n_experts),
+                                   experts.device)
+    if (plan.tokens, plan.k, plan.experts) != (T, k, n_experts):
+        raise ValueError(f"plan is for {plan.tokens} tokens, {plan.k} of {plan.experts} experts")
+    _on_current_device("nvfp4_plan_experts", experts, plan.offsets, plan.pair_row, plan.row_token)
+    _check(lib().nvfp4_plan_experts(_ptr(experts), ctypes.byref(plan.struct()), _ptr(workspace),
+                                    _ptr(dev_status), _stream(stream)), "nvfp4_plan_experts")
+    return plan
+
+
+def _source_rows(plan, gather):
+    return plan.tokens if gather else plan.rows
+
+
+def quantize_grouped(x, plan, flags, sign_mask=0, seed=0, offset=0, out_row=None, out_col=None,
+                     workspace=None, dev_status=None, stream=None):
+    """nvfp4_quantize_grouped: an expert-ordered matrix row-wise (out_row) and / or RHT'd
+    column-wise (out_col); with GATHER x has a row per token."""
+    _matrix("x", x, _BF16, _source_rows(plan, flags & GATHER), None)
+    cols = x.shape[1]
+    with _allocating(stream):
+        if flags & ROWWISE and out_row is None:
+            out_row = QuantizedTensor(plan.rows, cols, x.device)
+        if flags & COLWISE and out_col is None:
+            out_col = QuantizedTensor(cols, plan.rows, x.device)
+        if workspace is None:
+            workspace = _workspace(workspace_bytes(plan.rows, cols, flags), x.device)
+    _on_current_device("nvfp4_quantize_grouped", x, plan.offsets)
+    op_r = out_row.operand() if out_row is not None else None
+    op_c = out_col.operand() if out_col is not None else None
+    _check(lib().nvfp4_quantize_grouped(
+        _ptr(x), cols, _row_stride(x), ctypes.byref(plan.struct()), sign_mask, flags, seed, offset,
+        ctypes.byref(op_r) if op_r is not None else None,
+        ctypes.byref(op_c) if op_c is not None else None, _ptr(workspace), _ptr(dev_status),
+        _stream(stream)), "nvfp4_quantize_grouped")
+    return out_row, out_col
+
+
+def _grouped_out(what, out, rows, cols, out_dtype, device, stream):
+    if out is None:
+        with _allocating(stream):
+            out = _poisoned(torch.empty((rows, cols), dtype=out_dtype, device=device))
+    _matrix(what, out, _F32_BF16, rows, cols)
+    return out
+
+
+def gemm_grouped(A, W, plan, out=None, out_dtype=torch.bfloat16, dev_status=None, stream=None):
+    """nvfp4_gemm_grouped: every expert's rows of A times its matrix of W, stacked by rows
+    ((E * N) x K) or side by side (N x (E * K))."""
+    E = plan.experts
+    N = W.rows // E if W.cols == A.cols and W.rows % E == 0 else W.rows
+    out = _grouped_out("out", out, plan.rows, N, out_dtype, A.codes.device, stream)
+    _on_current_device("nvfp4_gemm_grouped", A.codes, W.codes, plan.offsets, out)
+    oa, ob = A.operand(), W.operand()
+    _check(lib().nvfp4_gemm_grouped(ctypes.byref(oa), ctypes.byref(ob), ctypes.byref(plan.struct()),
+                                    _ptr(out), _dtype_code(out.dtype), _row_stride(out),
+                                    _ptr(dev_status), _stream(stream)), "nvfp4_gemm_grouped")
+    return out
+
+
+def gemm_grouped_k(A, B, plan, out=None, out_dtype=torch.float32, dev_status=None, stream=None):
+    """nvfp4_gemm_grouped_k: D_e = A . B^T over expert e's rows, [(E * A.rows) x B.rows]."""
+    out = _grouped_out("out", out, plan.experts * A.rows, B.rows, out_dtype, A.codes.device, stream)
+    _on_current_device("nvfp4_gemm_grouped_k", A.codes, B.codes, plan.offsets, out)
+    oa, ob = A.operand(), B.operand()
+    _check(lib().nvfp4_gemm_grouped_k(ctypes.byref(oa), ctypes.byref(ob),
+                                      ctypes.byref(plan.struct()), _ptr(out), _dtype_code(out.dtype),
+                                      _row_stride(out), _ptr(dev_status), _stream(stream)),
+           "nvfp4_gemm_grouped_k")
+    return out
+
+
+def _experts_workspace(workspace, plan, I, O, device, stream):
+    if workspace is None:
+        with _allocating(stream):
+            workspace = _workspace(experts_workspace_bytes(plan, I, O), device)
+    elif workspace.numel() * workspace.element_size() < experts_workspace_bytes(plan, I, O):
+        raise ValueError("workspace is smaller than experts_workspace_bytes")
+    return workspace
+
+
+def experts_fprop(X, W, plan, gather=True, out=None, out_dtype=torch.bfloat16, workspace=None,
+                  dev_status=None, stream=None):
+    """nvfp4_experts_fprop: Y [rows x O] of X (a row per token, or with gather=False in expert
+    order) and the stacked, row-wise quantized weights W [(E * O) x I]."""
+    _matrix("X", X, _BF16, _source_rows(plan, gather), W.cols)
+    I, O = W.cols, W.rows // plan.experts
+    out = _grouped_out("out", out, plan.rows, O, out_dtype, X.device, stream)
+    workspace = _experts_workspace(workspace, plan, I, O, X.device, stream)
+    _on_current_device("nvfp4_experts_fprop", X, W.codes, plan.offsets, out, workspace)
+    op = W.operand()
+    _check(lib().nvfp4_experts_fprop(_ptr(X), _row_stride(X), int(bool(gather)), ctypes.byref(op),
+                                     ctypes.byref(plan.struct()), I, O, _ptr(out),
+                                     _dtype_code(out.dtype), _row_stride(out), _ptr(workspace),
+                                     _ptr(dev_status), _stream(stream)), "nvfp4_experts_fprop")
+    return out
+
+
+def experts_dgrad(dY, Wt, plan, seed, offset, out=None, out_dtype=torch.bfloat16, workspace=None,
+                  dev_status=None, stream=None):
+    """nvfp4_experts_dgrad: dX [rows x I] of dY [rows x O] and the column-wise quantized weights
+    Wt [I x (E * O)]."""
+    I, O = Wt.rows, Wt.cols // plan.experts
+    _matrix("dY", dY, _BF16, plan.rows, O)
+    out = _grouped_out("out", out, plan.rows, I, out_dtype, dY.device, stream)
+    workspace = _experts_workspace(workspace, plan, I, O, dY.device, stream)
+    _on_current_device("nvfp4_experts_dgrad", dY, Wt.codes, plan.offsets, out, workspace)
+    op = Wt.operand()
+    _check(lib().nvfp4_experts_dgrad(_ptr(dY), _row_stride(dY), ctypes.byref(op),
+                                     ctypes.byref(plan.struct()), I, O, seed, offset, _ptr(out),
+                                     _dtype_code(out.dtype), _row_stride(out), _ptr(workspace),
+                                     _ptr(dev_status), _stream(stream)), "nvfp4_experts_dgrad")
+    return out
+
+
+def experts_wgrad(dY, X, plan, sign_mask, seed, offset, gather=True, out=None,
+                  out_dtype=torch.float32, workspace=None, dev_status=None, stream=None):
+    """nvfp4_experts_wgrad: dW [(E * O) x I] of dY [rows x O] and X (a row per token, or with
+    gather=False in expert order)."""
+    _matrix("X", X, _BF16, _source_rows(plan, gather), None)
+    _matrix("dY", dY, _BF16, plan.rows, None)
+    I, O = X.shape[1], dY.shape[1]
+    out = _grouped_out("out", out, plan.experts * O, I, out_dtype, dY.device, stream)
+    workspace = _experts_workspace(workspace, plan, I, O, dY.device, stream)
+    _on_current_device("nvfp4_experts_wgrad", dY, X, plan.offsets, out, workspace)
+    _check(lib().nvfp4_experts_wgrad(_ptr(dY), _row_stride(dY), _ptr(X), _row_stride(X),
+                                     int(bool(gather)), ctypes.byref(plan.struct()), I, O, sign_mask,
+                                     seed, offset, _ptr(out), _dtype_code(out.dtype),
+                                     _row_stride(out), _ptr(workspace), _ptr(dev_status),
+                                     _stream(stream)), "nvfp4_experts_wgrad")
+    return out
+
+
+def combine(Y, plan, weights=None, out=None, out_dtype=torch.bfloat16, dev_status=None, stream=None):
+    """nvfp4_combine: out[t] = sum_j weights[t, j] Y[row of pair (t, j)] (weights None: all 1)."""
+    _matrix("Y", Y, _BF16, plan.rows, None)
+    if weights is not None:
+        _dense("weights", weights, torch.float32, (plan.tokens, plan.k))
+    out = _grouped_out("out", out, plan.tokens, Y.shape[1], out_dtype, Y.device, stream)
+    _on_current_device("nvfp4_combine", Y, plan.pair_row, weights, out)
+    _check(lib().nvfp4_combine(_ptr(Y), Y.shape[1], _row_stride(Y), ctypes.byref(plan.struct()),
+                               _ptr(weights), _ptr(out), _dtype_code(out.dtype), _row_stride(out),
+                               _ptr(dev_status), _stream(stream)), "nvfp4_combine")
+    return out
+
+
+def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=None, stream=None):
+    """nvfp4_combine_backward: (dY [rows x cols] bf16, dweights [T, k] float32)."""
+    _matrix("dout", dout, _F32_BF16, plan.tokens, None)
+    cols = dout.shape[1]
+    _matrix("Y", Y, _BF16, plan.rows, cols)
+    _dense("weights", weights, torch.float32, (plan.tokens, plan.k))
+    with _allocating(stream):
+        if dy is None:
+            dy = _poisoned(torch.empty((plan.rows, cols), dtype=torch.bfloat16, device=Y.device))
+        if dweights is None:
+            dweights = _poisoned(torch.empty((plan.tokens, plan.k), dtype=torch.float32,
+                                             device=Y.device))
+    _matrix("dy", dy, _BF16, plan.rows, cols)
+    _dense("dweights", dweights, torch.float32, (plan.tokens, plan.k))
+    _on_current_device("nvfp4_combine_backward", dout, Y, plan.pair_row, weights, dy, dweights)
+    _check(lib().nvfp4_combine_backward(_ptr(dout), _dtype_code(dout.dtype), _row_stride(dout),
+                                        _ptr(Y), cols, _row_stride(Y), ctypes.byref(plan.struct()),
+                                        _ptr(weights), _ptr(dy), _row_stride(dy), _ptr(dweights),
+                                        _ptr(dev_status), _stream(stream)), "nvfp4_combine_backward")
+    return dy, dweights

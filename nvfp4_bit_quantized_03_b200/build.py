@@ -25,6 +25,10 @@ UNITS = {
     "api.cu": [],
     "quantize.cu": ["-fmad=false"],
     "gemm.cu": [],
+    "gemm_grouped.cu": [],
+    "route.cu": [],
+    "combine.cu": [],
+    "experts.cu": [],
     "noalloc.cu": [],
 }
 # library path, object folder and extra defines of each variant

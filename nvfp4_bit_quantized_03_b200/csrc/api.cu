@@ -7,8 +7,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "nvfp4.h"
-#include "nvfp4_internal.h"
+#include "api_common.h"
 
 using namespace nvfp4;
 
@@ -23,8 +22,9 @@ struct DeviceInfo {
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_device_mutex;
 
-// The current device if it is a compute-capability 10.0 GPU.
-nvfp4_status current_device(int* sm_count)
+}  // namespace
+
+nvfp4_status nvfp4::current_device(int* sm_count)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
@@ -45,23 +45,7 @@ nvfp4_status current_device(int* sm_count)
     return NVFP4_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-size_t round256(size_t v) { return (v + 255u) & ~static_cast<size_t>(255u); }
-
-constexpr int64_t kMaxDim = int64_t(1) << 31;
-
-nvfp4_status check_operand(const nvfp4_operand* op, int64_t rows, int64_t cols)
-{
-    if (!op || !op->codes || !op->scales || !op->amax) return NVFP4_ERR_NULL;
-    if (op->rows != rows || op->cols != cols) return NVFP4_ERR_SHAPE;
-    if (!aligned16(op->codes) || !aligned16(op->scales) || !aligned4(op->amax))
-        return NVFP4_ERR_ALIGN;
-    return NVFP4_OK;
-}
-
-nvfp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
+namespace {
 
 // Workspace layout of one linear-layer call: the quantized A and B operands, then the
 // partial maxima of the amax pass.
@@ -69,11 +53,6 @@ struct LinearWorkspace {
     nvfp4_operand a, b;
     void* partials;
 };
-
-size_t operand_bytes(int64_t rows, int64_t cols)
-{
-    return round256(nvfp4_codes_bytes(rows, cols)) + round256(nvfp4_scales_bytes(rows, cols)) + 256;
-}
 
 LinearWorkspace carve(void* ws, int64_t ar, int64_t ac, int64_t br, int64_t bc)
 {

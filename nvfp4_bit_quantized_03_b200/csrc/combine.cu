@@ -1,0 +1,152 @@
+// The rows of a mixture layer's experts back to tokens, and the gradient of that.
+//   combine          : out[t] = sum_j w[t, j] y[pair_row[t, j]] (FP32 sum in slot order; w = 1 without
+//                      weights, which is the backward pass of the gather into expert order)
+//   combine_backward : dy[pair_row[t, j]] = w[t, j] dout[t]; dw[t, j] = sum_c dout[t, c] y[row, c]
+// Pairs without a row add nothing and have zero gradient; a token without pairs gives zeros.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "bounds_check.cuh"
+#include "nvfp4_device.cuh"
+#include "nvfp4_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kMaxK = 32;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint4 pack8(const float* f)
+{
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                      pack_bf16(f[6], f[7]));
+}
+
+// A CTA per token and slice of its columns; a thread takes 8 columns at a time.
+template <bool F32>
+__global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a)
+{
+    __shared__ int64_t row[kMaxK];
+    __shared__ float weight[kMaxK];
+    const int64_t t = blockIdx.x;
+    if (threadIdx.x < a.map.k) {
+        const int64_t p = t * a.map.k + threadIdx.x;
+        row[threadIdx.x] = a.map.pair_target(t, threadIdx.x, a.rows);
+        weight[threadIdx.x] = a.weights ? a.weights[p] : 1.0f;
+    }
+    __syncthreads();
+    const int64_t yb = bf16_matrix_bytes(a.rows, a.cols, a.ldy);
+    const int64_t vecs = a.cols >> 3;
+    for (int64_t v = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; v < vecs;
+         v += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+        float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int j = 0; j < a.map.k; ++j) {
+            if (row[j] < 0) continue;
+            float f[8];
+            unpack8(ldg_checked(reinterpret_cast<const uint4*>(a.y + row[j] * a.ldy) + v, a.y, yb,
+                                a.dev_status), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += weight[j] * f[i];
+        }
+        if (F32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + t * a.ldo) + 2 * v;
+            o[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            o[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+        } else {
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.ldo)[v] = pack8(sum);
+        }
+    }
+}
+
+// A CTA per token: its gradient row is read for every pair (from cache after the first), the pair's
+// row of y once; each pair's dot product is a block reduction in a fixed order.  The CTAs behind the
+// tokens zero the rows without a token.
+template <bool F32>
+__global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs a)
+{
+    __shared__ float part[kMaxK][4];
+    const int64_t vecs = a.cols >> 3;
+    const int64_t yb = bf16_matrix_bytes(a.rows, a.cols, a.ldy);
+    const int64_t db = bf16_matrix_bytes(a.rows, a.cols, a.lddy);
+    if (blockIdx.x >= a.map.tokens) {
+        const int64_t used = a.map.used_rows(a.rows);
+        for (int64_t r = blockIdx.x - a.map.tokens; r < used; r += gridDim.x - a.map.tokens) {
+            const int64_t token = a.map.row_token[r];
+            if (token >= 0 && token < a.map.tokens) continue;
+            uint4* d = reinterpret_cast<uint4*>(a.dy + r * a.lddy);
+            for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x)
+                st_checked(d + v, make_uint4(0, 0, 0, 0), a.dy, db, a.dev_status);
+        }
+        return;
+    }
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int j = 0; j < a.map.k; ++j) {
+        const int64_t r = a.map.pair_target(t, j, a.rows);
+        float dot = 0.0f;
+        if (r >= 0) {
+            const float w = a.weights[t * a.map.k + j];
+            const uint4* y = reinterpret_cast<const uint4*>(a.y + r * a.ldy);
+            uint4* dy = reinterpret_cast<uint4*>(a.dy + r * a.lddy);
+            for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
+                float g[8], f[8], d[8];
+                if (F32) {
+                    const float4* p = reinterpret_cast<const float4*>(
+                        static_cast<const float*>(a.dout) + t * a.ldo) + 2 * v;
+                    const float4 lo = __ldg(p), hi = __ldg(p + 1);
+                    g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w;
+                    g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
+                } else {
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const uint16_t*>(a.dout) + t * a.ldo) + v), g);
+                }
+                unpack8(ldg_checked(y + v, a.y, yb, a.dev_status), f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot += g[i] * f[i];
+                    d[i] = w * g[i];
+                }
+                st_checked(dy + v, pack8(d), a.dy, db, a.dev_status);
+            }
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
+        if (lane == 0) part[j][warp] = dot;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.map.k)
+        a.dweights[t * a.map.k + threadIdx.x] =
+            (part[threadIdx.x][0] + part[threadIdx.x][1]) + (part[threadIdx.x][2] + part[threadIdx.x][3]);
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs& a, bool f32, int sm_count, cudaStream_t s)
+{
+    // one slice of 1024 columns per CTA when there are too few tokens to fill the SMs
+    const int64_t slices = (a.cols / 8 + 127) / 128;
+    int64_t y = (4 * sm_count + a.map.tokens - 1) / a.map.tokens;
+    if (y > slices) y = slices;
+    if (y < 1) y = 1;
+    const dim3 grid(static_cast<unsigned>(a.map.tokens), static_cast<unsigned>(y));
+    if (f32) combine_kernel<true><<<grid, 128, 0, s>>>(a);
+    else     combine_kernel<false><<<grid, 128, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_backward(const CombineArgs& a, bool f32, int sm_count, cudaStream_t s)
+{
+    const int64_t grid = a.map.tokens + (a.rows < sm_count ? a.rows : sm_count);
+    if (f32) combine_backward_kernel<true><<<static_cast<unsigned>(grid), 128, 0, s>>>(a);
+    else     combine_backward_kernel<false><<<static_cast<unsigned>(grid), 128, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace nvfp4

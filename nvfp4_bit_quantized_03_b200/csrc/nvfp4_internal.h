@@ -37,6 +37,38 @@ struct QuantSource {
     const float* amax_given;  // non-null: use *amax_given, ignore the partials
 };
 
+// Which row of x a row of an expert-ordered matrix holds.  Maps come from device memory that the
+// caller wrote, so every index is checked against its range before it is used.
+struct RowMap {
+    const int32_t* row_token;  // [rows] token of each row, negative: a row of zeros
+    const int32_t* pair_row;   // [tokens * k] row of each pair, negative: none
+    const int32_t* used;       // rows in use (the last of the region offsets)
+    int64_t tokens, k;
+    int64_t x_rows;            // rows of x: tokens when gathering, else the matrix's rows
+    bool gather;               // x has a row per token; otherwise it is in expert order itself
+
+#ifdef __CUDACC__
+    __device__ __forceinline__ int64_t used_rows(int64_t rows) const
+    {
+        const int64_t n = *used;
+        return n < 0 ? 0 : (n < rows ? n : rows) & ~static_cast<int64_t>(127);
+    }
+    // row of x behind row r, or -1
+    __device__ __forceinline__ int64_t source(int64_t r) const
+    {
+        const int64_t t = row_token[r];
+        if (t < 0 || t >= tokens) return -1;
+        return gather ? t : r;
+    }
+    // row of the pair (t, j), or -1
+    __device__ __forceinline__ int64_t pair_target(int64_t t, int64_t j, int64_t rows) const
+    {
+        const int64_t r = pair_row[t * k + j];
+        return r < rows ? r : -1;
+    }
+#endif
+};
+
 struct TileArgs {
     const uint16_t* x;
     int64_t rows, cols, ld;
@@ -53,6 +85,7 @@ struct TileArgs {
     uint64_t offset;
     uint64_t offset_col;  // dual mode: SR stream of the column output
     int* dev_status;
+    RowMap map;           // grouped passes only
 };
 
 int amax_grid(int64_t rows, int64_t cols, bool rht, int sm_count);
@@ -71,6 +104,15 @@ cudaError_t launch_quant_rowwise(const uint16_t* x, int64_t rows, int64_t cols, 
                                  uint64_t offset, int* dev_status, int sm_count, cudaStream_t s);
 cudaError_t launch_quant_tile(const TileArgs& a, bool row, bool col, bool block2d, bool rht,
                               bool sr, bool mx, int sm_count, cudaStream_t s);
+// The same passes over an expert-ordered matrix.  amax: plain (`partials`), RHT (`partials`), or
+// both (`partials_plain` not null).
+int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, int sm_count);
+cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, bool rht,
+                                uint32_t sign_mask, uint32_t* partials, uint32_t* partials_plain,
+                                int grid, const RowMap& map, int* dev_status, cudaStream_t s);
+cudaError_t launch_quant_grouped_rows(const TileArgs& a, bool sr, int sm_count, cudaStream_t s);
+cudaError_t launch_quant_grouped_tile(const TileArgs& a, bool row, bool sr, int sm_count,
+                                      cudaStream_t s);
 // Debug build only: one checked store just past a buffer's declared end (refused, recorded as
 // NVFP4_DEVSTAT_BOUNDS); cudaErrorNotSupported in the normal build.
 cudaError_t launch_bounds_selftest(int* dev_status, cudaStream_t s);
@@ -93,6 +135,67 @@ struct GemmArgs {
 };
 
 cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s);
+
+// Experts of a mixture layer: the grouped products keep 4 bytes of schedule per expert in the
+// shared memory that their pipeline leaves.
+constexpr int kMaxExperts = 512;
+
+// Products over the experts (gemm_grouped.cu).  By rows: A is rows x K in expert order, B holds
+// expert e's N x K matrix from row e * b_row_step and column e * b_k_step of a b_rows x b_cols
+// operand, D is rows x N.  By K: A is M x rows and B is N x rows (b_rows = N, b_cols = rows), D is
+// (experts * M) x N.
+struct GroupedGemmArgs {
+    bool by_k;
+    const uint8_t* a_codes;
+    const uint8_t* a_scales;
+    const float* a_amax;
+    const uint8_t* b_codes;
+    const uint8_t* b_scales;
+    const float* b_amax;
+    int64_t b_rows, b_cols, b_row_step, b_k_step;
+    const int32_t* offsets;
+    int64_t experts, rows;
+    int64_t M, N, K;
+    void* D;
+    int64_t ldd;
+    int out_bf16;
+    int* dev_status;
+};
+
+// Routing (route.cu).  The plan's first pass counts each kPlanPairs pairs apart; it needs no
+// workspace when there are no more.
+constexpr int kPlanPairs = 2048;
+cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int64_t E, int64_t ld,
+                         const float* bias, bool sigmoid, bool renorm, int groups, int top_groups,
+                         int k, float scale, int32_t* experts, float* weights, int* dev_status,
+                         cudaStream_t s);
+cudaError_t launch_route_backward(const void* logits, bool bf16, int64_t T, int64_t E, int64_t ld,
+                                  const int32_t* experts, const float* dweights, bool sigmoid,
+                                  bool renorm, int k, float scale, void* dlogits, int64_t ldd,
+                                  int* dev_status, cudaStream_t s);
+cudaError_t launch_plan(const int32_t* experts, int64_t pairs, int k, int E, int64_t rows,
+                        int32_t* offsets, int32_t* pair_row, int32_t* row_token, int32_t* counts,
+                        int* dev_status, cudaStream_t s);
+
+// Expert rows to tokens and back (combine.cu).
+struct CombineArgs {
+    RowMap map;
+    int64_t rows, cols;
+    const uint16_t* y;
+    int64_t ldy;
+    const float* weights;
+    void* out;            // combine: tokens x cols
+    const void* dout;     // backward: tokens x cols
+    int64_t ldo;          // row stride of out or dout
+    uint16_t* dy;
+    int64_t lddy;
+    float* dweights;
+    int* dev_status;
+};
+cudaError_t launch_combine(const CombineArgs& a, bool f32, int sm_count, cudaStream_t s);
+cudaError_t launch_combine_backward(const CombineArgs& a, bool f32, int sm_count, cudaStream_t s);
+
+cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, int sm_count, cudaStream_t s);
 // A kernel whose only thread waits, with the GEMM's bounded-wait routine, on an mbarrier that
 // nothing completes; it records NVFP4_DEVSTAT_TIMEOUT after limit_ns and returns.
 cudaError_t launch_wait_selftest(int* dev_status, unsigned long long limit_ns, cudaStream_t s);

@@ -68,13 +68,14 @@ __global__ void __launch_bounds__(256) amax_kernel(const uint16_t* __restrict__ 
 // amax of the random Hadamard transform along the rows: each work item is 16 rows x 4 columns
 // (16 coalesced 8-byte loads), i.e. four 16-element transforms.  With PLAIN the same loads also
 // give the amax of x itself (the row-wise output of the dual mode).
-template <bool PLAIN>
+// With GROUPED the rows are those of an expert-ordered matrix (RowMap).
+template <bool PLAIN, bool GROUPED = false>
 __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restrict__ x,
                                                        int64_t rows, int64_t cols, int64_t ld,
                                                        uint32_t sign_mask,
                                                        uint32_t* __restrict__ partials,
                                                        uint32_t* __restrict__ partials_plain,
-                                                       int* dev_status)
+                                                       int* dev_status, const RowMap map = {})
 {
     // The transform's sign flips are applied to the packed bf16 pairs (one xor per two
     // values), and its final x1/4 is applied once to the maximum: rounding is monotone, so the
@@ -83,9 +84,10 @@ __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restric
 #pragma unroll
     for (int k = 0; k < 16; ++k) flip[k] = ((sign_mask >> k) & 1u) ? 0x80008000u : 0u;
     uint32_t mp = 0;
-    const int64_t xb = bf16_matrix_bytes(rows, cols, ld);  // extent of x (bounds checks)
+    // extent of x (bounds checks)
+    const int64_t xb = bf16_matrix_bytes(GROUPED ? map.x_rows : rows, cols, ld);
     const int64_t cpr = cols >> 2;  // 8-byte column groups per row
-    const int64_t total = (rows >> 4) * cpr;
+    const int64_t total = ((GROUPED ? map.used_rows(rows) : rows) >> 4) * cpr;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     uint32_t m = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
@@ -94,8 +96,17 @@ __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restric
         const uint16_t* base = x + (g << 4) * ld + (c << 2);
         uint2 v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            v[k] = ldg_checked(reinterpret_cast<const uint2*>(base + k * ld), x, xb, dev_status);
+        for (int k = 0; k < 16; ++k) {
+            if (GROUPED) {
+                const int64_t src = map.source((g << 4) + k);
+                v[k] = make_uint2(0u, 0u);
+                if (src >= 0)
+                    v[k] = ldg_checked(reinterpret_cast<const uint2*>(x + src * ld + (c << 2)), x, xb,
+                                       dev_status);
+            } else {
+                v[k] = ldg_checked(reinterpret_cast<const uint2*>(base + k * ld), x, xb, dev_status);
+            }
+        }
         if (PLAIN) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -340,6 +351,8 @@ __device__ __forceinline__ void encode16(const float* y, const BlockScale& bs, c
 
 // Queue the copies of one tile's rows into `buf` (cp.async, 16 bytes each, zero-filled for
 // rows or column chunks outside the matrix) as one commit group.
+// With GROUPED the rows come through the row map (rows without a token are zeros).
+template <bool GROUPED>
 __device__ __forceinline__ void tile_load_async(const TileArgs& a, uint16_t* buf, int64_t r0,
                                                 int64_t c0, int nr, int nc)
 {
@@ -349,10 +362,16 @@ __device__ __forceinline__ void tile_load_async(const TileArgs& a, uint16_t* buf
     for (int k = 0; k < 8; ++k) {
         const int ch = t + 128 * k, row = ch >> 4, cc = ch & 15;
         bool in = row < nr && cc * 8 < nc;
-        const uint16_t* src = in ? a.x + (r0 + row) * a.ld + c0 + cc * 8 : a.x;
+        int64_t src_row = r0 + row;
+        if (GROUPED) {
+            if (in) src_row = a.map.source(src_row);
+            in = in && src_row >= 0;
+        }
+        const uint16_t* src = in ? a.x + src_row * a.ld + c0 + cc * 8 : a.x;
         if (kBoundsCheck && in &&
             !in_buffer(reinterpret_cast<const uint4*>(src), a.x,
-                       bf16_matrix_bytes(a.rows, a.cols, a.ld), a.dev_status)) {
+                       bf16_matrix_bytes(GROUPED ? a.map.x_rows : a.rows, a.cols, a.ld),
+                       a.dev_status)) {
             in = false;  // zero-filled instead
             src = a.x;
         }
@@ -426,7 +445,7 @@ constexpr int tile_min_ctas()
     return tile_buffers<COL, BLOCK2D, RHT, SR, MX>() == 1 ? 8 : tile_ctas_per_sm<SR>();
 }
 
-template <bool ROW, bool COL, bool BLOCK2D, bool RHT, bool SR, bool MX>
+template <bool ROW, bool COL, bool BLOCK2D, bool RHT, bool SR, bool MX, bool GROUPED = false>
 __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR, MX>()))
     quant_tile_kernel(TileArgs a)
 {
@@ -461,7 +480,8 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
     const Philox philox{a.keys};
     const int t = threadIdx.x;
     const int64_t tiles_c = (a.cols + kTileCols - 1) / kTileCols;
-    const int64_t tiles_r = (a.rows + kTileRows - 1) / kTileRows;
+    // (GROUPED: the rows in use, a multiple of 128; the tiles behind them are left as they were)
+    const int64_t tiles_r = ((GROUPED ? a.map.used_rows(a.rows) : a.rows) + kTileRows - 1) / kTileRows;
     const int64_t ntiles = tiles_c * tiles_r;
     // tiles are visited in reverse order (the amax pass left the tensor's tail in L2)
     auto coords = [&](int64_t id, int64_t& r0, int64_t& c0, int& nr, int& nc) {
@@ -476,7 +496,7 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
         int nr, nc;
         if (kBuffers == 2 && blockIdx.x < ntiles) {
             coords(blockIdx.x, r0, c0, nr, nc);
-            tile_load_async(a, tiles, r0, c0, nr, nc);
+            tile_load_async<GROUPED>(a, tiles, r0, c0, nr, nc);
         }
     }
     __syncthreads();  // the factor tables
@@ -488,14 +508,14 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
         coords(id, r0, c0, nr, nc);
         const uint16_t* tile = tiles + (kBuffers == 2 ? (k & 1) * kTileElems : 0);
         if (kBuffers == 1) {
-            tile_load_async(a, tiles, r0, c0, nr, nc);
+            tile_load_async<GROUPED>(a, tiles, r0, c0, nr, nc);
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         } else {
             if (id + gridDim.x < ntiles) {
                 int64_t r1, c1;
                 int nr1, nc1;
                 coords(id + gridDim.x, r1, c1, nr1, nc1);
-                tile_load_async(a, tiles + ((k + 1) & 1) * kTileElems, r1, c1, nr1, nc1);
+                tile_load_async<GROUPED>(a, tiles + ((k + 1) & 1) * kTileElems, r1, c1, nr1, nc1);
             } else {
                 asm volatile("cp.async.commit_group;" ::: "memory");  // keeps one group per tile
             }
@@ -740,6 +760,132 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
 }
 
 // ------------------------------------------------------------------------------------------
+// Expert-ordered rows (nvfp4_quantize_grouped).  The row map says which row of x a row of the
+// expert-ordered matrix holds; the Hadamard and tile passes above take it as a template option,
+// the row-wise passes have kernels of their own because a row of x may be needed several times.
+// ------------------------------------------------------------------------------------------
+
+// Partial maxima of |x| over the rows of x that some expert takes: a warp per row.  A row of x
+// is read once, however many experts take it.
+__global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __restrict__ x,
+                                                           int64_t rows, int64_t cols, int64_t ld,
+                                                           uint32_t* __restrict__ partials,
+                                                           int* dev_status, const RowMap map)
+{
+    const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
+    const int lane = threadIdx.x & 31;
+    const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    const int64_t n = map.gather ? map.tokens : map.used_rows(rows);
+    const int64_t cpr = cols >> 3;
+    uint32_t m = 0;
+    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
+         r += wstride) {
+        bool used;
+        if (map.gather) {
+            bool mine = false;
+            for (int64_t j = lane; j < map.k; j += 32) mine |= map.pair_target(r, j, rows) >= 0;
+            used = __any_sync(0xFFFFFFFFu, mine);
+        } else {
+            used = map.source(r) >= 0;
+        }
+        if (!used) continue;
+        const uint4* p = reinterpret_cast<const uint4*>(x + r * ld);
+        for (int64_t c = lane; c < cpr; c += 32)
+            m = max(m, absmax_bits8(ldg_checked(p + c, x, xb, dev_status)));
+    }
+    block_max_store(m, partials + blockIdx.x);
+}
+
+// One 16-byte chunk per lane (8 values, half a block) of a warp's row: the packed codes and, in the
+// lanes 8 k, the scale word of four blocks.
+template <bool SR>
+__device__ __forceinline__ void quant_chunk(const uint4& v, const TensorScale& ts,
+                                            const float* r_tab, const Philox& ph, uint64_t group,
+                                            uint64_t offset, uint32_t& packed, uint32_t& sfw)
+{
+    float e[8];
+    unpack8(v, e);
+    const float m = absmax_f32<8>(e);
+    const float b = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    const BlockScale bs = block_scale(b, ts.s_enc, r_tab);
+    packed = ts.nonfinite ? 0u : encode8<SR>(v, e, bs, ph, group, offset);
+    const uint32_t sf = ts.nonfinite ? 0u : bs.sf;
+    const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, sf, 2);
+    const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, sf, 4);
+    const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, sf, 6);
+    sfw = sf | (s1 << 8) | (s2 << 16) | (s3 << 24);
+}
+
+// Row-wise codes and scales of an expert-ordered matrix, a warp per row.
+//  * SCATTER (gathered, round to nearest): the warp takes a row of x, quantizes it once and writes
+//    it to the row of every expert that takes it; the rows without a token are zeroed after.
+//  * otherwise the warp takes a row of the expert-ordered matrix (stochastic rounding draws other
+//    bits for every such row).
+// Rows behind the last region are not written.
+template <bool SR, bool SCATTER>
+__global__ void __launch_bounds__(256) quant_grouped_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, QuantSource src,
+    float* amax_out, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+    const PhiloxKeys keys, uint64_t offset, int* dev_status, const RowMap map)
+{
+    __shared__ float r_tab[128];
+    const TensorScale ts = fold_amax(src, amax_out, nullptr, dev_status);
+    fill_factor_table(r_tab, ts.s_enc);
+    __syncthreads();
+    const Philox philox{keys};
+    const int lane = threadIdx.x & 31;
+    const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    const int64_t wfirst = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int64_t cpr = cols >> 3, gpr = cols >> 6;
+    const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
+    const int64_t cb = codes_extent(rows, cols), sb = scales_extent(rows, cols);
+    const int64_t used = map.used_rows(rows);
+    auto store = [&](int64_t r, int64_t c, uint32_t packed, uint32_t sfw) {
+        st_checked(reinterpret_cast<uint32_t*>(codes) + r * cpr + c, packed, codes, cb, dev_status);
+        if ((lane & 7) == 0)
+            st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, c >> 1, gpr)), sfw, scales, sb,
+                       dev_status);
+    };
+    if (SCATTER) {
+        for (int64_t t = wfirst; t < map.tokens; t += wstride) {
+            // lane j holds the row of the token's j-th expert
+            const int64_t target = lane < map.k ? map.pair_target(t, lane, rows) : -1;
+            const unsigned taken = __ballot_sync(0xFFFFFFFFu, target >= 0);
+            if (taken == 0) continue;
+            const uint4* p = reinterpret_cast<const uint4*>(x + t * ld);
+            for (int64_t c0 = 0; c0 < cpr; c0 += 32) {
+                const int64_t c = c0 + lane;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (c < cpr) v = ldg_checked(p + c, x, xb, dev_status);
+                uint32_t packed, sfw;
+                quant_chunk<false>(v, ts, r_tab, philox, 0, 0, packed, sfw);
+                for (unsigned left = taken; left; left &= left - 1) {
+                    const int64_t r = __shfl_sync(0xFFFFFFFFu, target, __ffs(left) - 1);
+                    if (c < cpr) store(r, c, packed, sfw);
+                }
+            }
+        }
+    }
+    for (int64_t r = wfirst; r < used; r += wstride) {
+        const int64_t from = map.source(r);
+        if (SCATTER) {
+            if (from >= 0) continue;
+            for (int64_t c = lane; c < cpr; c += 32) store(r, c, 0u, 0u);
+            continue;
+        }
+        const uint4* p = reinterpret_cast<const uint4*>(x + (from >= 0 ? from : 0) * ld);
+        for (int64_t c0 = 0; c0 < cpr; c0 += 32) {
+            const int64_t c = c0 + lane;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (c < cpr && from >= 0) v = ldg_checked(p + c, x, xb, dev_status);
+            uint32_t packed, sfw;
+            quant_chunk<SR>(v, ts, r_tab, philox, static_cast<uint64_t>(r * cpr + c), offset, packed, sfw);
+            if (c < cpr) store(r, c, packed, sfw);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------
 // Launchers
 // ------------------------------------------------------------------------------------------
 
@@ -821,15 +967,16 @@ cudaError_t launch_quant_rowwise(const uint16_t* x, int64_t rows, int64_t cols, 
     return cudaGetLastError();
 }
 
-template <bool ROW, bool COL, bool B2D, bool RHT, bool SR, bool MX = false>
+template <bool ROW, bool COL, bool B2D, bool RHT, bool SR, bool MX = false, bool GROUPED = false>
 static void launch_tile_t(const TileArgs& a, int64_t ntiles, int sm_count, cudaStream_t s)
 {
     static const int resident =
-        resident_ctas(quant_tile_kernel<ROW, COL, B2D, RHT, SR, MX>, 128);
+        resident_ctas(quant_tile_kernel<ROW, COL, B2D, RHT, SR, MX, GROUPED>, 128);
     int64_t grid = static_cast<int64_t>(sm_count) * resident;
     if (grid > ntiles) grid = ntiles;
     if (grid < 1) grid = 1;
-    quant_tile_kernel<ROW, COL, B2D, RHT, SR, MX><<<static_cast<int>(grid), 128, 0, s>>>(a);
+    quant_tile_kernel<ROW, COL, B2D, RHT, SR, MX, GROUPED>
+        <<<static_cast<int>(grid), 128, 0, s>>>(a);
 }
 
 cudaError_t launch_quant_tile(const TileArgs& a, bool row, bool col, bool block2d, bool rht,
@@ -866,6 +1013,68 @@ cudaError_t launch_quant_tile(const TileArgs& a, bool row, bool col, bool block2
     else if (col && !rht && sr)           launch_tile_t<false, true, false, false, true>(a, g, sm, s);
     else if (col && !rht && !sr)          launch_tile_t<false, true, false, false, false>(a, g, sm, s);
     else return cudaErrorInvalidValue;
+    return cudaGetLastError();
+}
+
+int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, int sm_count)
+{
+    if (rht) return amax_grid(rows, cols, true, sm_count);
+    static const int resident = resident_ctas(amax_grouped_kernel, 256);
+    const int64_t n = ((map.gather ? map.tokens : rows) + 7) / 8;  // a warp per row
+    int64_t g = static_cast<int64_t>(sm_count) * resident;
+    if (g > n) g = n;
+    if (g > kMaxPartials) g = kMaxPartials;
+    return static_cast<int>(g < 1 ? 1 : g);
+}
+
+cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, bool rht,
+                                uint32_t sign_mask, uint32_t* partials, uint32_t* partials_plain,
+                                int grid, const RowMap& map, int* dev_status, cudaStream_t s)
+{
+    if (rht && partials_plain)
+        amax_rht_kernel<true, true><<<grid, 256, 0, s>>>(x, rows, cols, ld, sign_mask, partials,
+                                                         partials_plain, dev_status, map);
+    else if (rht)
+        amax_rht_kernel<false, true><<<grid, 256, 0, s>>>(x, rows, cols, ld, sign_mask, partials,
+                                                          nullptr, dev_status, map);
+    else
+        amax_grouped_kernel<<<grid, 256, 0, s>>>(x, rows, cols, ld, partials, dev_status, map);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_quant_grouped_rows(const TileArgs& a, bool sr, int sm_count, cudaStream_t s)
+{
+    const bool scatter = a.map.gather && !sr;
+    static const int resident[3] = {resident_ctas(quant_grouped_kernel<false, false>, 256),
+                                    resident_ctas(quant_grouped_kernel<true, false>, 256),
+                                    resident_ctas(quant_grouped_kernel<false, true>, 256)};
+    int64_t grid = static_cast<int64_t>(sm_count) * resident[scatter ? 2 : (sr ? 1 : 0)];
+    const int64_t n = ((scatter && a.map.tokens > a.rows ? a.map.tokens : a.rows) + 7) / 8;
+    if (grid > n) grid = n;
+    const int g = static_cast<int>(grid);
+    if (scatter)
+        quant_grouped_kernel<false, true><<<g, 256, 0, s>>>(
+            a.x, a.rows, a.cols, a.ld, a.src, a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset,
+            a.dev_status, a.map);
+    else if (sr)
+        quant_grouped_kernel<true, false><<<g, 256, 0, s>>>(
+            a.x, a.rows, a.cols, a.ld, a.src, a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset,
+            a.dev_status, a.map);
+    else
+        quant_grouped_kernel<false, false><<<g, 256, 0, s>>>(
+            a.x, a.rows, a.cols, a.ld, a.src, a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset,
+            a.dev_status, a.map);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_quant_grouped_tile(const TileArgs& a, bool row, bool sr, int sm_count,
+                                      cudaStream_t s)
+{
+    const int64_t n = (a.rows / kTileRows) * ((a.cols + kTileCols - 1) / kTileCols);
+    if (row && sr)       launch_tile_t<true, true, false, true, true, false, true>(a, n, sm_count, s);
+    else if (row)        launch_tile_t<true, true, false, true, false, false, true>(a, n, sm_count, s);
+    else if (sr)         launch_tile_t<false, true, false, true, true, false, true>(a, n, sm_count, s);
+    else                 launch_tile_t<false, true, false, true, false, false, true>(a, n, sm_count, s);
     return cudaGetLastError();
 }
 

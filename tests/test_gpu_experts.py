@@ -1,0 +1,706 @@
+"""GPU parity of the mixture-of-experts operators: routing, plan, grouped quantization (bit for bit
+against the oracle), grouped products, combination, and a whole layer forward and backward."""
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as R
+import oracle
+import synth
+from nvfp4_testlib import (assert_gemm_close, need_gpu, sf_offsets, to_device_bf16,
+                           upload_quantized)
+
+nv = pytest.importorskip("nvfp4_bit_quantized_03_b200")
+B = nv.binding
+
+pytestmark = pytest.mark.gpu
+
+HALF_BF16 = 2.0 ** -8   # largest relative rounding error of bf16
+HALF_F32 = 2.0 ** -24   # of FP32
+
+
+@pytest.fixture(params=["release", "checked"], autouse=True)
+def _library(request):
+    """Every test runs through both libraries (the checked one skips and reports stray accesses)."""
+    need_gpu()
+    if request.param == "release":
+        yield
+    else:
+        with B.bounds_checked():
+            yield
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _bits(t):
+    return t.view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def _logits(rng, T, E, dtype):
+    l = torch.from_numpy(rng.normal(0, 2, (T, E)).astype(np.float32))
+    return l.to(dtype).cuda(), l.to(dtype).double().numpy()
+
+
+def _check_route(logits_dev, logits, k, what="", expect_status=0, **kw):
+    st = _status()
+    bias = kw.pop("bias", None)
+    e, w = B.route(logits_dev, k, bias=None if bias is None else _dev(bias), dev_status=st, **kw)
+    torch.cuda.synchronize()
+    assert int(st) == expect_status, what
+    er, wr = R.route(logits, k, bias=bias, **kw)
+    assert np.array_equal(e.cpu().numpy(), er), (what, np.argwhere(e.cpu().numpy() != er)[:5])
+    # w = c p / sum p, p = exp(q - top): the log-scores q carry an absolute error of at most
+    # (4 + |q|) half-steps each (log1p, subtraction), exp 4 half-steps, the sums over at most
+    # k <= 32 or E values 16 more (tree sums of at most log2(512) + 16 / 32 terms per lane), the
+    # quotient and the factor 2.
+    finite = np.where(np.isfinite(logits), np.abs(logits), 0)
+    tol = (40 + 4 * finite.max(axis=1, keepdims=True)) * HALF_F32
+    got = w.cpu().numpy().astype(np.float64)
+    # scores below FP32's normal range come as its subnormals or zero
+    assert np.all(np.abs(got - wr) <= tol * wr + 2.0 ** -126), what
+    return e, w
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 6), (3, 5, 5), (7, 33, 4), (130, 128, 8),
+                                   (65, 256, 8), (9, 257, 32), (5, 512, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route(T, E, k, dtype, sigmoid, renorm):
+    rng = np.random.default_rng(T * 1000 + E)
+    ld, l = _logits(rng, T, E, dtype)
+    kw = dict(sigmoid=sigmoid, renorm=renorm, scale=2.5)
+    _check_route(ld, l, k, "plain", **kw)
+    bias = rng.normal(0, 0.1, E).astype(np.float32)
+    _check_route(ld, l, k, "bias", bias=bias, **kw)
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(64, 8, 3, 6), (256, 8, 4, 8), (60, 4, 1, 15),
+                                            (7, 7, 3, 3), (96, 32, 5, 4), (512, 32, 32, 8),
+                                            (30, 3, 2, 20)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_groups(E, groups, top, k, sigmoid, with_bias):
+    rng = np.random.default_rng(E + k)
+    ld, l = _logits(rng, 50, E, torch.bfloat16)
+    bias = rng.normal(0, 0.2, E).astype(np.float32) if with_bias else None
+    _check_route(ld, l, k, bias=bias, sigmoid=sigmoid, groups=groups, top_groups=top)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_excluded_and_bad_rows(sigmoid):
+    rng = np.random.default_rng(3)
+    _, l = _logits(rng, 12, 40, torch.float32)
+    l = l.astype(np.float32)
+    l[0] = -np.inf                       # nothing to choose
+    l[1, :37] = -np.inf                  # three left for four slots
+    l[2, 5] = np.nan
+    l[3, 39] = np.inf
+    l[4] = -3.0e38                       # the lowest values of the type
+    l[5] = 0.0                           # all equal: the lowest indices
+    l[6, ::2] = -0.0
+    l[6, 1::2] = 0.0
+    l[7, 10:] = -np.inf
+    l[8] = -200.0 - np.arange(40)        # scores that underflow: shares stay exact
+    l[9] = 120.0 + np.arange(40) % 7     # scores that saturate
+    for bias in (None, rng.normal(0, 0.1, 40).astype(np.float32)):
+        for groups, top in ((1, 1), (8, 2), (4, 4)):
+            _check_route(_dev(l), l.astype(np.float64), 4, (bias is None, groups),
+                         expect_status=B.DEVSTAT_NONFINITE, bias=bias, sigmoid=sigmoid,
+                         groups=groups, top_groups=top)
+
+
+def test_route_bias_excludes_and_flags():
+    rng = np.random.default_rng(4)
+    ld, l = _logits(rng, 9, 16, torch.float32)
+    bias = np.zeros(16, np.float32)
+    bias[3] = bias[7] = -np.inf
+    _check_route(ld, l, 5, bias=bias)
+    bias[3] = np.inf
+    e, w = B.route(ld, 5, bias=_dev(bias), dev_status=(st := _status()))
+    assert int(st) == B.DEVSTAT_NONFINITE and (e == -1).all() and (w == 0).all()
+
+
+def test_route_decides_what_fp32_cannot():
+    """Scores plus bias that differ by less than an FP32 step: the choice is that of FP64."""
+    rng = np.random.default_rng(5)
+    T, E = 64, 48
+    l = rng.normal(0, 1, (T, E)).astype(np.float32)
+    for sigmoid in (False, True):
+        # a bias that makes row 0's values equal to within FP32, different in FP64
+        bias = (1.0 - R.scores(l[:1].astype(np.float64), sigmoid)[0]).astype(np.float32)
+        l2 = np.repeat(l[:1], T, 0)
+        l2 += (rng.integers(-3, 4, (T, E)) * 2.0 ** -23).astype(np.float32)
+        _check_route(_dev(l2), l2.astype(np.float64), 6, bias=bias, sigmoid=sigmoid)
+        _check_route(_dev(l2), l2.astype(np.float64), 6, bias=bias, sigmoid=sigmoid, groups=6,
+                     top_groups=2)
+
+
+def test_route_strided_rows_and_given_outputs():
+    rng = np.random.default_rng(6)
+    wide = torch.from_numpy(rng.normal(0, 1, (33, 101)).astype(np.float32)).cuda()
+    view = wide[:, 3:70]
+    e = torch.empty(33, 3, dtype=torch.int32, device="cuda")
+    w = torch.empty(33, 3, device="cuda")
+    got = B.route(view, 3, experts=e, weights=w)
+    assert got[0] is e and got[1] is w
+    er, _ = R.route(view.double().cpu().numpy(), 3)
+    assert np.array_equal(e.cpu().numpy(), er)
+
+
+def _check_backward(ld, l, experts, dw, sigmoid, renorm, scale):
+    d = B.route_backward(ld, _dev(experts), _dev(dw), sigmoid=sigmoid, renorm=renorm, scale=scale)
+    ref = R.route_backward(l, experts, dw, sigmoid, renorm, scale)
+    got = d.double().cpu().numpy()
+    # every result is a sum of products of magnitude at most scale p (|g| + sum |g| p): forward
+    # error of the shares as in the weights, taken over at most k + 2 terms
+    g = scale * np.abs(dw).max(axis=1, keepdims=True)
+    tol = (60 + 8 * np.abs(l).max(axis=1, keepdims=True)) * HALF_F32 * g * (2 + experts.shape[1])
+    if d.dtype == torch.bfloat16:
+        tol = tol + HALF_BF16 * np.abs(ref)
+    assert np.all(np.abs(got - ref) <= tol), float(np.abs(got - ref).max())
+    return ref
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (5, 7, 7), (66, 64, 6), (33, 200, 8), (3, 512, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward(T, E, k, dtype, sigmoid, renorm):
+    rng = np.random.default_rng(E * 10 + k)
+    ld, l = _logits(rng, T, E, dtype)
+    experts, _ = R.route(l, k, sigmoid=sigmoid)
+    if T > 2:
+        experts[1] = -1          # a row without experts
+        experts[2, 1:] = -1      # and one with one only
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32)
+    _check_backward(ld, l, experts, dw, sigmoid, renorm, 1.5)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_against_differences(sigmoid, renorm):
+    rng = np.random.default_rng(11)
+    T, E, k, h = 4, 9, 3, 1e-5
+    l = rng.normal(0, 1, (T, E)).astype(np.float32).astype(np.float64)
+    experts, _ = R.route(l, k, sigmoid=sigmoid, renorm=renorm)
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32)
+
+    def weights(x):
+        s = np.take_along_axis(R.scores(x, sigmoid), experts, 1)
+        return 2.0 * (s / s.sum(1, keepdims=True) if renorm else s)
+    num = np.zeros_like(l)
+    for e in range(E):
+        step = np.zeros(E)
+        step[e] = h
+        num[:, e] = ((weights(l + step) - weights(l - step)) * dw).sum(1) / (2 * h)
+    got = B.route_backward(_dev(l.astype(np.float32)), _dev(experts), _dev(dw), sigmoid=sigmoid,
+                           renorm=renorm, scale=2.0).double().cpu().numpy()
+    # central differences: h^2 / 6 of a third derivative below 2 * 3 * |dw|, rounding 2^-52 / h;
+    # the kernel's FP32 as above
+    tol = h * h * np.abs(dw).max() + 2.0 ** -50 / h + 200 * HALF_F32 * 2 * np.abs(dw).sum()
+    assert np.abs(got - num).max() <= tol
+
+
+def test_route_backward_odd_inputs():
+    rng = np.random.default_rng(12)
+    l = rng.normal(0, 1, (6, 20)).astype(np.float32)
+    l[0] = np.nan                   # routed nowhere
+    l[1, 4:] = -np.inf              # excluded experts get no gradient
+    experts = np.stack([rng.permutation(4)[:3] for _ in range(6)]).astype(np.int32)
+    experts[0] = -1
+    experts[2] = [3, 3, 1]          # the same expert twice counts twice
+    experts[3] = [0, 20, -7]        # outside: no part, and a status
+    dw = rng.normal(0, 1, (6, 3)).astype(np.float32)
+    ref_experts = experts.copy()
+    ref_experts[3, 1:] = -1
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            st = _status()
+            got = B.route_backward(_dev(l), _dev(experts), _dev(dw), sigmoid=sigmoid, renorm=renorm,
+                                   dev_status=st).double().cpu().numpy()
+            assert int(st) == B.DEVSTAT_INDEX
+            assert np.all(got[0] == 0)
+            ref = R.route_backward(np.where(np.isnan(l), 0, l), ref_experts, dw, sigmoid, renorm, 1.0)
+            assert np.abs(got - ref).max() <= 400 * HALF_F32 * np.abs(dw).sum(1).max()
+
+
+# ---- the plan ------------------------------------------------------------------------------
+
+def _plan(experts, E, rows=None):
+    rows = R.expert_rows(*experts.shape, E) if rows is None else rows
+    o, p, r = R.plan(experts, E, rows)
+    return B.ExpertPlan(_dev(o), _dev(p), _dev(r)), o, p, r
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 6, 64), (5, 3, 7), (300, 2, 3), (257, 8, 64),
+                                   (2048, 1, 5), (2049, 1, 512), (1500, 8, 200), (9000, 2, 16)])
+def test_plan(T, k, E):
+    rng = np.random.default_rng(T + E)
+    experts = R.routing(rng, T, E, k, pad=T // 4)
+    experts[T // 2, k - 1] = -1
+    _, o, p, r = _plan(experts, E)
+    st = _status()
+    got = B.expert_plan(_dev(experts), E, dev_status=st)
+    assert int(st) == 0
+    assert np.array_equal(got.offsets.cpu().numpy(), o)
+    assert np.array_equal(got.pair_row.cpu().numpy(), p)
+    assert np.array_equal(got.row_token.cpu().numpy(), r)
+
+
+def test_plan_one_expert_takes_all_and_none_takes_any():
+    for experts, E in ((np.full((700, 1), 5, np.int32), 9), (np.full((50, 2), -1, np.int32), 4)):
+        _, o, p, r = _plan(experts, E)
+        got = B.expert_plan(_dev(experts), E)
+        for a, b in ((got.offsets, o), (got.pair_row, p), (got.row_token, r)):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("T", [40, 3000])
+def test_plan_stray_and_repeated_indices(T):
+    rng = np.random.default_rng(1)
+    experts = R.routing(rng, T, 8, 3)
+    experts[3] = [2, 2, 2]
+    clean = experts.copy()
+    for t, v in ((5, 8), (7, -2), (11, 2 ** 31 - 1), (T - 1, -2 ** 31)):
+        experts[t, 1] = v
+        clean[t, 1] = -1
+    _, o, p, r = _plan(clean, 8)
+    st = _status()
+    got = B.expert_plan(_dev(experts), 8, dev_status=st)
+    assert int(st) == B.DEVSTAT_INDEX
+    for a, b in ((got.offsets, o), (got.pair_row, p), (got.row_token, r)):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_plan_with_spare_rows():
+    experts = R.routing(np.random.default_rng(2), 30, 6, 2)
+    rows = R.expert_rows(30, 2, 6) + 384
+    _, o, p, r = _plan(experts, 6, rows)
+    plan = B.ExpertPlan.empty(30, 2, 6, rows=rows)
+    B.expert_plan(_dev(experts), 6, plan=plan)
+    assert np.array_equal(plan.row_token.cpu().numpy(), r)
+    assert np.array_equal(plan.offsets.cpu().numpy(), o)
+
+
+# ---- grouped quantization --------------------------------------------------------------------
+
+def _check_quantized(q, ref, used, by_cols, what):
+    """Codes and scales of the used rows (columns) equal the oracle's; the others untouched."""
+    codes, scales = q.codes.cpu().numpy(), q.scales.cpu().numpy()
+    assert float(q.amax) == ref.amax or (np.isinf(float(q.amax)) and np.isinf(ref.amax)), what
+    plain = scales[sf_offsets(q.rows, q.cols)]
+    if by_cols:
+        assert np.array_equal(codes[:, :used // 2], ref.codes[:, :used // 2]), what
+        assert np.array_equal(plain[:, :used // 16], ref.scales[:, :used // 16]), what
+        assert np.all(codes[:, used // 2:] == 0xFF) and np.all(plain[:, used // 16:] == 0xFF), what
+    else:
+        assert np.array_equal(codes[:used], ref.codes[:used]), what
+        assert np.array_equal(plain[:used], ref.scales[:used]), what
+        assert np.all(codes[used:] == 0xFF) and np.all(plain[used:] == 0xFF), what
+
+
+def _source(rng, plan_parts, T, rows, C, gather, grads=False):
+    """bf16 bits of x (token rows or expert order) and of the expert-ordered matrix it stands for.
+    Rows that nothing takes hold NaN."""
+    o, p, r = plan_parts
+    make = synth.gradients if grads else synth.activations
+    x = make((T if gather else rows, C), seed=int(rng.integers(1 << 30)))
+    if gather:
+        x[~(p >= 0).any(axis=1)] = 0x7FC0
+        return x, R.gather_bits(x, r)
+    x[r < 0] = 0x7FC0
+    full = x.copy()
+    full[r < 0] = 0
+    return x, full
+
+
+CASES = [(1, 1, 1, 64, 0), (1, 8, 64, 256, 0), (40, 2, 5, 192, 6), (300, 3, 8, 320, 0),
+         (129, 1, 2, 1088, 30)]
+
+
+@pytest.mark.parametrize("T,k,E,C,pad", CASES)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("sr", [False, True])
+def test_quantize_grouped(T, k, E, C, pad, gather, sr):
+    rng = np.random.default_rng(T * 7 + C)
+    experts = R.routing(rng, T, E, k, pad=pad, empty=(1,) if E > k + 1 else ())
+    plan, *parts = _plan(experts, E)
+    used = int(parts[0][-1])
+    x, full = _source(rng, parts, T, plan.rows, C, gather, sr)
+    xd = to_device_bf16(x)
+    flags = (B.SR if sr else 0) | (B.GATHER if gather else 0)
+    mask, seed = 0x5A3C, 77
+    row = oracle.quantize(full, sr=sr, seed=seed, offset=4)
+    col = oracle.quantize(full, transpose=True, rht=True, sign_mask=mask, sr=sr, seed=seed, offset=5)
+    kw = dict(sign_mask=mask, seed=seed, offset=4)
+    for f in (B.ROWWISE, B.COLWISE, B.ROWWISE | B.COLWISE):
+        st = _status()
+        qr, qc = B.quantize_grouped(xd, plan, f | flags, dev_status=st, **kw)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        if f & B.ROWWISE:
+            _check_quantized(qr, row, used, False, (f, "row"))
+        if f & B.COLWISE:
+            _check_quantized(qc, col, used, True, (f, "col"))
+
+
+def test_quantize_grouped_strided_given_amax_and_narrow_columns():
+    rng = np.random.default_rng(8)
+    experts = R.routing(rng, 50, 4, 2)
+    plan, *parts = _plan(experts, 4)
+    used = int(parts[0][-1])
+    wide = synth.activations((50, 448), seed=3)
+    for c0, C in ((64, 320), (8, 128)):
+        full = R.gather_bits(np.ascontiguousarray(wide[:, c0:c0 + C]), parts[2])
+        xd = to_device_bf16(wide)[:, c0:c0 + C]
+        qr, _ = B.quantize_grouped(xd, plan, B.ROWWISE | B.GATHER)
+        ref = oracle.quantize(full)
+        _check_quantized(qr, ref, used, False, "strided")
+        again = B.QuantizedTensor(plan.rows, C)
+        again.amax.copy_(qr.amax)
+        B.quantize_grouped(xd, plan, B.ROWWISE | B.GATHER | B.AMAX_GIVEN, out_row=again)
+        _check_quantized(again, ref, used, False, "amax given")
+    # columns a multiple of 16 only: the column-wise output alone
+    x = synth.activations((50, 80), seed=4)
+    full = R.gather_bits(x, parts[2])
+    _, qc = B.quantize_grouped(to_device_bf16(x), plan, B.COLWISE | B.GATHER, sign_mask=9)
+    _check_quantized(qc, oracle.quantize(full, transpose=True, rht=True, sign_mask=9), used, True,
+                     "narrow")
+
+
+@pytest.mark.parametrize("value", [0x7FC0, 0x7F80, 0xFF80])
+def test_quantize_grouped_nonfinite_token(value):
+    rng = np.random.default_rng(9)
+    experts = R.routing(rng, 20, 3, 1)
+    plan, *parts = _plan(experts, 3)
+    x = synth.activations((20, 128), seed=5)
+    x[7, 100] = value
+    st = _status()
+    qr, qc = B.quantize_grouped(to_device_bf16(x), plan, B.ROWWISE | B.COLWISE | B.GATHER,
+                                dev_status=st)
+    assert int(st) == B.DEVSTAT_NONFINITE
+    used = int(parts[0][-1])
+    assert np.isinf(float(qr.amax)) and np.isinf(float(qc.amax))
+    assert (qr.codes[:used] == 0).all() and (qc.codes[:, :used // 2] == 0).all()
+
+
+def test_quantize_grouped_without_any_pair():
+    experts = np.full((5, 2), -1, np.int32)
+    plan, *parts = _plan(experts, 4)
+    x = np.full((5, 64), 0x7FC0, np.uint16)
+    st = _status()
+    qr, qc = B.quantize_grouped(to_device_bf16(x), plan, B.ROWWISE | B.COLWISE | B.GATHER,
+                                dev_status=st)
+    assert int(st) == 0 and float(qr.amax) == 0 and float(qc.amax) == 0
+    assert (qr.codes == 0xFF).all() and (qc.codes == 0xFF).all()
+
+
+# ---- grouped products ------------------------------------------------------------------------
+
+def _weights(E, O, I, seed):
+    w = synth.weights((E * O, I), seed=seed)
+    return w, oracle.quantize(w, block2d=True), oracle.quantize(w, transpose=True, block2d=True)
+
+
+def _rows_of(q, a, b):
+    return oracle.Quantized(q.codes[a:b], q.scales[a:b], q.amax, q.status)
+
+
+def _cols_of(q, a, b):
+    return oracle.Quantized(np.ascontiguousarray(q.codes[:, a // 2:b // 2]),
+                            np.ascontiguousarray(q.scales[:, a // 16:b // 16]), q.amax, q.status)
+
+
+def _check_rows(D, qa, offsets, weight_of, bf16, what):
+    D = D.float().cpu().numpy()
+    for e in range(len(offsets) - 1):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if a < b:
+            ref, norm = oracle.gemm_ref(_rows_of(qa, a, b), weight_of(e))
+            assert_gemm_close(D[a:b], ref, norm, bf16=bf16, what=(what, e))
+    assert np.isnan(D[int(offsets[-1]):]).all(), (what, "rows behind the last region were written")
+
+
+PRODUCTS = [(1, 1, 1, 64, 128), (1, 4, 9, 256, 256), (200, 2, 3, 320, 384), (530, 1, 4, 192, 128),
+            (900, 2, 2, 576, 640)]
+
+
+@pytest.mark.parametrize("T,k,E,I,O", PRODUCTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gemm_grouped_by_rows(T, k, E, I, O, dtype):
+    rng = np.random.default_rng(T + O)
+    experts = R.routing(rng, T, E, k, empty=(0,) if E > k else ())
+    plan, o, p, r = _plan(experts, E)
+    _, wr, wc = _weights(E, O, I, 1)
+    bf16 = dtype == torch.bfloat16
+    st = _status()
+    full = R.gather_bits(synth.activations((T, I), seed=2), r)
+    qa = oracle.quantize(full)
+    D = B.gemm_grouped(upload_quantized(qa, B), upload_quantized(wr, B), plan, out_dtype=dtype,
+                       dev_status=st)
+    _check_rows(D, qa, o, lambda e: _rows_of(wr, e * O, (e + 1) * O), bf16, "stacked")
+    g = R.gather_bits(synth.gradients((T, O), seed=3), r)
+    qg = oracle.quantize(g, sr=True, seed=5, offset=0)
+    D = B.gemm_grouped(upload_quantized(qg, B), upload_quantized(wc, B), plan, out_dtype=dtype,
+                       dev_status=st)
+    _check_rows(D, qg, o, lambda e: _cols_of(wc, e * O, (e + 1) * O), bf16, "side by side")
+    torch.cuda.synchronize()
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("T,k,E,I,O", PRODUCTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gemm_grouped_by_k(T, k, E, I, O, dtype):
+    rng = np.random.default_rng(T + I)
+    experts = R.routing(rng, T, E, k, empty=(E - 1,) if E > k else ())
+    plan, o, p, r = _plan(experts, E)
+    x = R.gather_bits(synth.activations((T, I), seed=2), r)
+    g = R.gather_bits(synth.gradients((T, O), seed=3), r)
+    qx = oracle.quantize(x, transpose=True, rht=True, sign_mask=77)
+    qg = oracle.quantize(g, transpose=True, rht=True, sign_mask=77, sr=True, seed=1, offset=1)
+    st = _status()
+    D = B.gemm_grouped_k(upload_quantized(qg, B), upload_quantized(qx, B), plan, out_dtype=dtype,
+                         dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    D = D.float().cpu().numpy().reshape(E, O, I)
+    for e in range(E):
+        a, b = int(o[e]), int(o[e + 1])
+        if a == b:
+            assert np.all(D[e] == 0)
+            continue
+        ref, norm = oracle.gemm_ref(_cols_of(qg, a, b), _cols_of(qx, a, b))
+        assert_gemm_close(D[e], ref, norm, bf16=dtype == torch.bfloat16, what=e)
+
+
+def test_gemm_grouped_strided_output_leaves_the_gaps():
+    experts = R.routing(np.random.default_rng(0), 70, 3, 2)
+    plan, o, p, r = _plan(experts, 3)
+    _, wr, _ = _weights(3, 128, 128, 4)
+    qa = oracle.quantize(R.gather_bits(synth.activations((70, 128), seed=6), r))
+    wide = torch.full((plan.rows, 160), 7.0, device="cuda")
+    B.gemm_grouped(upload_quantized(qa, B), upload_quantized(wr, B), plan, out=wide[:, 16:144])
+    used = int(o[-1])
+    assert (wide[:, :16] == 7).all() and (wide[:, 144:] == 7).all() and (wide[used:] == 7).all()
+    D = wide[:used, 16:144].cpu().numpy()
+    for e in range(3):
+        ref, norm = oracle.gemm_ref(_rows_of(qa, o[e], o[e + 1]), _rows_of(wr, e * 128, e * 128 + 128))
+        assert_gemm_close(D[o[e]:o[e + 1]], ref, norm)
+
+
+# ---- combination -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,k,E,C,pad", [(1, 1, 1, 8, 0), (1, 8, 16, 4096, 0), (37, 3, 5, 1000, 4),
+                                         (300, 2, 4, 64, 0), (5, 32, 40, 2056, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_combine_and_backward(T, k, E, C, pad, dtype):
+    rng = np.random.default_rng(T + C)
+    experts = R.routing(rng, T, E, k, pad=pad)
+    experts[0, k - 1] = -1 if k > 1 else experts[0, 0]
+    plan, o, p, r = _plan(experts, E)
+    y = torch.from_numpy(rng.normal(0, 1, (plan.rows, C)).astype(np.float32)).bfloat16()
+    y[torch.from_numpy(r < 0)] = float("nan")   # rows that nothing takes are not looked at
+    w = rng.normal(0, 1, (T, k)).astype(np.float32)
+    w[p < 0] = np.nan
+    yd, half = y.double().numpy(), HALF_BF16 if dtype == torch.bfloat16 else 0.0
+    taken = np.where((p >= 0)[..., None], yd[np.maximum(p, 0)], 0.0)
+    for weights in (w, None):
+        ww = np.where(p >= 0, 1.0 if weights is None else w.astype(np.float64), 0.0)
+        ref = (ww[..., None] * taken).sum(1)
+        size = (np.abs(ww)[..., None] * np.abs(taken)).sum(1)
+        out = B.combine(y.cuda(), plan, None if weights is None else _dev(w), out_dtype=dtype)
+        err = np.abs(out.double().cpu().numpy() - ref)
+        # k products and sums in FP32, then the output's rounding
+        tol = (k + 1) * HALF_F32 * size
+        assert np.all(err <= tol + half * (np.abs(ref) + tol))
+    dout = torch.from_numpy(rng.normal(0, 1, (T, C)).astype(np.float32)).to(dtype)
+    dy, dw = B.combine_backward(dout.cuda(), y.cuda(), plan, _dev(w))
+    dd = dout.double().numpy()
+    dy = dy.double().cpu().numpy()
+    used = int(o[-1])
+    assert np.all(dy[:used][r[:used] < 0] == 0) and np.isnan(dy[used:]).all()
+    ok = p >= 0
+    ref = np.where(ok[..., None], np.where(ok, w, 0).astype(np.float64)[..., None] * dd[:, None], 0)
+    got = np.where(ok[..., None], dy[np.maximum(p, 0)], 0)
+    # one FP32 product, rounded to bf16
+    assert np.all(np.abs(got - ref) <= (HALF_BF16 * (1 + HALF_F32) + HALF_F32) * np.abs(ref))
+    rw = (dd[:, None] * taken).sum(2)
+    sw = (np.abs(dd)[:, None] * np.abs(taken)).sum(2)
+    # C products and sums in FP32: a thread's run of C / 128, then a tree
+    assert np.all(np.abs(dw.double().cpu().numpy() - rw) <= (C / 128 + 16) * HALF_F32 * sw)
+
+
+def test_combine_strided():
+    rng = np.random.default_rng(1)
+    experts = R.routing(rng, 20, 4, 2)
+    plan, o, p, r = _plan(experts, 4)
+    wide = torch.from_numpy(rng.normal(0, 1, (plan.rows, 72)).astype(np.float32)).bfloat16().cuda()
+    out = torch.full((20, 80), 5.0, dtype=torch.bfloat16, device="cuda")
+    B.combine(wide[:, 8:64], plan, out=out[:, 16:72])
+    ref = wide.double()[_dev(p).long()][:, :, 8:64].sum(1)
+    assert (out[:, :16] == 5).all() and (out[:, 72:] == 5).all()
+    err = (out[:, 16:72].double() - ref).abs()
+    assert (err <= HALF_BF16 * ref.abs() + 2 * HALF_F32 * wide.double().abs().max() * 2).all()
+    dy = torch.full((plan.rows, 72), 3.0, dtype=torch.bfloat16, device="cuda")
+    B.combine_backward(out[:, 16:72], wide[:, 8:64], plan, torch.ones(20, 2, device="cuda"),
+                       dy=dy[:, 8:64])
+    assert (dy[:, :8] == 3).all() and (dy[:, 64:] == 3).all()
+    assert torch.equal(dy[_dev(p).long().reshape(-1)][:, 8:64],
+                       out[:, None, 16:72].expand(20, 2, 56).reshape(40, 56))
+
+
+# ---- the whole layer -------------------------------------------------------------------------
+
+class _Layer:
+    """Up-projection, squared ReLU, down-projection over E experts, as a user writes it."""
+
+    def __init__(self, T, D, F, E, k, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def randn(*shape, s=1.0):
+            return (s * torch.randn(*shape, generator=g, device="cuda"))
+        self.k, self.E, self.T = k, E, T
+        self.x = randn(T, D).bfloat16()
+        self.logits = randn(T, E)
+        self.w1, self.w2 = randn(E * F, D, s=0.05).bfloat16(), randn(E * D, F, s=0.05).bfloat16()
+        self.dout = randn(T, D, s=1e-2).bfloat16()
+        both = B.ROWWISE | B.COLWISE | B.BLOCK2D
+        self.q1, self.q1t = B.quantize(self.w1, both)
+        self.q2, self.q2t = B.quantize(self.w2, both)
+        self.mask = B.sign_mask_from_seed(seed)
+        self.plan = B.ExpertPlan.empty(T, k, E)
+        self.status = _status()
+
+    def step(self):
+        st = self.status
+        experts, w = B.route(self.logits, self.k, sigmoid=True, scale=1.5, dev_status=st)
+        plan = B.expert_plan(experts, self.E, plan=self.plan, dev_status=st)
+        there = (plan.row_token >= 0)[:, None]
+        h = B.experts_fprop(self.x, self.q1, plan, dev_status=st)
+        h = torch.where(there, h, 0)
+        a = torch.relu(h).square()
+        y = B.experts_fprop(a, self.q2, plan, gather=False, dev_status=st)
+        out = B.combine(y, plan, w, dev_status=st)
+        dy, dw = B.combine_backward(self.dout, y, plan, w, dev_status=st)
+        da = B.experts_dgrad(dy, self.q2t, plan, 9, 0, dev_status=st)
+        dw2 = B.experts_wgrad(dy, a, plan, self.mask, 9, 0, gather=False, dev_status=st)
+        dh = torch.where(there, da, 0) * 2 * torch.relu(h)
+        dxr = B.experts_dgrad(dh, self.q1t, plan, 9, 2, dev_status=st)
+        dw1 = B.experts_wgrad(dh, self.x, plan, self.mask, 9, 2, dev_status=st)
+        dx = B.combine(dxr, plan, dev_status=st)
+        dl = B.route_backward(self.logits, experts, dw, sigmoid=True, scale=1.5, dev_status=st)
+        return dict(out=out, dx=dx, dw1=dw1, dw2=dw2, dl=dl, experts=experts, w=w)
+
+
+def _dense_reference(layer, got):
+    """The same layer in FP64 without quantization, by autograd."""
+    x = layer.x.double().requires_grad_()
+    w1, w2 = layer.w1.double().requires_grad_(), layer.w2.double().requires_grad_()
+    l = layer.logits.double().requires_grad_()
+    E, D = layer.E, x.shape[1]
+    e = got["experts"].long()
+    s = torch.sigmoid(l).gather(1, e)
+    w = 1.5 * s / s.sum(1, keepdim=True)
+    out = 0
+    for j in range(layer.k):
+        w1e, w2e = w1.view(E, -1, D)[e[:, j]], w2.view(E, D, -1)[e[:, j]]
+        h = torch.einsum("tfd,td->tf", w1e, x)
+        out = out + w[:, j:j + 1] * torch.einsum("tdf,tf->td", w2e, torch.relu(h).square())
+    g = torch.autograd.grad((out * layer.dout.double()).sum(), (x, w1, w2, l))
+    return dict(out=out.detach(), dx=g[0], dw1=g[1], dw2=g[2], dl=g[3])
+
+
+@pytest.mark.parametrize("T,D,F,E,k", [(96, 256, 384, 4, 2), (1, 128, 128, 5, 3), (210, 128, 256, 2, 1)])
+def test_layer_forward_and_backward(T, D, F, E, k):
+    layer = _Layer(T, D, F, E, k, seed=T)
+    got = layer.step()
+    torch.cuda.synchronize()
+    assert int(layer.status) == 0
+    ref = _dense_reference(layer, got)
+    # E2M1 with block scales keeps about 2.3 significant bits: an operand's relative error (2-norm) is
+    # near 0.1, of a stochastically rounded one 0.15; at most four such products follow one another.
+    # A wrong row, expert or transpose gives an error of 1 and more.
+    for name in ("out", "dx", "dw1", "dw2", "dl"):
+        a, b = got[name].double(), ref[name]
+        if name == "dl" and k == 1:
+            # the renormalised weight of a single expert is the constant 1.5 s / s: its gradient is
+            # zero, and the reference holds only the rounding of s (1 / s) - 1
+            assert torch.all(a == 0)
+            continue
+        rel = float((a - b).norm() / b.norm().clamp_min(1e-30))
+        assert rel < 0.5, (name, rel)
+
+
+def test_layer_runs_are_reproducible_and_graphs_follow_the_routing():
+    layer = _Layer(96, 128, 256, 6, 2, seed=1)
+    first = layer.step()
+    again = layer.step()
+    for name in first:
+        a, b = first[name], again[name]
+        assert torch.equal(a, b), name
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = layer.step()
+    for seed in (2, 3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        layer.logits.copy_(torch.randn(layer.logits.shape, generator=g, device="cuda"))
+        layer.logits[:, seed] += 4.0            # another routing, one expert crowded
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = {n: v.clone() for n, v in captured.items()}
+        eager = layer.step()
+        for name in kept:
+            assert torch.equal(kept[name], eager[name]), name
+    assert int(layer.status) == 0
+
+
+def test_calls_on_a_stream_of_their_own():
+    experts = R.routing(np.random.default_rng(0), 50, 4, 2)
+    plan, o, p, r = _plan(experts, 4)
+    x = to_device_bf16(synth.activations((50, 256), seed=1))
+    w = to_device_bf16(synth.weights((4 * 128, 256), seed=2))
+    q, _ = B.quantize(w, B.ROWWISE | B.BLOCK2D)
+    ref = B.experts_fprop(x, q, plan)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = B.experts_fprop(x, q, plan, stream=s)
+    out = B.combine(got, plan, stream=s)
+    s.synchronize()
+    used = int(o[-1])
+    assert torch.equal(got[:used], ref[:used])
+    assert torch.equal(out, B.combine(ref, plan))
+
+
+def test_a_plan_of_another_routing_stays_inside_the_buffers():
+    """Indices outside their ranges count as absent; nothing outside the buffers is touched."""
+    rng = np.random.default_rng(5)
+    experts = R.routing(rng, 40, 4, 2)
+    plan, o, p, r = _plan(experts, 4)
+    plan.pair_row[3, 0] = plan.rows + 5
+    plan.pair_row[4, 1] = -9
+    plan.row_token[0] = 40
+    plan.row_token[1] = 2 ** 31 - 1
+    plan.offsets[4] = plan.rows + 128
+    plan.offsets[2] = -128
+    x = to_device_bf16(synth.activations((40, 128), seed=1))
+    w = to_device_bf16(synth.weights((4 * 128, 128), seed=2))
+    q, _ = B.quantize(w, B.ROWWISE | B.BLOCK2D)
+    st = _status()
+    y = B.experts_fprop(x, q, plan, dev_status=st)
+    B.combine(y, plan, dev_status=st)
+    B.combine_backward(x, torch.zeros(plan.rows, 128, dtype=torch.bfloat16, device="cuda"), plan,
+                       torch.ones(40, 2, device="cuda"), dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) & ~B.DEVSTAT_NONFINITE == 0
