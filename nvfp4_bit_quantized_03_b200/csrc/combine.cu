@@ -28,17 +28,21 @@ __device__ __forceinline__ uint4 pack8(const float* f)
                       pack_bf16(f[6], f[7]));
 }
 
+// Pairs whose rows are read together: eight loads in flight per thread.
+constexpr int kTogether = 8;
+
 // A CTA per token and slice of its columns; a thread takes 8 columns at a time.
 template <bool F32>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a)
 {
-    __shared__ int64_t row[kMaxK];
+    __shared__ int row[kMaxK];
     __shared__ float weight[kMaxK];
     const int64_t t = blockIdx.x;
-    if (threadIdx.x < a.map.k) {
-        const int64_t p = t * a.map.k + threadIdx.x;
-        row[threadIdx.x] = a.map.pair_target(t, threadIdx.x, a.rows);
-        weight[threadIdx.x] = a.weights ? a.weights[p] : 1.0f;
+    const int k = static_cast<int>(a.map.k);
+    if (threadIdx.x < kMaxK) {
+        const int r = threadIdx.x < k ? static_cast<int>(a.map.pair_target(t, threadIdx.x, a.rows)) : -1;
+        row[threadIdx.x] = r;
+        weight[threadIdx.x] = r >= 0 && a.weights ? a.weights[t * k + threadIdx.x] : 1.0f;
     }
     __syncthreads();
     const int64_t yb = bf16_matrix_bytes(a.rows, a.cols, a.ldy);
@@ -46,14 +50,24 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a)
     for (int64_t v = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; v < vecs;
          v += static_cast<int64_t>(gridDim.y) * blockDim.x) {
         float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int j = 0; j < a.map.k; ++j) {
-            if (row[j] < 0) continue;
-            float f[8];
-            unpack8(ldg_checked(reinterpret_cast<const uint4*>(a.y + row[j] * a.ldy) + v, a.y, yb,
-                                a.dev_status), f);
+        for (int j0 = 0; j0 < k; j0 += kTogether) {
+            uint4 y[kTogether];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += weight[j] * f[i];
+            for (int j = 0; j < kTogether; ++j) {
+                const int r = row[j0 + j];
+                y[j] = make_uint4(0, 0, 0, 0);
+                if (r >= 0)
+                    y[j] = ldg_checked(reinterpret_cast<const uint4*>(a.y + r * a.ldy) + v, a.y, yb,
+                                       a.dev_status);
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                if (row[j0 + j] < 0) continue;  // adds nothing, whatever its weight
+                float f[8];
+                unpack8(y[j], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] += weight[j0 + j] * f[i];
+            }
         }
         if (F32) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + t * a.ldo) + 2 * v;
@@ -65,9 +79,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a)
     }
 }
 
-// A CTA per token: its gradient row is read for every pair (from cache after the first), the pair's
-// row of y once; each pair's dot product is a block reduction in a fixed order.  The CTAs behind the
-// tokens zero the rows without a token.
+// A CTA per token.  Its pairs are taken eight at a time: the thread's 8 columns of the gradient are
+// read once for them, the pairs' columns of y together, and the eight dot products are reduced over
+// the CTA in a fixed order.  The CTAs behind the tokens zero the rows without a token.
 template <bool F32>
 __global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs a)
 {
@@ -75,54 +89,81 @@ __global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs
     const int64_t vecs = a.cols >> 3;
     const int64_t yb = bf16_matrix_bytes(a.rows, a.cols, a.ldy);
     const int64_t db = bf16_matrix_bytes(a.rows, a.cols, a.lddy);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= a.map.tokens) {
+        // a warp looks at 32 rows at once
         const int64_t used = a.map.used_rows(a.rows);
-        for (int64_t r = blockIdx.x - a.map.tokens; r < used; r += gridDim.x - a.map.tokens) {
-            const int64_t token = a.map.row_token[r];
-            if (token >= 0 && token < a.map.tokens) continue;
-            uint4* d = reinterpret_cast<uint4*>(a.dy + r * a.lddy);
-            for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x)
-                st_checked(d + v, make_uint4(0, 0, 0, 0), a.dy, db, a.dev_status);
+        const int64_t warps = (gridDim.x - a.map.tokens) * 4;
+        for (int64_t r0 = 32 * ((blockIdx.x - a.map.tokens) * 4 + warp); r0 < used; r0 += 32 * warps) {
+            const int64_t token = a.map.row_token[r0 + lane];  // used is a multiple of 128
+            for (unsigned left = __ballot_sync(0xFFFFFFFFu, token < 0 || token >= a.map.tokens); left;
+                 left &= left - 1) {
+                uint4* d = reinterpret_cast<uint4*>(a.dy + (r0 + __ffs(left) - 1) * a.lddy);
+                for (int64_t v = lane; v < vecs; v += 32)
+                    st_checked(d + v, make_uint4(0, 0, 0, 0), a.dy, db, a.dev_status);
+            }
         }
         return;
     }
     const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j = 0; j < a.map.k; ++j) {
-        const int64_t r = a.map.pair_target(t, j, a.rows);
-        float dot = 0.0f;
-        if (r >= 0) {
-            const float w = a.weights[t * a.map.k + j];
-            const uint4* y = reinterpret_cast<const uint4*>(a.y + r * a.ldy);
-            uint4* dy = reinterpret_cast<uint4*>(a.dy + r * a.lddy);
-            for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
-                float g[8], f[8], d[8];
-                if (F32) {
-                    const float4* p = reinterpret_cast<const float4*>(
-                        static_cast<const float*>(a.dout) + t * a.ldo) + 2 * v;
-                    const float4 lo = __ldg(p), hi = __ldg(p + 1);
-                    g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w;
-                    g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
-                } else {
-                    unpack8(__ldg(reinterpret_cast<const uint4*>(
-                        static_cast<const uint16_t*>(a.dout) + t * a.ldo) + v), g);
-                }
-                unpack8(ldg_checked(y + v, a.y, yb, a.dev_status), f);
+    const int k = static_cast<int>(a.map.k);
+    __shared__ int row[kMaxK];
+    __shared__ float weight[kMaxK];
+    if (threadIdx.x < kMaxK) {
+        const int r = threadIdx.x < k ? static_cast<int>(a.map.pair_target(t, threadIdx.x, a.rows)) : -1;
+        row[threadIdx.x] = r;
+        weight[threadIdx.x] = r >= 0 ? a.weights[t * k + threadIdx.x] : 0.0f;
+    }
+    __syncthreads();
+    for (int j0 = 0; j0 < k; j0 += kTogether) {
+        float dot[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) dot[j] = 0.0f;
+        for (int64_t v = threadIdx.x; v < vecs; v += blockDim.x) {
+            uint4 y[kTogether];
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                const int r = row[j0 + j];
+                if (r >= 0)
+                    y[j] = ldg_checked(reinterpret_cast<const uint4*>(a.y + r * a.ldy) + v, a.y, yb,
+                                       a.dev_status);
+            }
+            float g[8];
+            if (F32) {
+                const float4* p = reinterpret_cast<const float4*>(
+                    static_cast<const float*>(a.dout) + t * a.ldo) + 2 * v;
+                const float4 lo = __ldg(p), hi = __ldg(p + 1);
+                g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w;
+                g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
+            } else {
+                unpack8(__ldg(reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(a.dout) + t * a.ldo) + v), g);
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                const int r = row[j0 + j];
+                if (r < 0) continue;
+                float f[8], d[8];
+                unpack8(y[j], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    dot += g[i] * f[i];
-                    d[i] = w * g[i];
+                    dot[j] += g[i] * f[i];
+                    d[i] = weight[j0 + j] * g[i];
                 }
-                st_checked(dy + v, pack8(d), a.dy, db, a.dev_status);
+                st_checked(reinterpret_cast<uint4*>(a.dy + r * a.lddy) + v, pack8(d), a.dy, db,
+                           a.dev_status);
             }
         }
 #pragma unroll
-        for (int s = 16; s; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
-        if (lane == 0) part[j][warp] = dot;
+        for (int j = 0; j < kTogether; ++j) {
+#pragma unroll
+            for (int s = 16; s; s >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], s);
+            if (lane == 0) part[j0 + j][warp] = dot[j];
+        }
     }
     __syncthreads();
-    if (threadIdx.x < a.map.k)
-        a.dweights[t * a.map.k + threadIdx.x] =
+    if (threadIdx.x < k)
+        a.dweights[t * k + threadIdx.x] =
             (part[threadIdx.x][0] + part[threadIdx.x][1]) + (part[threadIdx.x][2] + part[threadIdx.x][3]);
 }
 
