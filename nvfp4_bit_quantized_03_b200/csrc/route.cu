@@ -62,14 +62,54 @@ __device__ __forceinline__ float warp_maxf(float v)
     return v;
 }
 
-template <typename T>
-__device__ __forceinline__ float load_logit(const T* p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p)
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(uint16_t v)
 {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p) { return to_float(__ldg(p)); }
+
+// The lane's NPL values of a row of E (-inf behind its end), in loads of up to 16 bytes when the
+// rows allow them (`wide`).
+template <int NPL, typename T>
+__device__ __forceinline__ void load_values(const T* row, int lane, int E, bool wide, float (&x)[NPL])
+{
+    constexpr int BYTES = NPL * static_cast<int>(sizeof(T));
+    if (wide && (lane + 1) * NPL <= E) {
+        if constexpr (BYTES >= 16) {
+#pragma unroll
+            for (int c = 0; c < BYTES / 16; ++c) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + lane * NPL) + c);
+                if constexpr (sizeof(T) == 4) {
+                    x[4 * c] = __uint_as_float(v.x);
+                    x[4 * c + 1] = __uint_as_float(v.y);
+                    x[4 * c + 2] = __uint_as_float(v.z);
+                    x[4 * c + 3] = __uint_as_float(v.w);
+                } else {
+                    unpack8(v, x + 8 * c);
+                }
+            }
+            return;
+        } else if constexpr (BYTES == 8) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + lane * NPL));
+            if constexpr (sizeof(T) == 4) {
+                x[0] = __uint_as_float(v.x);
+                x[1] = __uint_as_float(v.y);
+            } else {
+                x[0] = bf16_lo(v.x);
+                x[1] = bf16_hi(v.x);
+                x[2] = bf16_lo(v.y);
+                x[3] = bf16_hi(v.y);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane * NPL + i;
+        x[i] = e < E ? load_logit(row + e) : -INFINITY;
+    }
 }
 
 __device__ __forceinline__ float log_sigmoid(float x)
@@ -78,14 +118,12 @@ __device__ __forceinline__ float log_sigmoid(float x)
 }
 
 // The r-th best of the warp's keys, r = 0 .. rounds - 1, best first: lane r of the result holds the
-// expert (lane * NPL + i of its owner), -1 when nothing is left.  With `gap` also the smallest
-// difference between consecutive values, up to the one after the last.
+// expert (lane * NPL + i of its owner), -1 when nothing is left.  Exact for any key.
 template <int NPL, typename Key>
-__device__ __forceinline__ int select_best(Key (&key)[NPL], int rounds, int lane, float* gap)
+__device__ __forceinline__ int select_best(Key (&key)[NPL], int rounds, int lane)
 {
     int mine = -1;
-    float before = 0.0f;
-    for (int r = 0; r < rounds + (gap ? 1 : 0); ++r) {
+    for (int r = 0; r < rounds; ++r) {
         Key best = 0;
         int at = 0;
 #pragma unroll
@@ -96,19 +134,62 @@ __device__ __forceinline__ int select_best(Key (&key)[NPL], int rounds, int lane
             }
         const Key top = warp_max(best);
         if (top == 0) break;
-        if constexpr (sizeof(Key) == 4) {
-            if (gap) {
-                const float v = key_value(top);
-                if (r > 0) *gap = fminf(*gap, before - v);
-                before = v;
-            }
-        }
         const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
         const int chosen = __shfl_sync(kAll, at, owner);
-        if (r < rounds && lane == r) mine = owner * NPL + chosen;
+        if (lane == r) mine = owner * NPL + chosen;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
             if (lane == owner && i == chosen) key[i] = 0;
+    }
+    return mine;
+}
+
+// The same, faster, on 32-bit keys whose lowest log2(NPL) bits give way to the place in the lane
+// (NPL - 1 - i, so that equal keys come in the order of their places).  Each lane sorts its keys
+// once (Batcher's odd-even merge sort); a round then compares the lanes' first ones and its owner
+// moves up.  gap: the smallest difference between the values of consecutive rounds, the one after
+// the last included, without those bits (0 for equal ones).
+template <int NPL>
+__device__ __forceinline__ void pack_and_sort(uint32_t (&key)[NPL])
+{
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        if (key[i]) key[i] = (key[i] & ~(NPL - 1u)) | static_cast<uint32_t>(NPL - 1 - i);
+#pragma unroll
+    for (int p = 1; p < NPL; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < NPL; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < NPL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t a = key[i + j], b = key[i + j + q];
+                        key[i + j] = max(a, b);
+                        key[i + j + q] = min(a, b);
+                    }
+}
+template <int NPL>
+__device__ __forceinline__ int take_best(uint32_t (&key)[NPL], int rounds, int lane, float& gap)
+{
+    constexpr uint32_t kPlace = NPL - 1u;
+    int mine = -1;
+    float before = INFINITY;
+    for (int r = 0; r <= rounds; ++r) {
+        const uint32_t first = key[0] & ~kPlace;
+        const uint32_t top = __reduce_max_sync(kAll, first);
+        if (top == 0) break;
+        const float v = key_value(top);
+        gap = fminf(gap, before - v);
+        before = v;
+        const int owner = __ffs(__ballot_sync(kAll, first == top)) - 1;
+        const int place = static_cast<int>(kPlace - (__shfl_sync(kAll, key[0], owner) & kPlace));
+        if (lane == r && r < rounds) mine = owner * NPL + place;
+        if (lane == owner) {
+#pragma unroll
+            for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
+            key[NPL - 1] = 0;
+        }
     }
     return mine;
 }
@@ -119,72 +200,126 @@ struct RouteArgs {
     int64_t ld;
     int T, E, k, groups, top_groups;
     bool sigmoid, renorm;
+    bool wide;         // logits (and bias) can be read 16 bytes at a time
+    int group_lanes;   // lanes that hold one group, a power of two; 0: groups end inside lanes
     float scale;
     int32_t* experts;
     float* weights;
     int* dev_status;
 };
 
-// Choice by scores in type F (float, or double where a float comparison is too close to call).
-// x: the lane's logits (-inf: cannot be chosen), mx their warp maximum.  values: the warp's shared
-// buffer of E group-search values.  Returns the chosen expert of lane j; close: a comparison was
-// closer than the error of F (never set for double).
-template <int NPL, typename F>
-__device__ __forceinline__ int choose(const RouteArgs& a, const float (&x)[NPL], float mx, int lane,
-                                      F* values, bool& close, bool& bad)
+// The lane's keys of the choice v = s + bias, s in FP64 or, for a float key, by the fast intrinsics.
+// bad: a value was NaN or +inf.
+template <int NPL, typename F, typename Key>
+__device__ __forceinline__ void choice_keys(const RouteArgs& a, const float (&x)[NPL], float mx,
+                                            int lane, F (&s)[NPL], Key (&key)[NPL], bool& bad)
 {
-    using Key = decltype(order_key(F(0)));
-    F s[NPL];
+    constexpr bool FAST = sizeof(F) == 4;
     F sum = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        if (sizeof(F) == 8)
-            s[i] = a.sigmoid ? F(1) / (F(1) + F(exp(-double(x[i])))) : F(exp(double(x[i]) - double(mx)));
+        if constexpr (FAST)
+            s[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : __expf(x[i] - mx);
         else
-            s[i] = a.sigmoid ? F(1) / (F(1) + F(expf(-x[i]))) : F(expf(x[i] - mx));
+            s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x[i])))
+                             : exp(static_cast<double>(x[i]) - static_cast<double>(mx));
         sum += s[i];
     }
     if (!a.sigmoid) {
-        sum = warp_sum(sum);
+        const F inv = F(1) / warp_sum(sum);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = s[i] / sum;
+        for (int i = 0; i < NPL; ++i) s[i] *= inv;
     }
-    Key key[NPL];
-    float largest = 0.0f;
+    float b[NPL];
+    if (a.bias) load_values<NPL>(a.bias, lane, a.E, a.wide, b);
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        const int e = lane * NPL + i;
         key[i] = 0;
-        if (e < a.E && x[i] > -INFINITY) {
-            if (a.bias) s[i] += F(__ldg(a.bias + e));
+        if (a.bias) s[i] += F(b[i]);
+        if (x[i] > -INFINITY) {  // false behind the last expert too
             nan |= !(s[i] < F(INFINITY));
-            if (s[i] > -F(INFINITY)) {
-                key[i] = order_key(s[i]);
-                largest = fmaxf(largest, fabsf(float(s[i])));
-            }
+            if (s[i] > -F(INFINITY)) key[i] = order_key(s[i]);
         }
     }
     bad = __any_sync(kAll, nan);
+}
+
+// Fast choice by FP32 scores.  close: some comparison was too close to call, and the choice has to
+// be made in FP64.  An FP32 score is off by at most 10 units of 2^-23 (exp by its intrinsic: 2 +
+// 1.2 |d| units at an argument d, times s; the sum of up to 512; the quotient; the bias), and the
+// keys give way up to 15 units of the value to the place: two values are told apart from 2^-18 of
+// 1 + the largest on, sums of two from twice that.
+template <int NPL>
+__device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[NPL], float mx,
+                                           int lane, bool& close, bool& bad)
+{
+    float s[NPL];
+    uint32_t key[NPL];
+    choice_keys<NPL>(a, x, mx, lane, s, key, bad);
     if (bad) return -1;
-    // An FP32 score is off by at most 5 half-steps of 2^-24 (exp 2 ulp, sum, quotient, bias), of a
-    // value no larger than 1 + largest; a softmax sum adds log2(32 NPL) more.  Differences below
-    // 2^-19 of that are decided in FP64.
-    const float tol = sizeof(F) == 8 ? 0.0f : 0x1p-19f * (1.0f + warp_maxf(largest));
+    float largest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        if (key[i]) largest = fmaxf(largest, fabsf(s[i]));
+    largest = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(largest)));
+    pack_and_sort<NPL>(key);
     float gap = INFINITY;
+    if (a.groups > 1) {
+        // the group's two best: the lane's own, then across the group's lanes
+        uint32_t m1 = key[0], m2 = NPL > 1 ? key[NPL > 1 ? 1 : 0] : 0u;
+        for (int d = 1; d < a.group_lanes; d <<= 1) {
+            const uint32_t o1 = __shfl_xor_sync(kAll, m1, d), o2 = __shfl_xor_sync(kAll, m2, d);
+            m2 = max(min(m1, o1), max(m2, o2));
+            m1 = max(m1, o1);
+        }
+        constexpr uint32_t kPlace = NPL - 1u;
+        float score = m1 ? key_value(m1 & ~kPlace) : -INFINITY;
+        if (m2) score += key_value(m2 & ~kPlace);
+        // rank of this lane's group among all
+        const int mine = lane / a.group_lanes;
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const float o = __shfl_sync(kAll, score, g * a.group_lanes);
+            rank += (o > score || (o == score && g < mine)) ? 1 : 0;
+        }
+        const bool kept = mine < a.groups && rank < a.top_groups;
+        const uint32_t okey = score > -INFINITY ? order_key(score) : 0u;
+        const uint32_t low = __reduce_min_sync(kAll, kept && okey ? okey : 0xFFFFFFFFu);
+        const uint32_t high = __reduce_max_sync(kAll, kept || mine >= a.groups ? 0u : okey);
+        if (high && low != 0xFFFFFFFFu) gap = 0.5f * (key_value(low) - key_value(high));
+        if (!kept) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) key[i] = 0;
+        }
+    }
+    const int mine = take_best<NPL>(key, a.k, lane, gap);
+    close = gap < 0x1p-18f * (1.0f + largest);
+    return mine;
+}
+
+// The choice in FP64, for groups of any size.  values: the warp's shared buffer of E.
+template <int NPL>
+__device__ __noinline__ int choose_exact(const RouteArgs& a, const float (&x)[NPL], float mx,
+                                         int lane, double* values, bool& bad)
+{
+    double s[NPL];
+    unsigned long long key[NPL];
+    choice_keys<NPL>(a, x, mx, lane, s, key, bad);
+    if (bad) return -1;
     if (a.groups > 1) {
         const int size = a.E / a.groups;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = lane * NPL + i;
-            if (e < a.E) values[e] = key[i] ? s[i] : -F(INFINITY);
+            if (e < a.E) values[e] = key[i] ? s[i] : -INFINITY;
         }
         __syncwarp();
-        Key gkey[1] = {0};
+        unsigned long long gkey[1] = {0};
         if (lane < a.groups) {
-            F m1 = -F(INFINITY), m2 = -F(INFINITY);
+            double m1 = -INFINITY, m2 = -INFINITY;
             for (int i = 0; i < size; ++i) {
-                const F v = values[lane * size + (i + lane) % size];
+                const double v = values[lane * size + i];
                 if (v > m1) {
                     m2 = m1;
                     m1 = v;
@@ -192,13 +327,10 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const float (&x)[NPL],
                     m2 = v;
                 }
             }
-            if (m1 > -F(INFINITY)) gkey[0] = order_key(m2 > -F(INFINITY) ? m1 + m2 : m1);
+            if (m1 > -INFINITY) gkey[0] = order_key(m2 > -INFINITY ? m1 + m2 : m1);
         }
         __syncwarp();
-        // sums of two have twice the error
-        float ggap = INFINITY;
-        const int g = select_best<1>(gkey, a.top_groups, lane, sizeof(F) == 8 ? nullptr : &ggap);
-        gap = 0.5f * ggap;
+        const int g = select_best<1>(gkey, a.top_groups, lane);
         const unsigned kept = __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -206,9 +338,7 @@ __device__ __forceinline__ int choose(const RouteArgs& a, const float (&x)[NPL],
             if (e < a.E && !((kept >> (e / size)) & 1u)) key[i] = 0;
         }
     }
-    const int mine = select_best<NPL>(key, a.k, lane, sizeof(F) == 8 ? nullptr : &gap);
-    close = sizeof(F) == 4 && gap < tol;
-    return mine;
+    return select_best<NPL>(key, a.k, lane);
 }
 
 // A warp per token; lane l holds the logits of experts l * NPL .. l * NPL + NPL - 1.
@@ -221,33 +351,38 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
     if (t >= a.T) return;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     float x[NPL];
+    load_values<NPL>(row, lane, a.E, a.wide, x);
     bool bad = false;
-    float mx = -INFINITY;
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        const int e = lane * NPL + i;
-        x[i] = e < a.E ? load_logit(row + e) : -INFINITY;
         bad |= !(x[i] < INFINITY);
-        mx = fmaxf(mx, x[i]);
+        top = max(top, order_key(x[i]));
     }
     bad = __any_sync(kAll, bad);
-    mx = warp_maxf(mx);
+    const float mx = key_value(__reduce_max_sync(kAll, top));
     int expert = -1;
     if (!bad && mx > -INFINITY) {
         if (!a.bias && a.groups == 1) {
-            // scores rise with the logits: the logits themselves are compared, exactly
+            // scores rise with the logits: the logits themselves are compared.  The packed keys
+            // hold a bf16 exactly; FP32 logits that differ in their last bits only are told apart
+            // by the whole keys.
             uint32_t key[NPL];
 #pragma unroll
             for (int i = 0; i < NPL; ++i) key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
-            expert = select_best<NPL>(key, a.k, lane, nullptr);
-        } else {
-            double* values = group_values + warp * a.E;
-            bool close = false;
-            expert = choose<NPL, float>(a, x, mx, lane, reinterpret_cast<float*>(values), close, bad);
-            if (close && !bad) {
-                bool never;
-                expert = choose<NPL, double>(a, x, mx, lane, values, never, bad);
+            pack_and_sort<NPL>(key);
+            float gap = INFINITY;
+            expert = take_best<NPL>(key, a.k, lane, gap);
+            if (sizeof(T) == 4 && !(gap > 0.0f)) {
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
+                expert = select_best<NPL>(key, a.k, lane);
             }
+        } else {
+            bool close = a.group_lanes == 0;
+            if (!close) expert = choose_fast<NPL>(a, x, mx, lane, close, bad);
+            if (close && !bad)
+                expert = choose_exact<NPL>(a, x, mx, lane, group_values + warp * a.E, bad);
         }
     }
     if (bad) {
@@ -287,6 +422,7 @@ struct RouteBackwardArgs {
     const float* dweights;
     int T, E, k;
     bool sigmoid, renorm;
+    bool wide;  // logits and dlogits can be read and written 16 bytes at a time
     float scale;
     void* dlogits;
     int64_t ldd;
@@ -339,13 +475,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
             if (chosen) d = g * rest * (1.0f / (1.0f + expf(-l)));
         } else {
             float x[NPL];
+            load_values<NPL>(row, lane, a.E, a.wide, x);
             float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const int e = lane * NPL + i;
-                x[i] = e < a.E ? load_logit(row + e) : -INFINITY;
-                mx = fmaxf(mx, x[i]);
-            }
+            for (int i = 0; i < NPL; ++i) mx = fmaxf(mx, x[i]);
             mx = warp_maxf(mx);
             float sum = 0.0f;
 #pragma unroll
@@ -370,6 +503,27 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
         }
     }
     T* drow = static_cast<T*>(a.dlogits) + t * a.ldd;
+    if constexpr (NPL * sizeof(T) >= 16) {
+        if (a.wide && (lane + 1) * NPL <= a.E) {
+            constexpr int PER = 16 / sizeof(T);
+#pragma unroll
+            for (int c = 0; c < NPL / PER; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    if constexpr (sizeof(T) == 4) {
+                        w[h] = __float_as_uint(out[PER * c + h]);
+                    } else {
+                        const __nv_bfloat162 v =
+                            __floats2bfloat162_rn(out[PER * c + 2 * h], out[PER * c + 2 * h + 1]);
+                        w[h] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                }
+                reinterpret_cast<uint4*>(drow + lane * NPL)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = lane * NPL + i;
@@ -425,13 +579,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs
 
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs a)
 {
-    __shared__ int next[kPlanWarps][kMaxExperts];  // pairs of each warp, then its next row
+    extern __shared__ int next[];  // [kPlanWarps][E] pairs of each warp, then its next row
     __shared__ int total[kMaxExperts], before[kMaxExperts], start[kMaxExperts + 1];
     __shared__ int warp_sums[kPlanWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = blockIdx.x, chunks = gridDim.x;
-    for (int i = threadIdx.x; i < kPlanWarps * kMaxExperts; i += kPlanThreads)
-        next[i / kMaxExperts][i % kMaxExperts] = 0;
+    int* warp_next = next + warp * a.E;
+    for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) next[i] = 0;
     __syncthreads();
     // the warp's share of the chunk, in order
     constexpr int kPerWarp = kPlanPairs / kPlanWarps;
@@ -441,19 +595,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     for (int i = 0; i < kPerWarp / 32; ++i) {
         const int64_t p = first + 32 * i + lane;
         mine[i] = p < a.pairs ? pair_expert(a, p) : -1;
-        if (mine[i] >= 0) atomicAdd(&next[warp][mine[i]], 1);
+        if (mine[i] >= 0) atomicAdd(&warp_next[mine[i]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
         int sum = 0, prior = 0;
         if (a.counts) {
+#pragma unroll 8
             for (int c = 0; c < chunks; ++c) {
                 const int n = a.counts[static_cast<int64_t>(c) * a.E + e];
                 if (c < chunk) prior += n;
                 sum += n;
             }
         } else {
-            for (int w = 0; w < kPlanWarps; ++w) sum += next[w][e];
+            for (int w = 0; w < kPlanWarps; ++w) sum += next[w * a.E + e];
         }
         total[e] = sum;
         before[e] = prior;
@@ -491,8 +646,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
         int row = start[e] + before[e];
         for (int w = 0; w < kPlanWarps; ++w) {
-            const int n = next[w][e];
-            next[w][e] = row;
+            const int n = next[w * a.E + e];
+            next[w * a.E + e] = row;
             row += n;
         }
     }
@@ -501,11 +656,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
 #pragma unroll
     for (int i = 0; i < kPerWarp / 32; ++i) {
         const int64_t p = first + 32 * i + lane;
+        if (first + 32 * i >= a.pairs) break;  // the whole warp
         const unsigned same = __match_any_sync(kAll, mine[i]);
         int row = -1;
-        if (mine[i] >= 0) row = next[warp][mine[i]] + __popc(same & ((1u << lane) - 1u));
+        if (mine[i] >= 0) row = warp_next[mine[i]] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
-        if (mine[i] >= 0 && lane == 31 - __clz(same)) next[warp][mine[i]] = row + 1;
+        if (mine[i] >= 0 && lane == 31 - __clz(same)) warp_next[mine[i]] = row + 1;
         __syncwarp();
         if (p < a.pairs) {
             a.pair_row[p] = row;
@@ -526,7 +682,7 @@ cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s)
 {
     const int warps = kRouteThreads / 32;
     const int grid = (a.T + warps - 1) / warps;
-    const size_t smem = a.groups > 1 ? sizeof(double) * warps * a.E : 0;
+    const size_t smem = a.groups > 1 ? sizeof(double) * warps * a.E : 0;  // choose_exact's
     if (a.E <= 32)       route_kernel<1, T><<<grid, kRouteThreads, smem, s>>>(a);
     else if (a.E <= 64)  route_kernel<2, T><<<grid, kRouteThreads, smem, s>>>(a);
     else if (a.E <= 128) route_kernel<4, T><<<grid, kRouteThreads, smem, s>>>(a);
@@ -548,6 +704,15 @@ cudaError_t launch_route_backward_t(const RouteBackwardArgs& a, cudaStream_t s)
     return cudaGetLastError();
 }
 
+// Rows that start on 16-byte boundaries.
+bool rows_aligned(const void* p, int64_t ld, int64_t esize)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * esize % 16 == 0;
+}
+
+// Experts per lane of the kernels' variants.
+int per_lane(int64_t E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : 16; }
+
 }  // namespace
 
 cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int64_t E, int64_t ld,
@@ -566,6 +731,9 @@ cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int64_t E, in
     a.top_groups = top_groups;
     a.sigmoid = sigmoid;
     a.renorm = renorm;
+    a.wide = rows_aligned(logits, ld, bf16 ? 2 : 4) && (!bias || rows_aligned(bias, 0, 4));
+    const int npl = per_lane(E), size = static_cast<int>(E / groups), lanes = size / npl;
+    a.group_lanes = groups == 1 ? 1 : (size % npl == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0);
     a.scale = scale;
     a.experts = experts;
     a.weights = weights;
@@ -588,6 +756,7 @@ cudaError_t launch_route_backward(const void* logits, bool bf16, int64_t T, int6
     a.k = k;
     a.sigmoid = sigmoid;
     a.renorm = renorm;
+    a.wide = rows_aligned(logits, ld, bf16 ? 2 : 4) && rows_aligned(dlogits, ldd, bf16 ? 2 : 4);
     a.scale = scale;
     a.dlogits = dlogits;
     a.ldd = ldd;
@@ -616,7 +785,7 @@ cudaError_t launch_plan(const int32_t* experts, int64_t pairs, int k, int E, int
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    plan_place_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
+    plan_place_kernel<<<chunks, kPlanThreads, sizeof(int) * kPlanWarps * E, s>>>(a);
     return cudaGetLastError();
 }
 
