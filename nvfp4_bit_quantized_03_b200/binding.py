@@ -465,12 +465,23 @@ def experts_workspace_bytes(plan, I, O):
     return lib().nvfp4_experts_workspace_bytes(plan.tokens, plan.k, plan.experts, plan.rows, I, O)
 
 
-def _on_current_device(what, *tensors):
-    """The calls run on the current device: its stream, its kernels.  Refuses tensors elsewhere."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else -1
+def _queue(what, stream, *tensors):
+    """The handle of the stream a call goes to (None: the current one).  The calls run on the current
+    device, with its kernels: tensors elsewhere are refused."""
+    here = -1
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != here):
+        if t is None:
+            continue
+        d = t.get_device()
+        if d >= 0 and here < 0:
+            here = torch.cuda.current_device()
+        if d < 0 or d != here:
             raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _matrix(what, t, dtypes, rows, cols):
@@ -499,9 +510,12 @@ _F32_BF16 = (torch.float32, torch.bfloat16)
 _BF16 = (torch.bfloat16,)
 
 
+_no_stream = contextlib.nullcontext()
+
+
 def _allocating(stream):
     """Buffers made for a call belong to the stream that uses them."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _no_stream if stream is None else torch.cuda.stream(stream)
 
 
 class ExpertPlan:
@@ -516,6 +530,9 @@ class ExpertPlan:
         self.offsets, self.pair_row, self.row_token = offsets, pair_row, row_token
         self.tokens, self.k = pair_row.shape
         self.experts, self.rows = offsets.shape[0] - 1, row_token.shape[0]
+        self._struct = PlanStruct(offsets.data_ptr(), pair_row.data_ptr(), row_token.data_ptr(),
+                                  self.tokens, self.k, self.experts, self.rows)
+        self.ref = ctypes.byref(self._struct)  # what the C calls take
 
     @classmethod
     def empty(cls, tokens, k, experts, rows=None, device="cuda"):
@@ -527,10 +544,6 @@ class ExpertPlan:
         def ints(*shape):
             return torch.empty(shape, dtype=torch.int32, device=device)
         return cls(ints(experts + 1), ints(tokens, k), ints(rows))
-
-    def struct(self):
-        return PlanStruct(self.offsets.data_ptr(), self.pair_row.data_ptr(),
-                          self.row_token.data_ptr(), self.tokens, self.k, self.experts, self.rows)
 
 
 def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=True, scale=1.0,
@@ -547,11 +560,11 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=Tr
             weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
     _dense("experts", experts, torch.int32, (T, k))
     _dense("weights", weights, torch.float32, (T, k))
-    _on_current_device("nvfp4_route", logits, bias, experts, weights)
-    _check(lib().nvfp4_route(_ptr(logits), _dtype_code(logits.dtype), T, E, _row_stride(logits),
-                             _ptr(bias), int(bool(sigmoid)), groups, top_groups, k, int(bool(renorm)),
-                             scale, _ptr(experts), _ptr(weights), _ptr(dev_status),
-                             _stream(stream)), "nvfp4_route")
+    queue = _queue("nvfp4_route", stream, logits, bias, experts, weights)
+    _check(lib().nvfp4_route(_address(logits), _dtype_code(logits.dtype), T, E, _row_stride(logits),
+                             _address(bias), int(bool(sigmoid)), groups, top_groups, k, int(bool(renorm)),
+                             scale, _address(experts), _address(weights), _address(dev_status),
+                             queue), "nvfp4_route")
     return experts, weights
 
 
@@ -567,12 +580,12 @@ def route_backward(logits, experts, dweights, sigmoid=False, renorm=True, scale=
         with _allocating(stream):
             dlogits = _poisoned(torch.empty((T, E), dtype=logits.dtype, device=logits.device))
     _matrix("dlogits", dlogits, (logits.dtype,), T, E)
-    _on_current_device("nvfp4_route_backward", logits, experts, dweights, dlogits)
-    _check(lib().nvfp4_route_backward(_ptr(logits), _dtype_code(logits.dtype), T, E,
-                                      _row_stride(logits), _ptr(experts), _ptr(dweights),
+    queue = _queue("nvfp4_route_backward", stream, logits, experts, dweights, dlogits)
+    _check(lib().nvfp4_route_backward(_address(logits), _dtype_code(logits.dtype), T, E,
+                                      _row_stride(logits), _address(experts), _address(dweights),
                                       int(bool(sigmoid)), k, int(bool(renorm)), scale,
-                                      _ptr(dlogits), _row_stride(dlogits), _ptr(dev_status),
-                                      _stream(stream)), "nvfp4_route_backward")
+                                      _address(dlogits), _row_stride(dlogits), _address(dev_status),
+                                      queue), "nvfp4_route_backward")
     return dlogits
 
 
@@ -588,9 +601,9 @@ def expert_plan(experts, n_experts, plan=None, workspace=None, dev_status=None, 
                                    experts.device)
     if (plan.tokens, plan.k, plan.experts) != (T, k, n_experts):
         raise ValueError(f"plan is for {plan.tokens} tokens, {plan.k} of {plan.experts} experts")
-    _on_current_device("nvfp4_plan_experts", experts, plan.offsets, plan.pair_row, plan.row_token)
-    _check(lib().nvfp4_plan_experts(_ptr(experts), ctypes.byref(plan.struct()), _ptr(workspace),
-                                    _ptr(dev_status), _stream(stream)), "nvfp4_plan_experts")
+    queue = _queue("nvfp4_plan_experts", stream, experts, plan.offsets, plan.pair_row, plan.row_token)
+    _check(lib().nvfp4_plan_experts(_address(experts), plan.ref, _address(workspace),
+                                    _address(dev_status), queue), "nvfp4_plan_experts")
     return plan
 
 
@@ -611,14 +624,14 @@ def quantize_grouped(x, plan, flags, sign_mask=0, seed=0, offset=0, out_row=None
             out_col = QuantizedTensor(cols, plan.rows, x.device)
         if workspace is None:
             workspace = _workspace(workspace_bytes(plan.rows, cols, flags), x.device)
-    _on_current_device("nvfp4_quantize_grouped", x, plan.offsets)
+    queue = _queue("nvfp4_quantize_grouped", stream, x, plan.offsets)
     op_r = out_row.operand() if out_row is not None else None
     op_c = out_col.operand() if out_col is not None else None
     _check(lib().nvfp4_quantize_grouped(
-        _ptr(x), cols, _row_stride(x), ctypes.byref(plan.struct()), sign_mask, flags, seed, offset,
+        _address(x), cols, _row_stride(x), plan.ref, sign_mask, flags, seed, offset,
         ctypes.byref(op_r) if op_r is not None else None,
-        ctypes.byref(op_c) if op_c is not None else None, _ptr(workspace), _ptr(dev_status),
-        _stream(stream)), "nvfp4_quantize_grouped")
+        ctypes.byref(op_c) if op_c is not None else None, _address(workspace), _address(dev_status),
+        queue), "nvfp4_quantize_grouped")
     return out_row, out_col
 
 
@@ -636,22 +649,22 @@ def gemm_grouped(A, W, plan, out=None, out_dtype=torch.bfloat16, dev_status=None
     E = plan.experts
     N = W.rows // E if W.cols == A.cols and W.rows % E == 0 else W.rows
     out = _grouped_out("out", out, plan.rows, N, out_dtype, A.codes.device, stream)
-    _on_current_device("nvfp4_gemm_grouped", A.codes, W.codes, plan.offsets, out)
+    queue = _queue("nvfp4_gemm_grouped", stream, A.codes, W.codes, plan.offsets, out)
     oa, ob = A.operand(), W.operand()
-    _check(lib().nvfp4_gemm_grouped(ctypes.byref(oa), ctypes.byref(ob), ctypes.byref(plan.struct()),
-                                    _ptr(out), _dtype_code(out.dtype), _row_stride(out),
-                                    _ptr(dev_status), _stream(stream)), "nvfp4_gemm_grouped")
+    _check(lib().nvfp4_gemm_grouped(ctypes.byref(oa), ctypes.byref(ob), plan.ref,
+                                    _address(out), _dtype_code(out.dtype), _row_stride(out),
+                                    _address(dev_status), queue), "nvfp4_gemm_grouped")
     return out
 
 
 def gemm_grouped_k(A, B, plan, out=None, out_dtype=torch.float32, dev_status=None, stream=None):
     """nvfp4_gemm_grouped_k: D_e = A . B^T over expert e's rows, [(E * A.rows) x B.rows]."""
     out = _grouped_out("out", out, plan.experts * A.rows, B.rows, out_dtype, A.codes.device, stream)
-    _on_current_device("nvfp4_gemm_grouped_k", A.codes, B.codes, plan.offsets, out)
+    queue = _queue("nvfp4_gemm_grouped_k", stream, A.codes, B.codes, plan.offsets, out)
     oa, ob = A.operand(), B.operand()
     _check(lib().nvfp4_gemm_grouped_k(ctypes.byref(oa), ctypes.byref(ob),
-                                      ctypes.byref(plan.struct()), _ptr(out), _dtype_code(out.dtype),
-                                      _row_stride(out), _ptr(dev_status), _stream(stream)),
+                                      plan.ref, _address(out), _dtype_code(out.dtype),
+                                      _row_stride(out), _address(dev_status), queue),
            "nvfp4_gemm_grouped_k")
     return out
 
@@ -673,12 +686,12 @@ def experts_fprop(X, W, plan, gather=True, out=None, out_dtype=torch.bfloat16, w
     I, O = W.cols, W.rows // plan.experts
     out = _grouped_out("out", out, plan.rows, O, out_dtype, X.device, stream)
     workspace = _experts_workspace(workspace, plan, I, O, X.device, stream)
-    _on_current_device("nvfp4_experts_fprop", X, W.codes, plan.offsets, out, workspace)
+    queue = _queue("nvfp4_experts_fprop", stream, X, W.codes, plan.offsets, out, workspace)
     op = W.operand()
-    _check(lib().nvfp4_experts_fprop(_ptr(X), _row_stride(X), int(bool(gather)), ctypes.byref(op),
-                                     ctypes.byref(plan.struct()), I, O, _ptr(out),
-                                     _dtype_code(out.dtype), _row_stride(out), _ptr(workspace),
-                                     _ptr(dev_status), _stream(stream)), "nvfp4_experts_fprop")
+    _check(lib().nvfp4_experts_fprop(_address(X), _row_stride(X), int(bool(gather)), ctypes.byref(op),
+                                     plan.ref, I, O, _address(out),
+                                     _dtype_code(out.dtype), _row_stride(out), _address(workspace),
+                                     _address(dev_status), queue), "nvfp4_experts_fprop")
     return out
 
 
@@ -690,12 +703,12 @@ def experts_dgrad(dY, Wt, plan, seed, offset, out=None, out_dtype=torch.bfloat16
     _matrix("dY", dY, _BF16, plan.rows, O)
     out = _grouped_out("out", out, plan.rows, I, out_dtype, dY.device, stream)
     workspace = _experts_workspace(workspace, plan, I, O, dY.device, stream)
-    _on_current_device("nvfp4_experts_dgrad", dY, Wt.codes, plan.offsets, out, workspace)
+    queue = _queue("nvfp4_experts_dgrad", stream, dY, Wt.codes, plan.offsets, out, workspace)
     op = Wt.operand()
-    _check(lib().nvfp4_experts_dgrad(_ptr(dY), _row_stride(dY), ctypes.byref(op),
-                                     ctypes.byref(plan.struct()), I, O, seed, offset, _ptr(out),
-                                     _dtype_code(out.dtype), _row_stride(out), _ptr(workspace),
-                                     _ptr(dev_status), _stream(stream)), "nvfp4_experts_dgrad")
+    _check(lib().nvfp4_experts_dgrad(_address(dY), _row_stride(dY), ctypes.byref(op),
+                                     plan.ref, I, O, seed, offset, _address(out),
+                                     _dtype_code(out.dtype), _row_stride(out), _address(workspace),
+                                     _address(dev_status), queue), "nvfp4_experts_dgrad")
     return out
 
 
@@ -708,12 +721,12 @@ def experts_wgrad(dY, X, plan, sign_mask, seed, offset, gather=True, out=None,
     I, O = X.shape[1], dY.shape[1]
     out = _grouped_out("out", out, plan.experts * O, I, out_dtype, dY.device, stream)
     workspace = _experts_workspace(workspace, plan, I, O, dY.device, stream)
-    _on_current_device("nvfp4_experts_wgrad", dY, X, plan.offsets, out, workspace)
-    _check(lib().nvfp4_experts_wgrad(_ptr(dY), _row_stride(dY), _ptr(X), _row_stride(X),
-                                     int(bool(gather)), ctypes.byref(plan.struct()), I, O, sign_mask,
-                                     seed, offset, _ptr(out), _dtype_code(out.dtype),
-                                     _row_stride(out), _ptr(workspace), _ptr(dev_status),
-                                     _stream(stream)), "nvfp4_experts_wgrad")
+    queue = _queue("nvfp4_experts_wgrad", stream, dY, X, plan.offsets, out, workspace)
+    _check(lib().nvfp4_experts_wgrad(_address(dY), _row_stride(dY), _address(X), _row_stride(X),
+                                     int(bool(gather)), plan.ref, I, O, sign_mask,
+                                     seed, offset, _address(out), _dtype_code(out.dtype),
+                                     _row_stride(out), _address(workspace), _address(dev_status),
+                                     queue), "nvfp4_experts_wgrad")
     return out
 
 
@@ -723,10 +736,10 @@ def combine(Y, plan, weights=None, out=None, out_dtype=torch.bfloat16, dev_statu
     if weights is not None:
         _dense("weights", weights, torch.float32, (plan.tokens, plan.k))
     out = _grouped_out("out", out, plan.tokens, Y.shape[1], out_dtype, Y.device, stream)
-    _on_current_device("nvfp4_combine", Y, plan.pair_row, weights, out)
-    _check(lib().nvfp4_combine(_ptr(Y), Y.shape[1], _row_stride(Y), ctypes.byref(plan.struct()),
-                               _ptr(weights), _ptr(out), _dtype_code(out.dtype), _row_stride(out),
-                               _ptr(dev_status), _stream(stream)), "nvfp4_combine")
+    queue = _queue("nvfp4_combine", stream, Y, plan.pair_row, weights, out)
+    _check(lib().nvfp4_combine(_address(Y), Y.shape[1], _row_stride(Y), plan.ref,
+                               _address(weights), _address(out), _dtype_code(out.dtype), _row_stride(out),
+                               _address(dev_status), queue), "nvfp4_combine")
     return out
 
 
@@ -744,9 +757,9 @@ def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=
                                              device=Y.device))
     _matrix("dy", dy, _BF16, plan.rows, cols)
     _dense("dweights", dweights, torch.float32, (plan.tokens, plan.k))
-    _on_current_device("nvfp4_combine_backward", dout, Y, plan.pair_row, weights, dy, dweights)
-    _check(lib().nvfp4_combine_backward(_ptr(dout), _dtype_code(dout.dtype), _row_stride(dout),
-                                        _ptr(Y), cols, _row_stride(Y), ctypes.byref(plan.struct()),
-                                        _ptr(weights), _ptr(dy), _row_stride(dy), _ptr(dweights),
-                                        _ptr(dev_status), _stream(stream)), "nvfp4_combine_backward")
+    queue = _queue("nvfp4_combine_backward", stream, dout, Y, plan.pair_row, weights, dy, dweights)
+    _check(lib().nvfp4_combine_backward(_address(dout), _dtype_code(dout.dtype), _row_stride(dout),
+                                        _address(Y), cols, _row_stride(Y), plan.ref,
+                                        _address(weights), _address(dy), _row_stride(dy), _address(dweights),
+                                        _address(dev_status), queue), "nvfp4_combine_backward")
     return dy, dweights

@@ -197,7 +197,7 @@ nvfp4_status nvfp4_quantize_grouped(const void* x_bf16, int64_t cols, int64_t ld
     if (given) {
         a.src.amax_given = want_row ? out_row->amax : nullptr;
         a.src_col.amax_given = want_col ? out_col->amax : nullptr;
-    } else {
+    } else if (want_col || !grouped_amax_is_small(cols, a.map)) {
         // [RHT partials][plain partials], as in nvfp4_quantize_row_rht
         uint32_t* rht = static_cast<uint32_t*>(workspace);
         uint32_t* plain = rht + kMaxPartials;
@@ -231,9 +231,9 @@ nvfp4_status nvfp4_quantize_grouped(const void* x_bf16, int64_t cols, int64_t ld
     return from_cuda(launch_quant_grouped_tile(a, want_row, sr, sms, s));
 }
 
-nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* A, const nvfp4_operand* B,
-                                const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
-                                int* dev_status, void* stream)
+static nvfp4_status gemm_by_rows(const nvfp4_operand* A, const nvfp4_operand* B,
+                                 const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
+                                 bool after_quantizer, int* dev_status, void* stream)
 {
     nvfp4_status st = check_plan(plan);
     if (st != NVFP4_OK) return st;
@@ -264,15 +264,16 @@ nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* A, const nvfp4_operand* B,
     g.ldd = ldd;
     g.out_bf16 = d_dtype == NVFP4_OUT_BF16;
     g.dev_status = dev_status;
+    g.after_quantizer = after_quantizer;
     if (plan->rows / 128 * ((g.N + 255) / 256) >= kMaxDim) return NVFP4_ERR_SHAPE;
     int sms = 0;
     if ((st = current_device(&sms)) != NVFP4_OK) return st;
     return from_cuda(launch_gemm_grouped(g, sms, static_cast<cudaStream_t>(stream)));
 }
 
-nvfp4_status nvfp4_gemm_grouped_k(const nvfp4_operand* A, const nvfp4_operand* B,
-                                  const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
-                                  int* dev_status, void* stream)
+static nvfp4_status gemm_by_k(const nvfp4_operand* A, const nvfp4_operand* B,
+                              const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
+                              bool after_quantizer, int* dev_status, void* stream)
 {
     nvfp4_status st = check_plan(plan);
     if (st != NVFP4_OK) return st;
@@ -294,10 +295,25 @@ nvfp4_status nvfp4_gemm_grouped_k(const nvfp4_operand* A, const nvfp4_operand* B
     g.ldd = ldd;
     g.out_bf16 = d_dtype == NVFP4_OUT_BF16;
     g.dev_status = dev_status;
+    g.after_quantizer = after_quantizer;
     if (E * ((g.M + 255) / 256) * ((g.N + 255) / 256) >= kMaxDim) return NVFP4_ERR_SHAPE;
     int sms = 0;
     if ((st = current_device(&sms)) != NVFP4_OK) return st;
     return from_cuda(launch_gemm_grouped(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* A, const nvfp4_operand* B,
+                                const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
+                                int* dev_status, void* stream)
+{
+    return gemm_by_rows(A, B, plan, D, d_dtype, ldd, false, dev_status, stream);
+}
+
+nvfp4_status nvfp4_gemm_grouped_k(const nvfp4_operand* A, const nvfp4_operand* B,
+                                  const nvfp4_expert_plan* plan, void* D, int d_dtype, int64_t ldd,
+                                  int* dev_status, void* stream)
+{
+    return gemm_by_k(A, B, plan, D, d_dtype, ldd, false, dev_status, stream);
 }
 
 size_t nvfp4_experts_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t rows, int64_t I,
@@ -345,7 +361,7 @@ nvfp4_status nvfp4_experts_fprop(const void* X, int64_t ldx, int gather, const n
     if ((st = nvfp4_quantize_grouped(X, I, ldx, plan, 0, NVFP4_ROWWISE | (gather ? NVFP4_GATHER : 0),
                                      0, 0, &a, nullptr, c.at, dev_status, stream)) != NVFP4_OK)
         return st;
-    return nvfp4_gemm_grouped(&a, W, plan, Y, y_dtype, ldy, dev_status, stream);
+    return gemm_by_rows(&a, W, plan, Y, y_dtype, ldy, true, dev_status, stream);
 }
 
 nvfp4_status nvfp4_experts_dgrad(const void* dY, int64_t lddy, const nvfp4_operand* Wt,
@@ -362,7 +378,7 @@ nvfp4_status nvfp4_experts_dgrad(const void* dY, int64_t lddy, const nvfp4_opera
     if ((st = nvfp4_quantize_grouped(dY, O, lddy, plan, 0, NVFP4_ROWWISE | NVFP4_SR, seed, offset, &a,
                                      nullptr, c.at, dev_status, stream)) != NVFP4_OK)
         return st;
-    return nvfp4_gemm_grouped(&a, Wt, plan, dX, dx_dtype, lddx, dev_status, stream);
+    return gemm_by_rows(&a, Wt, plan, dX, dx_dtype, lddx, true, dev_status, stream);
 }
 
 nvfp4_status nvfp4_experts_wgrad(const void* dY, int64_t lddy, const void* X, int64_t ldx, int gather,
@@ -384,7 +400,7 @@ nvfp4_status nvfp4_experts_wgrad(const void* dY, int64_t lddy, const void* X, in
                                      NVFP4_COLWISE | (gather ? NVFP4_GATHER : 0), 0, 0, nullptr, &b,
                                      c.at, dev_status, stream)) != NVFP4_OK)
         return st;
-    return nvfp4_gemm_grouped_k(&a, &b, plan, dW, dw_dtype, lddw, dev_status, stream);
+    return gemm_by_k(&a, &b, plan, dW, dw_dtype, lddw, true, dev_status, stream);
 }
 
 nvfp4_status nvfp4_combine(const void* Y_bf16, int64_t cols, int64_t ldy,

@@ -225,18 +225,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         uint32_t phase = 0;
         uint32_t fills = 0;  // stages filled so far
         bool ok = true;
+        auto load_b = [&](const Tile& c, int kb, uint32_t st, uint32_t full) {
+            tma_load_2d(st + A_BYTES, &tmap_b, c.b_k / 2 + kb * (BK / 2),
+                        c.b_row + static_cast<int>(rank) * B_ROWS, full);
+            tma_load_3d(st + A_BYTES + B_BYTES + SFA_BYTES, &tmap_sfb, 0,
+                        c.b_k / MMA_K + kb * (BK / MMA_K), c.b_row / CTA_M, full);
+        };
+        // By rows the weights do not come from the kernel ahead: the ring is filled with them while
+        // it ends.
+        uint32_t ahead = 0;
+        if (!BY_K && !kBoundsCheck) {
+            for (int t = cluster; t < total && ahead < STAGES; t += clusters) {
+                const Tile c = sch.tile<BY_K>(t);
+                for (int kb = 0; kb < c.k_blocks() && ahead < STAGES; ++kb, ++ahead) {
+                    const uint32_t full = bar(BAR_FULL + ahead);
+                    mbar_expect_tx(full, STAGE_BYTES);
+                    load_b(c, kb, smem_u32(smem + ahead * STAGE_BYTES), full);
+                }
+            }
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         for (int t = cluster; t < total && ok; t += clusters) {
             const Tile c = sch.tile<BY_K>(t);
-            const int ya = c.a_row + static_cast<int>(rank) * CTA_M;   // this CTA's A and B rows
-            const int yb = c.b_row + static_cast<int>(rank) * B_ROWS;
+            const int ya = c.a_row + static_cast<int>(rank) * CTA_M;  // this CTA's A rows
             for (int kb = 0; kb < c.k_blocks(); ++kb) {
                 if (!wait_bounded(bar(BAR_EMPTY + stage), phase ^ 1, abort_flag, p.dev_status)) {
                     ok = false;
                     break;
                 }
-                const int xa = c.a_k / 2 + kb * (BK / 2), xb = c.b_k / 2 + kb * (BK / 2);
+                const int xa = c.a_k / 2 + kb * (BK / 2);
                 if (kBoundsCheck && !(tma_box_start_ok(xa, ya, 1, p.dev_status) &&
-                                      tma_box_start_ok(xb, yb, 1, p.dev_status))) {
+                                      tma_box_start_ok(c.b_k / 2 + kb * (BK / 2), c.b_row, 1,
+                                                       p.dev_status))) {
                     // no copy for this stage: the roles waiting for it stop at the abort flag
                     *abort_flag = 1;
                     ok = false;
@@ -244,13 +264,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
                 const uint32_t full = bar(BAR_FULL + stage);
                 const uint32_t st = smem_u32(smem + stage * STAGE_BYTES);
-                mbar_expect_tx(full, STAGE_BYTES);
+                if (fills >= ahead) {
+                    mbar_expect_tx(full, STAGE_BYTES);
+                    load_b(c, kb, st, full);
+                }
                 tma_load_2d(st, &tmap_a, xa, ya, full);
-                tma_load_2d(st + A_BYTES, &tmap_b, xb, yb, full);
                 tma_load_3d(st + A_BYTES + B_BYTES, &tmap_sfa, 0,
                             c.a_k / MMA_K + kb * (BK / MMA_K), ya / CTA_M, full);
-                tma_load_3d(st + A_BYTES + B_BYTES + SFA_BYTES, &tmap_sfb, 0,
-                            c.b_k / MMA_K + kb * (BK / MMA_K), c.b_row / CTA_M, full);
                 ++fills;
                 if (++stage == STAGES) {
                     stage = 0;
@@ -262,6 +282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // Let every copy already issued land before the CTA can exit: slot s was filled
             // n_s times, and its last fill completes phase n_s - 1 of its full barrier.
             for (int s = 0; s < STAGES; ++s) {
+                // (a slot with only its weights under way never completes: such an abort can only
+                // come from a wait that ran out, after every slot was filled once)
                 const uint32_t n_s = fills > static_cast<uint32_t>(s)
                                          ? (fills - static_cast<uint32_t>(s) + STAGES - 1) / STAGES
                                          : 0u;
@@ -428,6 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int chunk = (warp - FIRST_EPI_WARP) >> 2; // accumulator columns [64 chunk, +64)
         const uint32_t stage_buf = smem_u32(staging + (warp - FIRST_EPI_WARP) * STAGING_BYTES);
         // NVFP4: undo both tensor scales; MXFP4 has none (its amax only flags bad data)
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the quantizer's amax
         const Alpha alpha = epilogue_alpha<false>(*p.amax_a, *p.amax_b);
         int it = 0;  // tiles with an accumulator so far
         constexpr uint32_t EPI_THREADS = 32 * NUM_EPI_WARPS;
@@ -544,15 +567,23 @@ cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, int sm_count, cudaStre
     const int64_t tiles = g.by_k ? g.experts * ((g.M + PAIR_M - 1) / PAIR_M) * tiles_n
                                  : g.rows / 128 * tiles_n;
     const int grid = 2 * static_cast<int>(tiles < max_pairs[dev] ? tiles : max_pairs[dev]);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(g.out_bf16 ? grouped_smem<true>() : grouped_smem<false>());
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = g.after_quantizer ? 1 : 0;
     if (g.by_k && g.out_bf16)
-        gemm_grouped_kernel<true, true><<<grid, THREADS, grouped_smem<true>(), s>>>(ma, mb, msa, msb, md, p);
-    else if (g.by_k)
-        gemm_grouped_kernel<false, true><<<grid, THREADS, grouped_smem<false>(), s>>>(ma, mb, msa, msb, md, p);
-    else if (g.out_bf16)
-        gemm_grouped_kernel<true, false><<<grid, THREADS, grouped_smem<true>(), s>>>(ma, mb, msa, msb, md, p);
-    else
-        gemm_grouped_kernel<false, false><<<grid, THREADS, grouped_smem<false>(), s>>>(ma, mb, msa, msb, md, p);
-    return cudaGetLastError();
+        return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<true, true>, ma, mb, msa, msb, md, p);
+    if (g.by_k)
+        return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<false, true>, ma, mb, msa, msb, md, p);
+    if (g.out_bf16)
+        return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<true, false>, ma, mb, msa, msb, md, p);
+    return cudaLaunchKernelEx(&cfg, gemm_grouped_kernel<false, false>, ma, mb, msa, msb, md, p);
 }
 
 }  // namespace nvfp4

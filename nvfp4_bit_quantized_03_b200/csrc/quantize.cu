@@ -65,17 +65,47 @@ __global__ void __launch_bounds__(256) amax_kernel(const uint16_t* __restrict__ 
     block_max_store(m, partials + blockIdx.x);
 }
 
+// Largest magnitude of the four transforms (before their x1/4) of 16 rows x 4 columns, two columns
+// per pass on paired FP32 lanes (the packed bf16 pair of a word); flip: the sign of each row.
+__device__ __forceinline__ uint32_t absmax_rht4(const uint2 (&v)[16], const uint32_t (&flip)[16])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int jp = 0; jp < 2; ++jp) {
+        uint64_t y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const uint32_t w = (jp == 0 ? v[k].x : v[k].y) ^ flip[k];
+            y[k] = f2pack(bf16_lo(w), bf16_hi(w));
+        }
+#pragma unroll
+        for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                if (k & h) continue;
+                const uint64_t a = y[k], b = y[k + h];
+                y[k] = add2_rn(a, b);
+                y[k + h] = sub2_rn(a, b);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            m = max(m, max(__float_as_uint(f2lo(y[k])) & 0x7FFFFFFFu,
+                           __float_as_uint(f2hi(y[k])) & 0x7FFFFFFFu));
+    }
+    return m;
+}
+
 // amax of the random Hadamard transform along the rows: each work item is 16 rows x 4 columns
 // (16 coalesced 8-byte loads), i.e. four 16-element transforms.  With PLAIN the same loads also
 // give the amax of x itself (the row-wise output of the dual mode).
-// With GROUPED the rows are those of an expert-ordered matrix (RowMap).
-template <bool PLAIN, bool GROUPED = false>
+template <bool PLAIN>
 __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restrict__ x,
                                                        int64_t rows, int64_t cols, int64_t ld,
                                                        uint32_t sign_mask,
                                                        uint32_t* __restrict__ partials,
                                                        uint32_t* __restrict__ partials_plain,
-                                                       int* dev_status, const RowMap map = {})
+                                                       int* dev_status)
 {
     // The transform's sign flips are applied to the packed bf16 pairs (one xor per two
     // values), and its final x1/4 is applied once to the maximum: rounding is monotone, so the
@@ -84,10 +114,9 @@ __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restric
 #pragma unroll
     for (int k = 0; k < 16; ++k) flip[k] = ((sign_mask >> k) & 1u) ? 0x80008000u : 0u;
     uint32_t mp = 0;
-    // extent of x (bounds checks)
-    const int64_t xb = bf16_matrix_bytes(GROUPED ? map.x_rows : rows, cols, ld);
+    const int64_t xb = bf16_matrix_bytes(rows, cols, ld);  // extent of x (bounds checks)
     const int64_t cpr = cols >> 2;  // 8-byte column groups per row
-    const int64_t total = ((GROUPED ? map.used_rows(rows) : rows) >> 4) * cpr;
+    const int64_t total = (rows >> 4) * cpr;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     uint32_t m = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
@@ -96,46 +125,14 @@ __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restric
         const uint16_t* base = x + (g << 4) * ld + (c << 2);
         uint2 v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            if (GROUPED) {
-                const int64_t src = map.source((g << 4) + k);
-                v[k] = make_uint2(0u, 0u);
-                if (src >= 0)
-                    v[k] = ldg_checked(reinterpret_cast<const uint2*>(x + src * ld + (c << 2)), x, xb,
-                                       dev_status);
-            } else {
-                v[k] = ldg_checked(reinterpret_cast<const uint2*>(base + k * ld), x, xb, dev_status);
-            }
-        }
+        for (int k = 0; k < 16; ++k)
+            v[k] = ldg_checked(reinterpret_cast<const uint2*>(base + k * ld), x, xb, dev_status);
         if (PLAIN) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 mp = __vmaxu2(mp, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
         }
-        // two columns per transform pass, on paired FP32 lanes (the packed bf16 pair of a word)
-#pragma unroll
-        for (int jp = 0; jp < 2; ++jp) {
-            uint64_t y[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const uint32_t w = (jp == 0 ? v[k].x : v[k].y) ^ flip[k];
-                y[k] = f2pack(bf16_lo(w), bf16_hi(w));
-            }
-#pragma unroll
-            for (int h = 1; h < 16; h <<= 1) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    if (k & h) continue;
-                    const uint64_t a = y[k], b = y[k + h];
-                    y[k] = add2_rn(a, b);
-                    y[k + h] = sub2_rn(a, b);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                m = max(m, max(__float_as_uint(f2lo(y[k])) & 0x7FFFFFFFu,
-                               __float_as_uint(f2hi(y[k])) & 0x7FFFFFFFu));
-        }
+        m = max(m, absmax_rht4(v, flip));
     }
     // x1/4 of the largest magnitude (NaN and Inf stay at or above the Inf pattern)
     m = __float_as_uint(__fmul_rn(__uint_as_float(m), 0.25f));
@@ -145,6 +142,12 @@ __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restric
         block_max_store(max(mp & 0xFFFFu, mp >> 16) << 16, partials_plain + blockIdx.x);
     }
 }
+
+// A kernel of one of these chains (amax, quantize, product) may be launched before its predecessor
+// has ended: it waits here before it touches what the predecessor writes.  Without the launch
+// attribute both are no-ops.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------------------
 // Shared prologue of the quantize kernels: the tensor amax and its encode scale.
@@ -461,6 +464,10 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
     // block loops unrolled the kernel body overflows the instruction cache ("no instruction"
     // was its top stall), so those loops stay rolled.
     constexpr bool kRollBlocks = DUAL && SR;
+    if (GROUPED) {
+        chain_next();
+        chain_wait();
+    }
     TensorScale ts_row, ts_col;
     if (DUAL) {
         ts_row = fold_amax(a.src, a.row_amax, nullptr, a.dev_status);
@@ -765,8 +772,8 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
 // the row-wise passes have kernels of their own because a row of x may be needed several times.
 // ------------------------------------------------------------------------------------------
 
-// Partial maxima of |x| over the rows of x that some expert takes: a warp per row.  A row of x
-// is read once, however many experts take it.
+// Partial maxima of |x| over the rows of x that some expert takes: a warp per row, four loads in
+// flight per lane.  A row of x is read once, however many experts take it.
 __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __restrict__ x,
                                                            int64_t rows, int64_t cols, int64_t ld,
                                                            uint32_t* __restrict__ partials,
@@ -781,106 +788,221 @@ __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __res
     for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
          r += wstride) {
         bool used;
-        if (map.gather) {
-            bool mine = false;
-            for (int64_t j = lane; j < map.k; j += 32) mine |= map.pair_target(r, j, rows) >= 0;
-            used = __any_sync(0xFFFFFFFFu, mine);
-        } else {
+        if (map.gather)
+            used = __any_sync(0xFFFFFFFFu, lane < map.k && map.pair_target(r, lane, rows) >= 0);
+        else
             used = map.source(r) >= 0;
-        }
         if (!used) continue;
         const uint4* p = reinterpret_cast<const uint4*>(x + r * ld);
-        for (int64_t c = lane; c < cpr; c += 32)
-            m = max(m, absmax_bits8(ldg_checked(p + c, x, xb, dev_status)));
+        for (int64_t c = lane; c < cpr; c += 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (c + 32 * u < cpr) v[u] = ldg_checked(p + c + 32 * u, x, xb, dev_status);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) m = max(m, absmax_bits8(v[u]));
+        }
     }
     block_max_store(m, partials + blockIdx.x);
 }
 
-// One 16-byte chunk per lane (8 values, half a block) of a warp's row: the packed codes and, in the
-// lanes 8 k, the scale word of four blocks.
-template <bool SR>
-__device__ __forceinline__ void quant_chunk(const uint4& v, const TensorScale& ts,
-                                            const float* r_tab, const Philox& ph, uint64_t group,
-                                            uint64_t offset, uint32_t& packed, uint32_t& sfw)
+// The same of the random Hadamard transform along the expert-ordered rows (and, with PLAIN, of the
+// rows themselves): a warp takes 16 rows x 128 columns; its lanes look up one row each and pass
+// the places on.
+template <bool PLAIN>
+__global__ void __launch_bounds__(256) amax_rht_grouped_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, uint32_t sign_mask,
+    uint32_t* __restrict__ partials, uint32_t* __restrict__ partials_plain, int* dev_status,
+    const RowMap map)
 {
-    float e[8];
-    unpack8(v, e);
-    const float m = absmax_f32<8>(e);
-    const float b = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    const BlockScale bs = block_scale(b, ts.s_enc, r_tab);
-    packed = ts.nonfinite ? 0u : encode8<SR>(v, e, bs, ph, group, offset);
-    const uint32_t sf = ts.nonfinite ? 0u : bs.sf;
-    const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, sf, 2);
-    const uint32_t s2 = __shfl_down_sync(0xFFFFFFFFu, sf, 4);
-    const uint32_t s3 = __shfl_down_sync(0xFFFFFFFFu, sf, 6);
-    sfw = sf | (s1 << 8) | (s2 << 16) | (s3 << 24);
+    uint32_t flip[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) flip[k] = ((sign_mask >> k) & 1u) ? 0x80008000u : 0u;
+    const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
+    const int lane = threadIdx.x & 31;
+    const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    const int64_t cpr = cols >> 2, chunks = (cpr + 31) >> 5;
+    const int64_t total = (map.used_rows(rows) >> 4) * chunks;
+    uint32_t m = 0, mp = 0;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < total;
+         i += wstride) {
+        const int64_t g = i / chunks, c = (i - g * chunks) * 32 + lane;
+        const int mine = lane < 16 ? static_cast<int>(map.source((g << 4) + lane)) : -1;
+        if (!__any_sync(0xFFFFFFFFu, mine >= 0)) continue;
+        uint2 v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int src = __shfl_sync(0xFFFFFFFFu, mine, k);
+            v[k] = make_uint2(0u, 0u);
+            if (src >= 0 && c < cpr)
+                v[k] = ldg_checked(reinterpret_cast<const uint2*>(x + src * ld) + c, x, xb, dev_status);
+        }
+        if (PLAIN) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                mp = __vmaxu2(mp, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
+        }
+        m = max(m, absmax_rht4(v, flip));
+    }
+    // x1/4 of the largest magnitude (NaN and Inf stay at or above the Inf pattern)
+    m = __float_as_uint(__fmul_rn(__uint_as_float(m), 0.25f));
+    block_max_store(m, partials + blockIdx.x);
+    if (PLAIN) {
+        __syncthreads();  // block_max_store's shared scratch is reused
+        block_max_store(max(mp & 0xFFFFu, mp >> 16) << 16, partials_plain + blockIdx.x);
+    }
 }
 
-// Row-wise codes and scales of an expert-ordered matrix, a warp per row.
+// Source rows of a small matrix: the tokens when gathering, else the rows of the pairs.
+constexpr int kSmallRows = 512;
+
+// amax of a small matrix by one CTA, for itself: every CTA of the quantize kernel computes it
+// instead of waiting for a pass of its own.
+__device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, int64_t cols,
+                                               int64_t ld, const RowMap& map, int* dev_status)
+{
+    __shared__ int place[kSmallRows];
+    __shared__ uint32_t largest;
+    const int n = static_cast<int>(map.gather ? map.tokens : map.tokens * map.k);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        int row = -1;
+        if (map.gather) {
+            for (int j = 0; j < map.k; ++j)
+                if (map.pair_target(i, j, rows) >= 0) row = i;
+        } else {
+            row = static_cast<int>(map.pair_target(0, i, rows));
+            if (row >= 0 && (row >= map.used_rows(rows) || map.source(row) < 0)) row = -1;
+        }
+        place[i] = row;
+    }
+    if (threadIdx.x == 0) largest = 0;
+    __syncthreads();
+    const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
+    const unsigned cpr = static_cast<unsigned>(cols >> 3), total = n * cpr;
+    uint32_t m = 0;
+#pragma unroll 4
+    for (unsigned i = threadIdx.x; i < total; i += blockDim.x) {
+        const unsigned r = i / cpr, c = i - r * cpr;
+        const int src = place[r];
+        if (src >= 0)
+            m = max(m, absmax_bits8(ldg_checked(reinterpret_cast<const uint4*>(x + src * ld) + c, x, xb,
+                                                dev_status)));
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0 && m) atomicMax(&largest, m);
+    __syncthreads();
+    return largest;
+}
+
+// Row-wise codes and scales of an expert-ordered matrix.  A warp takes 1024 columns of a row, a lane
+// 32 of them: two whole blocks, so no maximum crosses lanes, and one 16-byte store of codes.
 //  * SCATTER (gathered, round to nearest): the warp takes a row of x, quantizes it once and writes
 //    it to the row of every expert that takes it; the rows without a token are zeroed after.
 //  * otherwise the warp takes a row of the expert-ordered matrix (stochastic rounding draws other
 //    bits for every such row).
 // Rows behind the last region are not written.
 template <bool SR, bool SCATTER>
-__global__ void __launch_bounds__(256) quant_grouped_kernel(
+__global__ void __launch_bounds__(256, 3) quant_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, QuantSource src,
     float* amax_out, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
     const PhiloxKeys keys, uint64_t offset, int* dev_status, const RowMap map)
 {
     __shared__ float r_tab[128];
-    const TensorScale ts = fold_amax(src, amax_out, nullptr, dev_status);
+    chain_next();
+    chain_wait();
+    TensorScale ts;
+    if (src.n_partials == 0 && !src.amax_given) {
+        const uint32_t bits = small_amax(x, rows, cols, ld, map, dev_status);
+        ts.nonfinite = bits >= kF32InfBits;
+        const float amax = ts.nonfinite ? INFINITY : __uint_as_float(bits);
+        ts.s_enc = ts.nonfinite ? 1.0f : tensor_scale(amax);
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            *amax_out = amax;
+            if (ts.nonfinite && dev_status) atomicOr(dev_status, static_cast<int>(kDevNonfinite));
+        }
+    } else {
+        ts = fold_amax(src, amax_out, nullptr, dev_status);
+    }
     fill_factor_table(r_tab, ts.s_enc);
     __syncthreads();
     const Philox philox{keys};
     const int lane = threadIdx.x & 31;
     const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int64_t wfirst = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t cpr = cols >> 3, gpr = cols >> 6;
+    const int64_t spr = cols >> 5, gpr = cols >> 6;  // lanes' spans and scale words per row
+    const int64_t segs = (spr + 31) >> 5;            // warps' pieces of a row
     const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
     const int64_t cb = codes_extent(rows, cols), sb = scales_extent(rows, cols);
     const int64_t used = map.used_rows(rows);
-    auto store = [&](int64_t r, int64_t c, uint32_t packed, uint32_t sfw) {
-        st_checked(reinterpret_cast<uint32_t*>(codes) + r * cpr + c, packed, codes, cb, dev_status);
-        if ((lane & 7) == 0)
-            st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, c >> 1, gpr)), sfw, scales, sb,
-                       dev_status);
+    // word: four blocks' scales, in the even lanes
+    auto store = [&](int64_t r, int64_t span, const uint4& w, uint32_t word) {
+        st_checked(reinterpret_cast<uint4*>(codes) + r * spr + span, w, codes, cb, dev_status);
+        if ((lane & 1) == 0)
+            st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, span << 1, gpr)), word, scales,
+                       sb, dev_status);
     };
-    if (SCATTER) {
-        for (int64_t t = wfirst; t < map.tokens; t += wstride) {
-            // lane j holds the row of the token's j-th expert
-            const int64_t target = lane < map.k ? map.pair_target(t, lane, rows) : -1;
-            const unsigned taken = __ballot_sync(0xFFFFFFFFu, target >= 0);
+    auto quantize = [&](const uint4* v, int64_t r, int64_t span, uint4& w, uint32_t& word) {
+        uint32_t out[4], sf[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float y[16];
+            unpack8(v[2 * b], y);
+            unpack8(v[2 * b + 1], y + 8);
+            const BlockScale bs = block_scale(absmax_f32<16>(y), ts.s_enc, r_tab);
+            encode16<SR>(y, bs, philox, static_cast<uint64_t>(r * cols + 32 * span + 16 * b), offset,
+                         out[2 * b], out[2 * b + 1]);
+            sf[b] = bs.sf;
+        }
+        w = ts.nonfinite ? make_uint4(0, 0, 0, 0) : make_uint4(out[0], out[1], out[2], out[3]);
+        const uint32_t pair = ts.nonfinite ? 0u : sf[0] | (sf[1] << 8);
+        word = pair | (__shfl_down_sync(0xFFFFFFFFu, pair, 1) << 16);
+    };
+    const int64_t source_rows = SCATTER ? map.tokens : used;
+    for (int64_t i = wfirst; i < source_rows * segs; i += wstride) {
+        const int64_t row = i / segs, span = (i - row * segs) * 32 + lane;
+        int target = -1;  // SCATTER: lane j holds the row of the token's j-th expert
+        unsigned taken = 0;
+        int64_t from = row;
+        if (SCATTER) {
+            if (lane < map.k) target = static_cast<int>(map.pair_target(row, lane, rows));
+            taken = __ballot_sync(0xFFFFFFFFu, target >= 0);
             if (taken == 0) continue;
-            const uint4* p = reinterpret_cast<const uint4*>(x + t * ld);
-            for (int64_t c0 = 0; c0 < cpr; c0 += 32) {
-                const int64_t c = c0 + lane;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (c < cpr) v = ldg_checked(p + c, x, xb, dev_status);
-                uint32_t packed, sfw;
-                quant_chunk<false>(v, ts, r_tab, philox, 0, 0, packed, sfw);
-                for (unsigned left = taken; left; left &= left - 1) {
-                    const int64_t r = __shfl_sync(0xFFFFFFFFu, target, __ffs(left) - 1);
-                    if (c < cpr) store(r, c, packed, sfw);
-                }
+        } else {
+            from = map.source(row);
+        }
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (span < spr && from >= 0)
+                v[u] = ldg_checked(reinterpret_cast<const uint4*>(x + from * ld) + 4 * span + u, x, xb,
+                                   dev_status);
+        }
+        uint4 w;
+        uint32_t word;
+        quantize(v, row, span, w, word);
+        if (SCATTER) {
+            for (unsigned left = taken; left; left &= left - 1) {
+                const int r = __shfl_sync(0xFFFFFFFFu, target, __ffs(left) - 1);
+                if (span < spr) store(r, span, w, word);
             }
+        } else if (span < spr) {
+            store(row, span, w, word);
         }
     }
-    for (int64_t r = wfirst; r < used; r += wstride) {
-        const int64_t from = map.source(r);
-        if (SCATTER) {
-            if (from >= 0) continue;
-            for (int64_t c = lane; c < cpr; c += 32) store(r, c, 0u, 0u);
-            continue;
-        }
-        const uint4* p = reinterpret_cast<const uint4*>(x + (from >= 0 ? from : 0) * ld);
-        for (int64_t c0 = 0; c0 < cpr; c0 += 32) {
-            const int64_t c = c0 + lane;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (c < cpr && from >= 0) v = ldg_checked(p + c, x, xb, dev_status);
-            uint32_t packed, sfw;
-            quant_chunk<SR>(v, ts, r_tab, philox, static_cast<uint64_t>(r * cpr + c), offset, packed, sfw);
-            if (c < cpr) store(r, c, packed, sfw);
+    if (SCATTER) {
+        // a warp looks at up to 32 rows at once and zeroes those without a token
+        const int64_t share = (used + wstride - 1) / wstride;
+        const int at_once = static_cast<int>(share < 32 ? share : 32);
+        for (int64_t r0 = at_once * wfirst; r0 < used; r0 += at_once * wstride) {
+            const bool empty = lane < at_once && r0 + lane < used && map.source(r0 + lane) < 0;
+            for (unsigned left = __ballot_sync(0xFFFFFFFFu, empty); left; left &= left - 1) {
+                const int64_t r = r0 + __ffs(left) - 1;
+                for (int64_t span = lane; span < spr; span += 32)
+                    store(r, span, make_uint4(0, 0, 0, 0), 0u);
+            }
         }
     }
 }
@@ -899,6 +1021,23 @@ static int resident_ctas(Kernel kernel, int threads)
         n < 1)
         n = 1;
     return n;
+}
+
+// A launch that may begin before the kernel ahead of it on the stream has ended (chain_wait).
+template <typename... Params, typename... Args>
+static cudaError_t launch_chained(void (*kernel)(Params...), int64_t grid, int threads, bool chained,
+                                  cudaStream_t s, Args... args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 int amax_grid(int64_t rows, int64_t cols, bool rht, int sm_count)
@@ -975,6 +1114,11 @@ static void launch_tile_t(const TileArgs& a, int64_t ntiles, int sm_count, cudaS
     int64_t grid = static_cast<int64_t>(sm_count) * resident;
     if (grid > ntiles) grid = ntiles;
     if (grid < 1) grid = 1;
+    if (GROUPED) {
+        launch_chained(quant_tile_kernel<ROW, COL, B2D, RHT, SR, MX, GROUPED>, grid, 128,
+                       a.src.n_partials > 0, s, a);
+        return;
+    }
     quant_tile_kernel<ROW, COL, B2D, RHT, SR, MX, GROUPED>
         <<<static_cast<int>(grid), 128, 0, s>>>(a);
 }
@@ -1018,13 +1162,21 @@ cudaError_t launch_quant_tile(const TileArgs& a, bool row, bool col, bool block2
 
 int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, int sm_count)
 {
-    if (rht) return amax_grid(rows, cols, true, sm_count);
     static const int resident = resident_ctas(amax_grouped_kernel, 256);
-    const int64_t n = ((map.gather ? map.tokens : rows) + 7) / 8;  // a warp per row
-    int64_t g = static_cast<int64_t>(sm_count) * resident;
-    if (g > n) g = n;
+    static const int resident_rht = resident_ctas(amax_rht_grouped_kernel<true>, 256);
+    // a warp per row, or per 16 rows x 128 columns
+    const int64_t items = rht ? rows / 16 * ((cols + 127) / 128) : (map.gather ? map.tokens : rows);
+    int64_t g = static_cast<int64_t>(sm_count) * (rht ? resident_rht : resident);
+    if (g > (items + 7) / 8) g = (items + 7) / 8;
     if (g > kMaxPartials) g = kMaxPartials;
     return static_cast<int>(g < 1 ? 1 : g);
+}
+
+bool grouped_amax_is_small(int64_t cols, const RowMap& map)
+{
+    // 64 KB of source rows, which every CTA reads from L2
+    const int64_t n = map.gather ? map.tokens : map.tokens * map.k;
+    return n <= kSmallRows && n * cols <= 32768;
 }
 
 cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, bool rht,
@@ -1032,11 +1184,11 @@ cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, i
                                 int grid, const RowMap& map, int* dev_status, cudaStream_t s)
 {
     if (rht && partials_plain)
-        amax_rht_kernel<true, true><<<grid, 256, 0, s>>>(x, rows, cols, ld, sign_mask, partials,
-                                                         partials_plain, dev_status, map);
+        amax_rht_grouped_kernel<true><<<grid, 256, 0, s>>>(x, rows, cols, ld, sign_mask, partials,
+                                                           partials_plain, dev_status, map);
     else if (rht)
-        amax_rht_kernel<false, true><<<grid, 256, 0, s>>>(x, rows, cols, ld, sign_mask, partials,
-                                                          nullptr, dev_status, map);
+        amax_rht_grouped_kernel<false><<<grid, 256, 0, s>>>(x, rows, cols, ld, sign_mask, partials,
+                                                            nullptr, dev_status, map);
     else
         amax_grouped_kernel<<<grid, 256, 0, s>>>(x, rows, cols, ld, partials, dev_status, map);
     return cudaGetLastError();
@@ -1045,26 +1197,20 @@ cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, i
 cudaError_t launch_quant_grouped_rows(const TileArgs& a, bool sr, int sm_count, cudaStream_t s)
 {
     const bool scatter = a.map.gather && !sr;
-    static const int resident[3] = {resident_ctas(quant_grouped_kernel<false, false>, 256),
-                                    resident_ctas(quant_grouped_kernel<true, false>, 256),
-                                    resident_ctas(quant_grouped_kernel<false, true>, 256)};
-    int64_t grid = static_cast<int64_t>(sm_count) * resident[scatter ? 2 : (sr ? 1 : 0)];
-    const int64_t n = ((scatter && a.map.tokens > a.rows ? a.map.tokens : a.rows) + 7) / 8;
-    if (grid > n) grid = n;
-    const int g = static_cast<int>(grid);
-    if (scatter)
-        quant_grouped_kernel<false, true><<<g, 256, 0, s>>>(
-            a.x, a.rows, a.cols, a.ld, a.src, a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset,
-            a.dev_status, a.map);
-    else if (sr)
-        quant_grouped_kernel<true, false><<<g, 256, 0, s>>>(
-            a.x, a.rows, a.cols, a.ld, a.src, a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset,
-            a.dev_status, a.map);
-    else
-        quant_grouped_kernel<false, false><<<g, 256, 0, s>>>(
-            a.x, a.rows, a.cols, a.ld, a.src, a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset,
-            a.dev_status, a.map);
-    return cudaGetLastError();
+    using Kernel = decltype(&quant_grouped_kernel<false, false>);
+    static const Kernel kernels[3] = {quant_grouped_kernel<false, false>,
+                                      quant_grouped_kernel<true, false>,
+                                      quant_grouped_kernel<false, true>};
+    static const int resident[3] = {resident_ctas(kernels[0], 256), resident_ctas(kernels[1], 256),
+                                    resident_ctas(kernels[2], 256)};
+    const int which = scatter ? 2 : (sr ? 1 : 0);
+    const int64_t n = scatter && a.map.tokens > a.rows ? a.map.tokens : a.rows;
+    int64_t grid = (n * ((a.cols + 1023) / 1024) + 7) / 8;
+    if (grid > static_cast<int64_t>(sm_count) * resident[which]) grid = static_cast<int64_t>(sm_count) * resident[which];
+    // the amax pass is ahead of it, unless the amax is given or computed here
+    const bool chained = a.src.n_partials > 0;
+    return launch_chained(kernels[which], grid, 256, chained, s, a.x, a.rows, a.cols, a.ld, a.src,
+                          a.row_amax, a.row_codes, a.row_scales, a.keys, a.offset, a.dev_status, a.map);
 }
 
 cudaError_t launch_quant_grouped_tile(const TileArgs& a, bool row, bool sr, int sm_count,
