@@ -497,7 +497,7 @@ def _matrix(what, t, dtypes, rows, cols):
 def _dense(what, t, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -508,6 +508,13 @@ def _row_stride(t):
 
 _F32_BF16 = (torch.float32, torch.bfloat16)
 _BF16 = (torch.bfloat16,)
+
+
+def _new(shape, dtype, device):
+    """torch.empty without its dispatch over layouts (a third of its time on the host)."""
+    if len(shape) == 1:
+        return torch.empty_strided(shape, (1,), dtype=dtype, device=device)
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
 
 
 _no_stream = contextlib.nullcontext()
@@ -541,9 +548,8 @@ class ExpertPlan:
         if rows == 0:
             raise NVFP4Error(ERR_SHAPE, f"expert plan of {tokens} tokens, {k} of {experts} experts")
 
-        def ints(*shape):
-            return torch.empty(shape, dtype=torch.int32, device=device)
-        return cls(ints(experts + 1), ints(tokens, k), ints(rows))
+        return cls(_new((experts + 1,), torch.int32, device), _new((tokens, k), torch.int32, device),
+                   _new((rows,), torch.int32, device))
 
 
 def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=True, scale=1.0,
@@ -555,9 +561,9 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=Tr
         _dense("bias", bias, torch.float32, (E,))
     with _allocating(stream):
         if experts is None:
-            experts = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+            experts = _new((T, max(k, 0)), torch.int32, logits.device)
         if weights is None:
-            weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+            weights = _new((T, max(k, 0)), torch.float32, logits.device)
     _dense("experts", experts, torch.int32, (T, k))
     _dense("weights", weights, torch.float32, (T, k))
     queue = _queue("nvfp4_route", stream, logits, bias, experts, weights)
@@ -578,7 +584,7 @@ def route_backward(logits, experts, dweights, sigmoid=False, renorm=True, scale=
     _dense("dweights", dweights, torch.float32, (T, k))
     if dlogits is None:
         with _allocating(stream):
-            dlogits = _poisoned(torch.empty((T, E), dtype=logits.dtype, device=logits.device))
+            dlogits = _poisoned(_new((T, E), logits.dtype, logits.device))
     _matrix("dlogits", dlogits, (logits.dtype,), T, E)
     queue = _queue("nvfp4_route_backward", stream, logits, experts, dweights, dlogits)
     _check(lib().nvfp4_route_backward(_address(logits), _dtype_code(logits.dtype), T, E,
@@ -638,7 +644,7 @@ def quantize_grouped(x, plan, flags, sign_mask=0, seed=0, offset=0, out_row=None
 def _grouped_out(what, out, rows, cols, out_dtype, device, stream):
     if out is None:
         with _allocating(stream):
-            out = _poisoned(torch.empty((rows, cols), dtype=out_dtype, device=device))
+            out = _poisoned(_new((rows, cols), out_dtype, device))
     _matrix(what, out, _F32_BF16, rows, cols)
     return out
 
@@ -751,10 +757,9 @@ def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=
     _dense("weights", weights, torch.float32, (plan.tokens, plan.k))
     with _allocating(stream):
         if dy is None:
-            dy = _poisoned(torch.empty((plan.rows, cols), dtype=torch.bfloat16, device=Y.device))
+            dy = _poisoned(_new((plan.rows, cols), torch.bfloat16, Y.device))
         if dweights is None:
-            dweights = _poisoned(torch.empty((plan.tokens, plan.k), dtype=torch.float32,
-                                             device=Y.device))
+            dweights = _poisoned(_new((plan.tokens, plan.k), torch.float32, Y.device))
     _matrix("dy", dy, _BF16, plan.rows, cols)
     _dense("dweights", dweights, torch.float32, (plan.tokens, plan.k))
     queue = _queue("nvfp4_combine_backward", stream, dout, Y, plan.pair_row, weights, dy, dweights)

@@ -234,6 +234,14 @@ __device__ __forceinline__ float max3f(float a, float b, float c)
     return d;
 }
 
+// The same, NaN if an operand is.
+__device__ __forceinline__ float max3f_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Largest magnitude of v[0..n), n even, two values per three-input maximum (exact, any order).
 template <int N>
 __device__ __forceinline__ float absmax_f32(const float* v)

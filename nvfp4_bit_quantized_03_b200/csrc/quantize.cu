@@ -65,37 +65,6 @@ __global__ void __launch_bounds__(256) amax_kernel(const uint16_t* __restrict__ 
     block_max_store(m, partials + blockIdx.x);
 }
 
-// Largest magnitude of the four transforms (before their x1/4) of 16 rows x 4 columns, two columns
-// per pass on paired FP32 lanes (the packed bf16 pair of a word); flip: the sign of each row.
-__device__ __forceinline__ uint32_t absmax_rht4(const uint2 (&v)[16], const uint32_t (&flip)[16])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int jp = 0; jp < 2; ++jp) {
-        uint64_t y[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const uint32_t w = (jp == 0 ? v[k].x : v[k].y) ^ flip[k];
-            y[k] = f2pack(bf16_lo(w), bf16_hi(w));
-        }
-#pragma unroll
-        for (int h = 1; h < 16; h <<= 1) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                if (k & h) continue;
-                const uint64_t a = y[k], b = y[k + h];
-                y[k] = add2_rn(a, b);
-                y[k + h] = sub2_rn(a, b);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            m = max(m, max(__float_as_uint(f2lo(y[k])) & 0x7FFFFFFFu,
-                           __float_as_uint(f2hi(y[k])) & 0x7FFFFFFFu));
-    }
-    return m;
-}
-
 // amax of the random Hadamard transform along the rows: each work item is 16 rows x 4 columns
 // (16 coalesced 8-byte loads), i.e. four 16-element transforms.  With PLAIN the same loads also
 // give the amax of x itself (the row-wise output of the dual mode).
@@ -132,7 +101,30 @@ __global__ void __launch_bounds__(256) amax_rht_kernel(const uint16_t* __restric
             for (int k = 0; k < 16; ++k)
                 mp = __vmaxu2(mp, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
         }
-        m = max(m, absmax_rht4(v, flip));
+        // two columns per transform pass, on paired FP32 lanes (the packed bf16 pair of a word)
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+            uint64_t y[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t w = (jp == 0 ? v[k].x : v[k].y) ^ flip[k];
+                y[k] = f2pack(bf16_lo(w), bf16_hi(w));
+            }
+#pragma unroll
+            for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    if (k & h) continue;
+                    const uint64_t a = y[k], b = y[k + h];
+                    y[k] = add2_rn(a, b);
+                    y[k + h] = sub2_rn(a, b);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                m = max(m, max(__float_as_uint(f2lo(y[k])) & 0x7FFFFFFFu,
+                               __float_as_uint(f2hi(y[k])) & 0x7FFFFFFFu));
+        }
     }
     // x1/4 of the largest magnitude (NaN and Inf stay at or above the Inf pattern)
     m = __float_as_uint(__fmul_rn(__uint_as_float(m), 0.25f));
@@ -825,7 +817,8 @@ __global__ void __launch_bounds__(256) amax_rht_grouped_kernel(
     const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int64_t cpr = cols >> 2, chunks = (cpr + 31) >> 5;
     const int64_t total = (map.used_rows(rows) >> 4) * chunks;
-    uint32_t m = 0, mp = 0;
+    float m = 0.0f;
+    uint32_t mp = 0;
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < total;
          i += wstride) {
         const int64_t g = i / chunks, c = (i - g * chunks) * 32 + lane;
@@ -844,11 +837,32 @@ __global__ void __launch_bounds__(256) amax_rht_grouped_kernel(
             for (int k = 0; k < 16; ++k)
                 mp = __vmaxu2(mp, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu));
         }
-        m = max(m, absmax_rht4(v, flip));
+        // as in amax_rht_kernel, two columns per pass on paired lanes; the maximum keeps a NaN
+        // (max.NaN: one instruction for two values, where comparing bit patterns takes four)
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+            uint64_t y[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t w = (jp == 0 ? v[k].x : v[k].y) ^ flip[k];
+                y[k] = f2pack(bf16_lo(w), bf16_hi(w));
+            }
+#pragma unroll
+            for (int h = 1; h < 16; h <<= 1) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    if (k & h) continue;
+                    const uint64_t a = y[k], b = y[k + h];
+                    y[k] = add2_rn(a, b);
+                    y[k + h] = sub2_rn(a, b);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) m = max3f_nan(m, fabsf(f2lo(y[k])), fabsf(f2hi(y[k])));
+        }
     }
     // x1/4 of the largest magnitude (NaN and Inf stay at or above the Inf pattern)
-    m = __float_as_uint(__fmul_rn(__uint_as_float(m), 0.25f));
-    block_max_store(m, partials + blockIdx.x);
+    block_max_store(__float_as_uint(__fmul_rn(m, 0.25f)) & 0x7FFFFFFFu, partials + blockIdx.x);
     if (PLAIN) {
         __syncthreads();  // block_max_store's shared scratch is reused
         block_max_store(max(mp & 0xFFFFu, mp >> 16) << 16, partials_plain + blockIdx.x);
@@ -904,7 +918,7 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
 //    bits for every such row).
 // Rows behind the last region are not written.
 template <bool SR, bool SCATTER>
-__global__ void __launch_bounds__(256, 3) quant_grouped_kernel(
+__global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, QuantSource src,
     float* amax_out, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
     const PhiloxKeys keys, uint64_t offset, int* dev_status, const RowMap map)

@@ -170,27 +170,35 @@ __device__ __forceinline__ void pack_and_sort(uint32_t (&key)[NPL])
                     }
 }
 template <int NPL>
-__device__ __forceinline__ int take_best(uint32_t (&key)[NPL], int rounds, int lane, float& gap)
+__device__ __forceinline__ int take_best(uint32_t (&key)[NPL], int rounds, int lane, uint2* found,
+                                         float& gap)
 {
     constexpr uint32_t kPlace = NPL - 1u;
-    int mine = -1;
-    float before = INFINITY;
+    const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll 3
     for (int r = 0; r <= rounds; ++r) {
         const uint32_t first = key[0] & ~kPlace;
         const uint32_t top = __reduce_max_sync(kAll, first);
-        if (top == 0) break;
-        const float v = key_value(top);
-        gap = fminf(gap, before - v);
-        before = v;
-        const int owner = __ffs(__ballot_sync(kAll, first == top)) - 1;
-        const int place = static_cast<int>(kPlace - (__shfl_sync(kAll, key[0], owner) & kPlace));
-        if (lane == r && r < rounds) mine = owner * NPL + place;
-        if (lane == owner) {
+        // the lowest lane that holds it writes it down and moves up
+        const unsigned holders = __ballot_sync(kAll, first == top);
+        if (first == top && !(holders & lower)) {
+            found[r] = make_uint2(top, lane * NPL + (kPlace - (key[0] & kPlace)));
 #pragma unroll
             for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
             key[NPL - 1] = 0;
         }
     }
+    __syncwarp();
+    // lane r looks at the values of rounds r and r + 1 (0: nothing was left)
+    int mine = -1;
+    if (lane < rounds) {
+        const uint2 a = found[lane];
+        const uint32_t next = found[lane + 1].x;
+        if (a.x) mine = static_cast<int>(a.y);
+        if (next) gap = fminf(gap, key_value(a.x) - key_value(next));
+    }
+    // gaps are not negative: their order is that of their bits
+    gap = __uint_as_float(__reduce_min_sync(kAll, __float_as_uint(gap)));
     return mine;
 }
 
@@ -252,7 +260,7 @@ __device__ __forceinline__ void choice_keys(const RouteArgs& a, const float (&x)
 // 1 + the largest on, sums of two from twice that.
 template <int NPL>
 __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[NPL], float mx,
-                                           int lane, bool& close, bool& bad)
+                                           int lane, uint2* found, bool& close, bool& bad)
 {
     float s[NPL];
     uint32_t key[NPL];
@@ -293,7 +301,7 @@ __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[
             for (int i = 0; i < NPL; ++i) key[i] = 0;
         }
     }
-    const int mine = take_best<NPL>(key, a.k, lane, gap);
+    const int mine = take_best<NPL>(key, a.k, lane, found, gap);
     close = gap < 0x1p-18f * (1.0f + largest);
     return mine;
 }
@@ -346,6 +354,7 @@ template <int NPL, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
 {
     extern __shared__ double group_values[];
+    __shared__ uint2 found[kRouteThreads / 32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * (kRouteThreads / 32) + warp;
     if (t >= a.T) return;
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
             for (int i = 0; i < NPL; ++i) key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
             pack_and_sort<NPL>(key);
             float gap = INFINITY;
-            expert = take_best<NPL>(key, a.k, lane, gap);
+            expert = take_best<NPL>(key, a.k, lane, found[warp], gap);
             if (sizeof(T) == 4 && !(gap > 0.0f)) {
 #pragma unroll
                 for (int i = 0; i < NPL; ++i) key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
             }
         } else {
             bool close = a.group_lanes == 0;
-            if (!close) expert = choose_fast<NPL>(a, x, mx, lane, close, bad);
+            if (!close) expert = choose_fast<NPL>(a, x, mx, lane, found[warp], close, bad);
             if (close && !bad)
                 expert = choose_exact<NPL>(a, x, mx, lane, group_values + warp * a.E, bad);
         }
@@ -393,12 +402,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
     const float l = chosen ? load_logit(row + expert) : -INFINITY;
     float w = 0.0f;
     if (a.renorm) {
-        // shares exp(q - max q) / sum of the chosen log-scores q (up to a common constant): no
-        // underflow however small the scores are
-        const float q = a.sigmoid && chosen ? log_sigmoid(l) : l;
-        const float top = warp_maxf(q);
-        const float p = chosen ? expf(q - top) : 0.0f;
-        const float sum = warp_sum(p);
+        float p = a.sigmoid && chosen ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+        float sum = a.sigmoid ? warp_sum(p) : 0.0f;
+        if (sum < 0x1p-100f) {
+            // softmax, or sigmoids near underflow: shares exp(q - max q) / sum of the chosen
+            // log-scores q (up to a common constant), exact however small the scores are
+            const float q = a.sigmoid && chosen ? log_sigmoid(l) : l;
+            const float top = warp_maxf(q);
+            p = chosen ? expf(q - top) : 0.0f;
+            sum = warp_sum(p);
+        }
         if (chosen) w = a.scale * (p / sum);
     } else if (a.sigmoid) {
         if (chosen) w = a.scale * (1.0f / (1.0f + expf(-l)));
@@ -669,9 +682,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
         }
     }
     // rows without a token: the ends of the regions, and everything behind the last
-    for (int e = chunk; e < a.E; e += chunks)
-        for (int r = start[e] + total[e] + threadIdx.x; r < start[e + 1]; r += kPlanThreads)
-            a.row_token[r] = -1;
+    for (int e = chunk * kPlanWarps + warp; e < a.E; e += chunks * kPlanWarps)
+        for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 32) a.row_token[r] = -1;
     for (int64_t r = start[a.E] + static_cast<int64_t>(chunk) * kPlanThreads + threadIdx.x; r < a.rows;
          r += static_cast<int64_t>(chunks) * kPlanThreads)
         a.row_token[r] = -1;
