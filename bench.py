@@ -947,6 +947,99 @@ def run_dense8b(args):
     return 0 if st == 0 else 1
 
 
+class ExpertsStep:
+    """One training step of a mixture-of-experts feed-forward layer through the public binding:
+    route, plan, both expert products forward with a squared ReLU between, the weighted
+    combination, and the whole way back (synthetic inputs, the weights quantized beforehand)."""
+
+    def __init__(self, wl, device):
+        import torch
+        from nvfp4_bit_quantized_03_b200 import binding as B
+        self.B, self.torch, self.wl = B, torch, wl
+        g = torch.Generator(device=device).manual_seed(wl.seed)
+
+        def randn(*shape, s=1.0):
+            return s * torch.randn(*shape, generator=g, device=device)
+        T, D, F, E = wl.T, wl.D, wl.F, wl.E
+        self.x = randn(T, D).bfloat16()
+        self.logits = randn(T, E, s=1.5)
+        self.bias = randn(E, s=0.1)
+        self.dout = randn(T, D, s=1e-3).bfloat16()
+        both = B.ROWWISE | B.COLWISE | B.BLOCK2D
+        self.up = B.quantize(randn(E * F, D, s=0.02).bfloat16(), both)
+        self.down = B.quantize(randn(E * D, F, s=0.02).bfloat16(), both)
+        self.mask = B.sign_mask_from_seed(wl.seed)
+        self.plan = B.ExpertPlan.empty(T, wl.k, E, device=device)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.events = None
+
+    def _timed(self, name, fn):
+        if self.events is None:
+            return fn()
+        start, end = (self.torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        out = fn()
+        end.record()
+        self.events.append((name, start, end))
+        return out
+
+    def run(self):
+        B, torch, wl, p, st = self.B, self.torch, self.wl, self.plan, dict(dev_status=self.dev_status)
+        timed, seed = self._timed, wl.seed
+        experts, w = timed("route", lambda: B.route(self.logits, wl.k, bias=self.bias, sigmoid=True, **st))
+        timed("plan", lambda: B.expert_plan(experts, wl.E, plan=p, **st))
+        h = timed("up fprop", lambda: B.experts_fprop(self.x, self.up[0], p, **st))
+        r = torch.relu(h)
+        a = r * r
+        y = timed("down fprop", lambda: B.experts_fprop(a, self.down[0], p, gather=False, **st))
+        out = timed("combine", lambda: B.combine(y, p, w, **st))
+        dy, dw = timed("combine backward", lambda: B.combine_backward(self.dout, y, p, w, **st))
+        da = timed("down dgrad", lambda: B.experts_dgrad(dy, self.down[1], p, seed, 0, **st))
+        dw2 = timed("down wgrad", lambda: B.experts_wgrad(dy, a, p, self.mask, seed, 0, gather=False, **st))
+        dh = 2 * r * da
+        dxr = timed("up dgrad", lambda: B.experts_dgrad(dh, self.up[1], p, seed, 2, **st))
+        dw1 = timed("up wgrad", lambda: B.experts_wgrad(dh, self.x, p, self.mask, seed, 2, **st))
+        dx = timed("gather backward", lambda: B.combine(dxr, p, **st))
+        dl = timed("route backward",
+                   lambda: B.route_backward(self.logits, experts, dw, sigmoid=True, **st))
+        return dict(out=out, dx=dx, dw1=dw1, dw2=dw2, dlogits=dl)
+
+
+def run_experts(args):
+    """A mixture-of-experts feed-forward layer (tokens 8192, d 4096, 64 experts of width 2048, 8 per
+    token), forward and backward, with the time of each operator.  Prints one JSON line (not the
+    benchmark's headline line)."""
+    import torch
+    wl = synth.experts_layer()
+    step = ExpertsStep(wl, torch.device("cuda", torch.cuda.current_device()))
+    for _ in range(args.warmup):
+        step.run()
+    torch.cuda.synchronize()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    for _ in range(args.steps):
+        step.run()
+    end.record()
+    torch.cuda.synchronize()
+    ms = start.elapsed_time(end) / args.steps
+    step.events = []
+    for _ in range(args.steps):
+        step.run()
+    torch.cuda.synchronize()
+    split = {}
+    for name, s, e in step.events:
+        split.setdefault(name, []).append(s.elapsed_time(e))
+    st = int(step.dev_status.item())
+    print(json.dumps({
+        "workload": wl.name, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms,
+        "gemm_tflop_per_step": wl.gemm_flops / 1e12,
+        "gemm_tflops_of_step": wl.gemm_flops / (ms / 1e3) / 1e12,
+        "operator_ms": {n: statistics.median(v) for n, v in split.items()},
+        "data": "synthetic, random routing (sigmoid scores, bias), weights quantized beforehand",
+        "dev_status": st}), flush=True)
+    return 0 if st == 0 else 1
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -963,9 +1056,9 @@ def main(argv=None):
                     help="quantizer bandwidth sweep over 2^n-element tensors (one line per point)")
     ap.add_argument("--sweep-min", type=int, default=20)
     ap.add_argument("--sweep-max", type=int, default=30)
-    ap.add_argument("--workload", choices=["mlp12b", "dense8b"], default="mlp12b",
-                    help="dense8b: the 8B-class layer stack (4 NVFP4 layers + 1 bf16 layer), "
-                         "reported on its own JSON line")
+    ap.add_argument("--workload", choices=["mlp12b", "dense8b", "experts"], default="mlp12b",
+                    help="dense8b: the 8B-class layer stack (4 NVFP4 layers + 1 bf16 layer); "
+                         "experts: a mixture-of-experts layer; each on its own JSON line")
     args = ap.parse_args(argv)
     args.warmup = max(args.warmup, 3)  # at least 3 untimed warm-up steps
     if args.impl == "reference":
@@ -976,6 +1069,8 @@ def main(argv=None):
         return run_sweep(args)
     if args.workload == "dense8b":
         return run_dense8b(args)
+    if args.workload == "experts":
+        return run_experts(args)
     return run_ours(args)
 
 

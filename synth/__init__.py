@@ -118,6 +118,28 @@ def dense_8b_layer() -> Workload:
                     "8B-class dense layer linears, 4 NVFP4 layers + 1 bf16 layer")
 
 
+@dataclass
+class ExpertsLayer:
+    """A mixture-of-experts feed-forward layer: T tokens of D features, each to k of E experts with
+    an up-projection D -> F and a down-projection F -> D."""
+    name: str
+    seed: int
+    T: int
+    D: int
+    F: int
+    E: int
+    k: int
+
+    @property
+    def gemm_flops(self) -> int:
+        return 3 * 2 * 2 * self.T * self.k * self.D * self.F
+
+
+def experts_layer() -> ExpertsLayer:
+    """Tokens 8192, d_model 4096, 64 experts of width 2048, 8 per token."""
+    return ExpertsLayer("experts_t8192_d4096_f2048_e64_k8", 5, 8192, 4096, 2048, 64, 8)
+
+
 QUANT_SWEEP_SEED = 3
 QUANT_SWEEP_ROW = 4096
 QUANT_SWEEP_LOG2 = list(range(20, 31))
