@@ -197,7 +197,7 @@ nvfp4_status nvfp4_quantize_grouped(const void* x_bf16, int64_t cols, int64_t ld
     if (given) {
         a.src.amax_given = want_row ? out_row->amax : nullptr;
         a.src_col.amax_given = want_col ? out_col->amax : nullptr;
-    } else if (want_col || !grouped_amax_is_small(cols, a.map)) {
+    } else if (want_col || sr || !grouped_amax_is_small(cols, a.map)) {
         // [RHT partials][plain partials], as in nvfp4_quantize_row_rht
         uint32_t* rht = static_cast<uint32_t*>(workspace);
         uint32_t* plain = rht + kMaxPartials;

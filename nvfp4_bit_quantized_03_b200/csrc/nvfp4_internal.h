@@ -107,7 +107,7 @@ cudaError_t launch_quant_tile(const TileArgs& a, bool row, bool col, bool block2
 // The same passes over an expert-ordered matrix.  amax: plain (`partials`), RHT (`partials`), or
 // both (`partials_plain` not null).
 int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, int sm_count);
-// Whether the row-wise pass computes the plain amax itself (n_partials 0, no amax pass).
+// Whether the gathered row-wise RTN pass computes the amax itself (n_partials 0, no amax pass).
 bool grouped_amax_is_small(int64_t cols, const RowMap& map);
 cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, bool rht,
                                 uint32_t sign_mask, uint32_t* partials, uint32_t* partials_plain,

@@ -869,40 +869,32 @@ __global__ void __launch_bounds__(256) amax_rht_grouped_kernel(
     }
 }
 
-// Source rows of a small matrix: the tokens when gathering, else the rows of the pairs.
-constexpr int kSmallRows = 512;
+// amax of a few gathered tokens by one CTA, for itself: every CTA of the quantize kernel computes
+// it instead of waiting for a pass of its own.
+constexpr int kSmallElements = 8192;
 
-// amax of a small matrix by one CTA, for itself: every CTA of the quantize kernel computes it
-// instead of waiting for a pass of its own.
 __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, int64_t cols,
                                                int64_t ld, const RowMap& map, int* dev_status)
 {
-    __shared__ int place[kSmallRows];
+    __shared__ bool used[kSmallElements / 64];
     __shared__ uint32_t largest;
-    const int n = static_cast<int>(map.gather ? map.tokens : map.tokens * map.k);
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        int row = -1;
-        if (map.gather) {
-            for (int j = 0; j < map.k; ++j)
-                if (map.pair_target(i, j, rows) >= 0) row = i;
-        } else {
-            row = static_cast<int>(map.pair_target(0, i, rows));
-            if (row >= 0 && (row >= map.used_rows(rows) || map.source(row) < 0)) row = -1;
-        }
-        place[i] = row;
+    const int n = static_cast<int>(map.tokens);
+    for (int t = threadIdx.x; t < n; t += blockDim.x) {
+        bool any = false;
+        for (int j = 0; j < map.k; ++j) any |= map.pair_target(t, j, rows) >= 0;
+        used[t] = any;
     }
     if (threadIdx.x == 0) largest = 0;
     __syncthreads();
     const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
     const unsigned cpr = static_cast<unsigned>(cols >> 3), total = n * cpr;
     uint32_t m = 0;
-#pragma unroll 4
     for (unsigned i = threadIdx.x; i < total; i += blockDim.x) {
-        const unsigned r = i / cpr, c = i - r * cpr;
-        const int src = place[r];
-        if (src >= 0)
-            m = max(m, absmax_bits8(ldg_checked(reinterpret_cast<const uint4*>(x + src * ld) + c, x, xb,
-                                                dev_status)));
+        const unsigned t = i / cpr, c = i - t * cpr;
+        if (used[t])
+            m = max(m, absmax_bits8(ldg_checked(
+                           reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t) * ld) + c, x, xb,
+                           dev_status)));
     }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0 && m) atomicMax(&largest, m);
@@ -927,7 +919,7 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     chain_next();
     chain_wait();
     TensorScale ts;
-    if (src.n_partials == 0 && !src.amax_given) {
+    if (SCATTER && src.n_partials == 0 && !src.amax_given) {
         const uint32_t bits = small_amax(x, rows, cols, ld, map, dev_status);
         ts.nonfinite = bits >= kF32InfBits;
         const float amax = ts.nonfinite ? INFINITY : __uint_as_float(bits);
@@ -985,12 +977,16 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
             if (taken == 0) continue;
         } else {
             from = map.source(row);
+            if (from < 0) {  // a row without a token
+                if (span < spr) store(row, span, make_uint4(0, 0, 0, 0), 0u);
+                continue;
+            }
         }
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             v[u] = make_uint4(0, 0, 0, 0);
-            if (span < spr && from >= 0)
+            if (span < spr)
                 v[u] = ldg_checked(reinterpret_cast<const uint4*>(x + from * ld) + 4 * span + u, x, xb,
                                    dev_status);
         }
@@ -1188,9 +1184,10 @@ int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, i
 
 bool grouped_amax_is_small(int64_t cols, const RowMap& map)
 {
-    // 64 KB of source rows, which every CTA reads from L2
-    const int64_t n = map.gather ? map.tokens : map.tokens * map.k;
-    return n <= kSmallRows && n * cols <= 32768;
+    // Every CTA reads these tokens from L2.  B200, 64 experts, 8 per token, computed here against in
+    // a pass of its own: 1 x 4096 5.7 against 7.3 us, 2 x 4096 7.0 / 8.5, 4 x 4096 9.5 / 9.2, 4 x 2048
+    // 7.0 / 7.5, 8 x 2048 8.6 / 7.9.  Matrices in expert order gain nothing (1 token: 5.9 / 5.3).
+    return map.gather && map.tokens * cols <= kSmallElements;
 }
 
 cudaError_t launch_amax_grouped(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, bool rht,

@@ -480,6 +480,35 @@ def test_gemm_grouped_by_k(T, k, E, I, O, dtype):
         assert_gemm_close(D[e], ref, norm, bf16=dtype == torch.bfloat16, what=e)
 
 
+def test_gemm_grouped_with_the_most_experts():
+    T, k, E, I, O = 70, 2, 512, 64, 128
+    experts = R.routing(np.random.default_rng(9), T, E, k)
+    plan, o, p, r = _plan(experts, E)
+    _, wr, _ = _weights(E, O, I, 8)
+    x = synth.activations((T, I), seed=7)
+    qa = oracle.quantize(R.gather_bits(x, r))
+    st = _status()
+    D = B.experts_fprop(to_device_bf16(x), upload_quantized(wr, B), plan, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    _check_rows(D, qa, o, lambda e: _rows_of(wr, e * O, (e + 1) * O), True, "512 experts")
+
+
+def test_one_expert_for_all_is_the_plain_linear():
+    """With one expert and full regions the operators give the linear layer's own bits."""
+    T, I, O = 256, 320, 384
+    X, W, dY = (to_device_bf16(a) for a in synth.linear_inputs(synth.Linear("t", T, I, O), 4))
+    plan = B.expert_plan(torch.zeros(T, 1, dtype=torch.int32, device="cuda"), 1)
+    q, qt = B.quantize(W, B.ROWWISE | B.COLWISE | B.BLOCK2D)
+    for dtype in (torch.float32, torch.bfloat16):
+        assert torch.equal(B.experts_fprop(X, q, plan, out_dtype=dtype),
+                           B.linear_fprop(X, W, out_dtype=dtype))
+        assert torch.equal(B.experts_dgrad(dY, qt, plan, 3, 5, out_dtype=dtype),
+                           B.linear_dgrad(dY, W, 3, 5, out_dtype=dtype))
+        assert torch.equal(B.experts_wgrad(dY, X, plan, 0x1234, 3, 5, out_dtype=dtype),
+                           B.linear_wgrad(dY, X, 0x1234, 3, 5, out_dtype=dtype))
+
+
 def test_gemm_grouped_strided_output_leaves_the_gaps():
     experts = R.routing(np.random.default_rng(0), 70, 3, 2)
     plan, o, p, r = _plan(experts, 3)
@@ -681,6 +710,50 @@ def test_calls_on_a_stream_of_their_own():
     used = int(o[-1])
     assert torch.equal(got[:used], ref[:used])
     assert torch.equal(out, B.combine(ref, plan))
+
+
+def test_two_layers_on_two_streams_at_once():
+    """Calls share no memory but what they are given: two layers interleaved on two streams give what
+    each gives alone."""
+    layers = [_Layer(80, 256, 256, 5, 2, seed=s) for s in (11, 12)]
+    alone = [l.step() for l in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in layers]
+    both = [None, None]
+    for _ in range(3):
+        for i, (l, s) in enumerate(zip(layers, streams)):
+            with torch.cuda.stream(s):
+                both[i] = l.step()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for name in a:
+            assert torch.equal(a[name], b[name]), name
+
+
+def test_two_graphs_may_share_a_workspace_on_one_stream():
+    rng = np.random.default_rng(3)
+    w = to_device_bf16(synth.weights((4 * 128, 256), seed=2))
+    q, _ = B.quantize(w, B.ROWWISE | B.BLOCK2D)
+    plans, xs, graphs, outs, ws = [], [], [], [], None
+    for i in range(2):
+        plans.append(_plan(R.routing(rng, 50 + i, 4, 2), 4)[0])
+        xs.append(to_device_bf16(synth.activations((50 + i, 256), seed=i)))
+    size = max(B.experts_workspace_bytes(p, 256, 128) for p in plans)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    refs = [B.experts_fprop(x, q, p) for x, p in zip(xs, plans)]
+    for x, p in zip(xs, plans):
+        out = torch.full((p.rows, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.experts_fprop(x, q, p, out=out, workspace=ws)
+        graphs.append(g)
+        outs.append(out)
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for out, ref, p in zip(outs, refs, plans):
+        used = int(p.offsets[-1])
+        assert torch.equal(out[:used], ref[:used])
 
 
 def test_a_plan_of_another_routing_stays_inside_the_buffers():
