@@ -169,7 +169,7 @@ struct GroupedGemmArgs {
 
 // Routing (route.cu).  The plan's first pass counts each kPlanPairs pairs apart; it needs no
 // workspace when there are no more.
-constexpr int kPlanPairs = 2048;
+constexpr int kPlanPairs = 1024;
 cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int64_t E, int64_t ld,
                          const float* bias, bool sigmoid, bool renorm, int groups, int top_groups,
                          int k, float scale, int32_t* experts, float* weights, int* dev_status,

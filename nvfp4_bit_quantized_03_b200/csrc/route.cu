@@ -24,8 +24,9 @@ constexpr int kRouteThreads = 128;
 constexpr uint32_t kDevIndex = 8u;  // NVFP4_DEVSTAT_INDEX
 
 // ---- order-preserving keys -----------------------------------------------------------------
-// Unsigned integers in the order of the values (-0 and +0 equal); 0 is below every key and marks
-// what cannot be chosen.
+// Unsigned integers in the order of the values (-0 and +0 equal).  Keys below kFirstKey (-inf, and 0
+// for what has been taken or excluded) cannot be chosen; a +inf or NaN is at or above kBadKey.
+constexpr uint32_t kFirstKey = 0x00800000u, kBadKey = 0xFF800000u;
 __device__ __forceinline__ uint32_t order_key(float v)
 {
     const uint32_t b = __float_as_uint(v + 0.0f);
@@ -146,15 +147,14 @@ __device__ __forceinline__ int select_best(Key (&key)[NPL], int rounds, int lane
 
 // The same, faster, on 32-bit keys whose lowest log2(NPL) bits give way to the place in the lane
 // (NPL - 1 - i, so that equal keys come in the order of their places).  Each lane sorts its keys
-// once (Batcher's odd-even merge sort); a round then compares the lanes' first ones and its owner
-// moves up.  gap: the smallest difference between the values of consecutive rounds, the one after
-// the last included, without those bits (0 for equal ones).
+// once (Batcher's odd-even merge sort); a round then compares the lanes' first ones, and the lowest
+// lane that holds the best writes it down and moves up.
 template <int NPL>
 __device__ __forceinline__ void pack_and_sort(uint32_t (&key)[NPL])
 {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-        if (key[i]) key[i] = (key[i] & ~(NPL - 1u)) | static_cast<uint32_t>(NPL - 1 - i);
+        key[i] = (key[i] & ~(NPL - 1u)) | static_cast<uint32_t>(NPL - 1 - i);
 #pragma unroll
     for (int p = 1; p < NPL; p <<= 1)
 #pragma unroll
@@ -169,9 +169,11 @@ __device__ __forceinline__ void pack_and_sort(uint32_t (&key)[NPL])
                         key[i + j + q] = min(a, b);
                     }
 }
+// close: two consecutive values (the one after the last round included) are no further apart than
+// `error` times 1 + the larger magnitude.
 template <int NPL>
 __device__ __forceinline__ int take_best(uint32_t (&key)[NPL], int rounds, int lane, uint2* found,
-                                         float& gap)
+                                         float error, bool& close)
 {
     constexpr uint32_t kPlace = NPL - 1u;
     const uint32_t lower = (1u << lane) - 1u;
@@ -179,7 +181,6 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[NPL], int rounds, int l
     for (int r = 0; r <= rounds; ++r) {
         const uint32_t first = key[0] & ~kPlace;
         const uint32_t top = __reduce_max_sync(kAll, first);
-        // the lowest lane that holds it writes it down and moves up
         const unsigned holders = __ballot_sync(kAll, first == top);
         if (first == top && !(holders & lower)) {
             found[r] = make_uint2(top, lane * NPL + (kPlace - (key[0] & kPlace)));
@@ -189,16 +190,19 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[NPL], int rounds, int l
         }
     }
     __syncwarp();
-    // lane r looks at the values of rounds r and r + 1 (0: nothing was left)
+    // lane r looks at the values of rounds r and r + 1
     int mine = -1;
+    bool near = false;
     if (lane < rounds) {
         const uint2 a = found[lane];
         const uint32_t next = found[lane + 1].x;
-        if (a.x) mine = static_cast<int>(a.y);
-        if (next) gap = fminf(gap, key_value(a.x) - key_value(next));
+        if (a.x >= kFirstKey) mine = static_cast<int>(a.y);
+        if (next >= kFirstKey) {
+            const float u = key_value(a.x), v = key_value(next);
+            near = !(u - v > error * (1.0f + fmaxf(fabsf(u), fabsf(v))));
+        }
     }
-    // gaps are not negative: their order is that of their bits
-    gap = __uint_as_float(__reduce_min_sync(kAll, __float_as_uint(gap)));
+    close = __any_sync(kAll, near);
     return mine;
 }
 
@@ -216,63 +220,47 @@ struct RouteArgs {
     int* dev_status;
 };
 
-// The lane's keys of the choice v = s + bias, s in FP64 or, for a float key, by the fast intrinsics.
-// bad: a value was NaN or +inf.
-template <int NPL, typename F, typename Key>
-__device__ __forceinline__ void choice_keys(const RouteArgs& a, const float (&x)[NPL], float mx,
-                                            int lane, F (&s)[NPL], Key (&key)[NPL], bool& bad)
-{
-    constexpr bool FAST = sizeof(F) == 4;
-    F sum = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        if constexpr (FAST)
-            s[i] = a.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x[i])) : __expf(x[i] - mx);
-        else
-            s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x[i])))
-                             : exp(static_cast<double>(x[i]) - static_cast<double>(mx));
-        sum += s[i];
-    }
-    if (!a.sigmoid) {
-        const F inv = F(1) / warp_sum(sum);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] *= inv;
-    }
-    float b[NPL];
-    if (a.bias) load_values<NPL>(a.bias, lane, a.E, a.wide, b);
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        key[i] = 0;
-        if (a.bias) s[i] += F(b[i]);
-        if (x[i] > -INFINITY) {  // false behind the last expert too
-            nan |= !(s[i] < F(INFINITY));
-            if (s[i] > -F(INFINITY)) key[i] = order_key(s[i]);
-        }
-    }
-    bad = __any_sync(kAll, nan);
-}
+// Fast choice by FP32 scores s + bias.  close: some comparison was too close to call, and the choice
+// has to be made in FP64.  An FP32 score is off by at most 10 units of 2^-23 (exp by its
+// intrinsic: 2 + 1.2 |d| units at an argument d, times s; the sum of up to 512; the quotient; the
+// bias), and the keys give way up to 15 units of the value to the place: two values are told
+// apart from 2^-18 of 1 + the larger on, sums of two from twice that.  bad: a value was NaN or
+// +inf.
+constexpr float kScoreError = 0x1p-18f;
 
-// Fast choice by FP32 scores.  close: some comparison was too close to call, and the choice has to
-// be made in FP64.  An FP32 score is off by at most 10 units of 2^-23 (exp by its intrinsic: 2 +
-// 1.2 |d| units at an argument d, times s; the sum of up to 512; the quotient; the bias), and the
-// keys give way up to 15 units of the value to the place: two values are told apart from 2^-18 of
-// 1 + the largest on, sums of two from twice that.
 template <int NPL>
 __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[NPL], float mx,
                                            int lane, uint2* found, bool& close, bool& bad)
 {
+    constexpr uint32_t kPlace = NPL - 1u;
     float s[NPL];
-    uint32_t key[NPL];
-    choice_keys<NPL>(a, x, mx, lane, s, key, bad);
-    if (bad) return -1;
-    float largest = 0.0f;
+    if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-        if (key[i]) largest = fmaxf(largest, fabsf(s[i]));
-    largest = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(largest)));
+        for (int i = 0; i < NPL; ++i) s[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
+    } else {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            s[i] = __expf(x[i] - mx);
+            sum += s[i];
+        }
+        const float inv = 1.0f / warp_sum(sum);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] *= inv;
+    }
+    if (a.bias) {
+        float b[NPL];
+        load_values<NPL>(a.bias, lane, a.E, a.wide, b);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] += b[i];
+    }
+    uint32_t key[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) key[i] = order_key(x[i] > -INFINITY ? s[i] : -INFINITY);
     pack_and_sort<NPL>(key);
-    float gap = INFINITY;
+    bad = __any_sync(kAll, (key[0] & ~kPlace) >= kBadKey);
+    if (bad) return -1;
+    bool close_groups = false;
     if (a.groups > 1) {
         // the group's two best: the lane's own, then across the group's lanes
         uint32_t m1 = key[0], m2 = NPL > 1 ? key[NPL > 1 ? 1 : 0] : 0u;
@@ -281,9 +269,9 @@ __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[
             m2 = max(min(m1, o1), max(m2, o2));
             m1 = max(m1, o1);
         }
-        constexpr uint32_t kPlace = NPL - 1u;
-        float score = m1 ? key_value(m1 & ~kPlace) : -INFINITY;
-        if (m2) score += key_value(m2 & ~kPlace);
+        const float v1 = key_value(m1 & ~kPlace), v2 = key_value(m2 & ~kPlace);
+        const bool any = m1 >= kFirstKey, two = m2 >= kFirstKey;
+        const float score = any ? (two ? v1 + v2 : v1) : -INFINITY;
         // rank of this lane's group among all
         const int mine = lane / a.group_lanes;
         int rank = 0;
@@ -291,18 +279,22 @@ __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[
             const float o = __shfl_sync(kAll, score, g * a.group_lanes);
             rank += (o > score || (o == score && g < mine)) ? 1 : 0;
         }
-        const bool kept = mine < a.groups && rank < a.top_groups;
-        const uint32_t okey = score > -INFINITY ? order_key(score) : 0u;
-        const uint32_t low = __reduce_min_sync(kAll, kept && okey ? okey : 0xFFFFFFFFu);
+        const bool kept = rank < a.top_groups;
+        const uint32_t okey = any ? order_key(score) : 0u;
+        const uint32_t low = __reduce_min_sync(kAll, kept && any ? okey : 0xFFFFFFFFu);
         const uint32_t high = __reduce_max_sync(kAll, kept || mine >= a.groups ? 0u : okey);
-        if (high && low != 0xFFFFFFFFu) gap = 0.5f * (key_value(low) - key_value(high));
+        const uint32_t size =
+            __reduce_max_sync(kAll, any ? __float_as_uint(fabsf(v1) + (two ? fabsf(v2) : 0.0f)) : 0u);
+        if (high && low != 0xFFFFFFFFu)
+            close_groups = !(key_value(low) - key_value(high) >
+                             2.0f * kScoreError * (1.0f + __uint_as_float(size)));
         if (!kept) {
 #pragma unroll
             for (int i = 0; i < NPL; ++i) key[i] = 0;
         }
     }
-    const int mine = take_best<NPL>(key, a.k, lane, found, gap);
-    close = gap < 0x1p-18f * (1.0f + largest);
+    const int mine = take_best<NPL>(key, a.k, lane, found, kScoreError, close);
+    close |= close_groups;
     return mine;
 }
 
@@ -311,9 +303,30 @@ template <int NPL>
 __device__ __noinline__ int choose_exact(const RouteArgs& a, const float (&x)[NPL], float mx,
                                          int lane, double* values, bool& bad)
 {
-    double s[NPL];
+    double s[NPL], sum = 0.0;
     unsigned long long key[NPL];
-    choice_keys<NPL>(a, x, mx, lane, s, key, bad);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        s[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x[i])))
+                         : exp(static_cast<double>(x[i]) - static_cast<double>(mx));
+        sum += s[i];
+    }
+    if (!a.sigmoid) {
+        sum = warp_sum(sum);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] /= sum;
+    }
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        key[i] = 0;
+        if (x[i] > -INFINITY) {  // false behind the last expert too
+            if (a.bias) s[i] += __ldg(a.bias + lane * NPL + i);
+            nan |= !(s[i] < INFINITY);
+            if (s[i] > -INFINITY) key[i] = order_key(s[i]);
+        }
+    }
+    bad = __any_sync(kAll, nan);
     if (bad) return -1;
     if (a.groups > 1) {
         const int size = a.E / a.groups;
@@ -362,14 +375,14 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
     float x[NPL];
     load_values<NPL>(row, lane, a.E, a.wide, x);
     bool bad = false;
-    uint32_t top = 0;
+    float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         bad |= !(x[i] < INFINITY);
-        top = max(top, order_key(x[i]));
+        mx = fmaxf(mx, x[i]);
     }
     bad = __any_sync(kAll, bad);
-    const float mx = key_value(__reduce_max_sync(kAll, top));
+    mx = key_value(__reduce_max_sync(kAll, order_key(mx)));
     int expert = -1;
     if (!bad && mx > -INFINITY) {
         if (!a.bias && a.groups == 1) {
@@ -378,11 +391,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
             // by the whole keys.
             uint32_t key[NPL];
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
+            for (int i = 0; i < NPL; ++i) key[i] = order_key(x[i]);
             pack_and_sort<NPL>(key);
-            float gap = INFINITY;
-            expert = take_best<NPL>(key, a.k, lane, found[warp], gap);
-            if (sizeof(T) == 4 && !(gap > 0.0f)) {
+            bool equal;
+            expert = take_best<NPL>(key, a.k, lane, found[warp], 0.0f, equal);
+            if (sizeof(T) == 4 && equal) {
 #pragma unroll
                 for (int i = 0; i < NPL; ++i) key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
                 expert = select_best<NPL>(key, a.k, lane);
@@ -614,7 +627,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
         int sum = 0, prior = 0;
         if (a.counts) {
-#pragma unroll 8
+#pragma unroll 32
             for (int c = 0; c < chunks; ++c) {
                 const int n = a.counts[static_cast<int64_t>(c) * a.E + e];
                 if (c < chunk) prior += n;
