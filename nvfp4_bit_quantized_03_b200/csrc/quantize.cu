@@ -902,12 +902,15 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
     return largest;
 }
 
-// Row-wise codes and scales of an expert-ordered matrix.  A warp takes 1024 columns of a row, a lane
-// 32 of them: two whole blocks, so no maximum crosses lanes, and one 16-byte store of codes.
-//  * SCATTER (gathered, round to nearest): the warp takes a row of x, quantizes it once and writes
-//    it to the row of every expert that takes it; the rows without a token are zeroed after.
-//  * otherwise the warp takes a row of the expert-ordered matrix (stochastic rounding draws other
-//    bits for every such row).
+// Row-wise codes and scales of an expert-ordered matrix.  A lane takes spans of 32 columns: two whole
+// blocks, so no maximum crosses lanes, and one 16-byte store of codes.  The spans of all rows are one
+// list that the warps go through 32 at a time, so that rows of any length fill the lanes; a span's
+// row and place are kept up to date without dividing.
+//  * SCATTER (gathered, round to nearest): the list is that of x; a span is quantized once and
+//    written to the row of every expert that takes its token.  The rows without a token are zeroed
+//    after.
+//  * otherwise the list is that of the expert-ordered matrix (stochastic rounding draws other bits
+//    for every such row).
 // Rows behind the last region are not written.
 template <bool SR, bool SCATTER>
 __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
@@ -938,68 +941,70 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int64_t wfirst = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t spr = cols >> 5, gpr = cols >> 6;  // lanes' spans and scale words per row
-    const int64_t segs = (spr + 31) >> 5;            // warps' pieces of a row
     const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
     const int64_t cb = codes_extent(rows, cols), sb = scales_extent(rows, cols);
     const int64_t used = map.used_rows(rows);
-    // word: four blocks' scales, in the even lanes
+    // word: four blocks' scales, in the even lanes (rows hold an even number of spans)
     auto store = [&](int64_t r, int64_t span, const uint4& w, uint32_t word) {
         st_checked(reinterpret_cast<uint4*>(codes) + r * spr + span, w, codes, cb, dev_status);
         if ((lane & 1) == 0)
             st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, span << 1, gpr)), word, scales,
                        sb, dev_status);
     };
-    auto quantize = [&](const uint4* v, int64_t r, int64_t span, uint4& w, uint32_t& word) {
-        uint32_t out[4], sf[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float y[16];
-            unpack8(v[2 * b], y);
-            unpack8(v[2 * b + 1], y + 8);
-            const BlockScale bs = block_scale(absmax_f32<16>(y), ts.s_enc, r_tab);
-            encode16<SR>(y, bs, philox, static_cast<uint64_t>(r * cols + 32 * span + 16 * b), offset,
-                         out[2 * b], out[2 * b + 1]);
-            sf[b] = bs.sf;
-        }
-        w = ts.nonfinite ? make_uint4(0, 0, 0, 0) : make_uint4(out[0], out[1], out[2], out[3]);
-        const uint32_t pair = ts.nonfinite ? 0u : sf[0] | (sf[1] << 8);
-        word = pair | (__shfl_down_sync(0xFFFFFFFFu, pair, 1) << 16);
-    };
-    const int64_t source_rows = SCATTER ? map.tokens : used;
-    for (int64_t i = wfirst; i < source_rows * segs; i += wstride) {
-        const int64_t row = i / segs, span = (i - row * segs) * 32 + lane;
-        int target = -1;  // SCATTER: lane j holds the row of the token's j-th expert
-        unsigned taken = 0;
-        int64_t from = row;
+    const int64_t list_rows = SCATTER ? map.tokens : used, total = list_rows * spr;
+    const int64_t step = wstride * 32, dq = step / spr, dr = step - dq * spr;
+    int64_t f = wfirst * 32 + lane, row = f / spr, span = f - row * spr;
+    for (int64_t first = wfirst * 32; first < total; first += step) {
+        const bool in = row < list_rows;
+        int64_t from = -1;
         if (SCATTER) {
-            if (lane < map.k) target = static_cast<int>(map.pair_target(row, lane, rows));
-            taken = __ballot_sync(0xFFFFFFFFu, target >= 0);
-            if (taken == 0) continue;
-        } else {
+            if (in) from = row;  // a token without an expert is read and stored nowhere
+        } else if (in) {
             from = map.source(row);
-            if (from < 0) {  // a row without a token
-                if (span < spr) store(row, span, make_uint4(0, 0, 0, 0), 0u);
-                continue;
-            }
         }
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             v[u] = make_uint4(0, 0, 0, 0);
-            if (span < spr)
+            if (from >= 0)
                 v[u] = ldg_checked(reinterpret_cast<const uint4*>(x + from * ld) + 4 * span + u, x, xb,
                                    dev_status);
         }
-        uint4 w;
-        uint32_t word;
-        quantize(v, row, span, w, word);
-        if (SCATTER) {
-            for (unsigned left = taken; left; left &= left - 1) {
-                const int r = __shfl_sync(0xFFFFFFFFu, target, __ffs(left) - 1);
-                if (span < spr) store(r, span, w, word);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        uint32_t pair = 0;
+        if (!SR || __any_sync(0xFFFFFFFFu, from >= 0)) {
+            uint32_t out[4], sf[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float y[16];
+                unpack8(v[2 * b], y);
+                unpack8(v[2 * b + 1], y + 8);
+                const BlockScale bs = block_scale(absmax_f32<16>(y), ts.s_enc, r_tab);
+                encode16<SR>(y, bs, philox, static_cast<uint64_t>(row * cols + 32 * span + 16 * b),
+                             offset, out[2 * b], out[2 * b + 1]);
+                sf[b] = bs.sf;
             }
-        } else if (span < spr) {
+            if (!ts.nonfinite && from >= 0) {
+                w = make_uint4(out[0], out[1], out[2], out[3]);
+                pair = sf[0] | (sf[1] << 8);
+            }
+        }
+        const uint32_t word = pair | (__shfl_down_sync(0xFFFFFFFFu, pair, 1) << 16);
+        if (SCATTER) {
+            if (in) {
+                for (int64_t j = 0; j < map.k; ++j) {
+                    const int64_t r = map.pair_target(row, j, rows);
+                    if (r >= 0) store(r, span, w, word);
+                }
+            }
+        } else if (in) {
             store(row, span, w, word);
+        }
+        row += dq;
+        span += dr;
+        if (span >= spr) {
+            span -= spr;
+            ++row;
         }
     }
     if (SCATTER) {
@@ -1216,7 +1221,7 @@ cudaError_t launch_quant_grouped_rows(const TileArgs& a, bool sr, int sm_count, 
                                     resident_ctas(kernels[2], 256)};
     const int which = scatter ? 2 : (sr ? 1 : 0);
     const int64_t n = scatter && a.map.tokens > a.rows ? a.map.tokens : a.rows;
-    int64_t grid = (n * ((a.cols + 1023) / 1024) + 7) / 8;
+    int64_t grid = (n * (a.cols / 32) + 255) / 256;
     if (grid > static_cast<int64_t>(sm_count) * resident[which]) grid = static_cast<int64_t>(sm_count) * resident[which];
     // the amax pass is ahead of it, unless the amax is given or computed here
     const bool chained = a.src.n_partials > 0;
