@@ -1010,7 +1010,7 @@ def run_experts(args):
     token), forward and backward, with the time of each operator.  Prints one JSON line (not the
     benchmark's headline line)."""
     import torch
-    wl = synth.experts_layer()
+    wl = synth.experts_layer_small() if args.experts_small else synth.experts_layer()
     step = ExpertsStep(wl, torch.device("cuda", torch.cuda.current_device()))
     for _ in range(args.warmup):
         step.run()
@@ -1059,6 +1059,8 @@ def main(argv=None):
     ap.add_argument("--workload", choices=["mlp12b", "dense8b", "experts"], default="mlp12b",
                     help="dense8b: the 8B-class layer stack (4 NVFP4 layers + 1 bf16 layer); "
                          "experts: a mixture-of-experts layer; each on its own JSON line")
+    ap.add_argument("--experts-small", action="store_true",
+                    help="the experts workload at 2048 tokens, 16 experts, 4 per token (profiling)")
     args = ap.parse_args(argv)
     args.warmup = max(args.warmup, 3)  # at least 3 untimed warm-up steps
     if args.impl == "reference":

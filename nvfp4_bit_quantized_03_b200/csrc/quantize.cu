@@ -765,7 +765,8 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
 // ------------------------------------------------------------------------------------------
 
 // Partial maxima of |x| over the rows of x that some expert takes: a warp per row, four loads in
-// flight per lane.  A row of x is read once, however many experts take it.
+// flight per lane.  A row of x is read once, however many experts take it.  Bound by HBM: B200,
+// 73000 x 4096 in expert order 97 us (6.2 TB/s); 8192 gathered tokens of 4096 16 us.
 __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __restrict__ x,
                                                            int64_t rows, int64_t cols, int64_t ld,
                                                            uint32_t* __restrict__ partials,
@@ -802,7 +803,8 @@ __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __res
 
 // The same of the random Hadamard transform along the expert-ordered rows (and, with PLAIN, of the
 // rows themselves): a warp takes 16 rows x 128 columns; its lanes look up one row each and pass
-// the places on.
+// the places on.  Bound by instruction issue (the transform and its unpacking).  B200, 36700 rows:
+// of 4096 columns 63 us, of 2048 31 us; four CTAs per SM instead of three, with spills, 7 % more.
 template <bool PLAIN>
 __global__ void __launch_bounds__(256) amax_rht_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, uint32_t sign_mask,
@@ -912,6 +914,11 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
 //  * otherwise the list is that of the expert-ordered matrix (stochastic rounding draws other bits
 //    for every such row).
 // Rows behind the last region are not written.
+// B200: 8192 tokens of 4096 to 8 experts each (67 MB in, 151 MB out) 62 us.  The stores bound it: with
+// none 32 us, with the codes' alone 50; a token's scale words lie 512 bytes apart in the MMA
+// layout.  Codes sent out as bulk copies from shared memory, or the rows looked up ahead, take the
+// same time.  Stochastic, bound by issue: 73000 x 4096 294 us (the row-wise pass of the linear layer
+// does as many elements per second), 7000 x 1536 15.6 us.
 template <bool SR, bool SCATTER>
 __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, QuantSource src,
@@ -1190,8 +1197,8 @@ int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, i
 bool grouped_amax_is_small(int64_t cols, const RowMap& map)
 {
     // Every CTA reads these tokens from L2.  B200, 64 experts, 8 per token, computed here against in
-    // a pass of its own: 1 x 4096 5.7 against 7.3 us, 2 x 4096 7.0 / 8.5, 4 x 4096 9.5 / 9.2, 4 x 2048
-    // 7.0 / 7.5, 8 x 2048 8.6 / 7.9.  Matrices in expert order gain nothing (1 token: 5.9 / 5.3).
+    // a pass of its own: 1 x 4096 6.0 against 7.8 us, 2 x 4096 7.6 / 9.2, 4 x 4096 9.6 / 9.7, 4 x 2048
+    // 7.3 / 8.0, 8 x 2048 8.8 / 8.4.  Matrices in expert order gain nothing (1 token: 5.9 / 5.3).
     return map.gather && map.tokens * cols <= kSmallElements;
 }
 

@@ -362,7 +362,12 @@ __device__ __noinline__ int choose_exact(const RouteArgs& a, const float (&x)[NP
     return select_best<NPL>(key, a.k, lane);
 }
 
-// A warp per token; lane l holds the logits of experts l * NPL .. l * NPL + NPL - 1.
+// A warp per token; lane l holds the logits of experts l * NPL .. l * NPL + NPL - 1, so that the
+// lowest lane with a value has the lowest index and a row is read in 16-byte loads.  Bound by
+// instruction issue: a token of 256 experts takes 857 instructions (scores 160, sort 40, groups
+// 90, k + 1 rounds of about 20, weights 100).  B200: 16384 x 256 FP32 logits, sigmoid, bias, 4 of 8
+// groups, k 8: 26.5 us (51 us with the rounds searching unsorted keys and exact scores); one
+// token 2.8 us, a launch.
 template <int NPL, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
 {
@@ -461,6 +466,8 @@ struct RouteBackwardArgs {
 //   sigmoid, renormalised: dl_i = p_i (1 - s_i) (g_i - sum_S g p) on S
 //   sigmoid:               dl_i = g_i s_i (1 - s_i)               on S
 // A warp per token; lane j holds the j-th chosen expert.  A row without one has zero gradient.
+// Renormalised weights need only the chosen logits, so a row is written and, but for them, not
+// read.  B200: 8192 x 128 bf16 4.2 us, of which a launch is 2.
 template <int NPL, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const RouteBackwardArgs a)
 {
@@ -564,7 +571,10 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
 
 // ---- the plan of the expert-ordered rows ---------------------------------------------------
 // A stable counting sort of the pairs (t, j) by expert, regions padded to 128 rows.  A CTA takes
-// kPlanPairs consecutive pairs, a warp an eighth of them in order.
+// kPlanPairs consecutive pairs, a warp an eighth of them in order; more pairs are counted by a pass
+// ahead, and each CTA adds up the counts of the chunks before its own.  Integer counts only, so the
+// order of the atomics does not show.  A chain of short latencies: B200, 131072 pairs of 256
+// experts 3.1 + 10.4 us, one token 3.2 us.
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 
 struct PlanArgs {

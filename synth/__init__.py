@@ -140,6 +140,11 @@ def experts_layer() -> ExpertsLayer:
     return ExpertsLayer("experts_t8192_d4096_f2048_e64_k8", 5, 8192, 4096, 2048, 64, 8)
 
 
+def experts_layer_small() -> ExpertsLayer:
+    """The same widths with 2048 tokens and 16 experts, 4 per token: fits a profiler's replays."""
+    return ExpertsLayer("experts_t2048_d4096_f2048_e16_k4", 5, 2048, 4096, 2048, 16, 4)
+
+
 QUANT_SWEEP_SEED = 3
 QUANT_SWEEP_ROW = 4096
 QUANT_SWEEP_LOG2 = list(range(20, 31))
