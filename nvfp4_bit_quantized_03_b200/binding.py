@@ -240,6 +240,8 @@ class QuantizedTensor:
                              "one float32 amax")
         q = cls.__new__(cls)
         q.rows, q.cols = codes.shape[0], 2 * codes.shape[1]
+        if scales.device != codes.device or amax.device != codes.device:
+            raise ValueError("an operand's codes, scales and amax are on one device")
         if scales.numel() < scales_bytes(q.rows, q.cols):
             raise ValueError(f"scales: {scales.numel()} bytes are too few for {q.rows} x {q.cols}")
         q.codes, q.scales, q.amax = codes, scales, amax
@@ -506,6 +508,12 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+def _workspace_size(workspace, need):
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError(f"the workspace has {have} bytes, the call needs {need}")
+
+
 _F32_BF16 = (torch.float32, torch.bfloat16)
 _BF16 = (torch.bfloat16,)
 
@@ -534,6 +542,8 @@ class ExpertPlan:
                              ("row_token", row_token, 1)):
             if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
                 raise ValueError(f"plan: {name} must be a contiguous int32 tensor of {dim} dimensions")
+        if pair_row.device != offsets.device or row_token.device != offsets.device:
+            raise ValueError("plan: its tensors are on one device")
         self.offsets, self.pair_row, self.row_token = offsets, pair_row, row_token
         self.tokens, self.k = pair_row.shape
         self.experts, self.rows = offsets.shape[0] - 1, row_token.shape[0]
@@ -566,7 +576,7 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=Tr
             weights = _new((T, max(k, 0)), torch.float32, logits.device)
     _dense("experts", experts, torch.int32, (T, k))
     _dense("weights", weights, torch.float32, (T, k))
-    queue = _queue("nvfp4_route", stream, logits, bias, experts, weights)
+    queue = _queue("nvfp4_route", stream, logits, bias, experts, weights, dev_status)
     _check(lib().nvfp4_route(_address(logits), _dtype_code(logits.dtype), T, E, _row_stride(logits),
                              _address(bias), int(bool(sigmoid)), groups, top_groups, k, int(bool(renorm)),
                              scale, _address(experts), _address(weights), _address(dev_status),
@@ -586,7 +596,7 @@ def route_backward(logits, experts, dweights, sigmoid=False, renorm=True, scale=
         with _allocating(stream):
             dlogits = _poisoned(_new((T, E), logits.dtype, logits.device))
     _matrix("dlogits", dlogits, (logits.dtype,), T, E)
-    queue = _queue("nvfp4_route_backward", stream, logits, experts, dweights, dlogits)
+    queue = _queue("nvfp4_route_backward", stream, logits, experts, dweights, dlogits, dev_status)
     _check(lib().nvfp4_route_backward(_address(logits), _dtype_code(logits.dtype), T, E,
                                       _row_stride(logits), _address(experts), _address(dweights),
                                       int(bool(sigmoid)), k, int(bool(renorm)), scale,
@@ -605,9 +615,10 @@ def expert_plan(experts, n_experts, plan=None, workspace=None, dev_status=None, 
         if workspace is None:
             workspace = _workspace(lib().nvfp4_expert_plan_workspace_bytes(T, k, n_experts),
                                    experts.device)
+    _workspace_size(workspace, lib().nvfp4_expert_plan_workspace_bytes(T, k, n_experts))
     if (plan.tokens, plan.k, plan.experts) != (T, k, n_experts):
         raise ValueError(f"plan is for {plan.tokens} tokens, {plan.k} of {plan.experts} experts")
-    queue = _queue("nvfp4_plan_experts", stream, experts, plan.offsets, plan.pair_row, plan.row_token)
+    queue = _queue("nvfp4_plan_experts", stream, experts, plan.offsets, workspace, dev_status)
     _check(lib().nvfp4_plan_experts(_address(experts), plan.ref, _address(workspace),
                                     _address(dev_status), queue), "nvfp4_plan_experts")
     return plan
@@ -630,7 +641,9 @@ def quantize_grouped(x, plan, flags, sign_mask=0, seed=0, offset=0, out_row=None
             out_col = QuantizedTensor(cols, plan.rows, x.device)
         if workspace is None:
             workspace = _workspace(workspace_bytes(plan.rows, cols, flags), x.device)
-    queue = _queue("nvfp4_quantize_grouped", stream, x, plan.offsets)
+    _workspace_size(workspace, workspace_bytes(plan.rows, cols, flags))
+    queue = _queue("nvfp4_quantize_grouped", stream, x, plan.offsets, workspace, dev_status,
+                   out_row and out_row.codes, out_col and out_col.codes)
     op_r = out_row.operand() if out_row is not None else None
     op_c = out_col.operand() if out_col is not None else None
     _check(lib().nvfp4_quantize_grouped(
@@ -655,7 +668,7 @@ def gemm_grouped(A, W, plan, out=None, out_dtype=torch.bfloat16, dev_status=None
     E = plan.experts
     N = W.rows // E if W.cols == A.cols and W.rows % E == 0 else W.rows
     out = _grouped_out("out", out, plan.rows, N, out_dtype, A.codes.device, stream)
-    queue = _queue("nvfp4_gemm_grouped", stream, A.codes, W.codes, plan.offsets, out)
+    queue = _queue("nvfp4_gemm_grouped", stream, A.codes, W.codes, plan.offsets, out, dev_status)
     oa, ob = A.operand(), W.operand()
     _check(lib().nvfp4_gemm_grouped(ctypes.byref(oa), ctypes.byref(ob), plan.ref,
                                     _address(out), _dtype_code(out.dtype), _row_stride(out),
@@ -666,7 +679,7 @@ def gemm_grouped(A, W, plan, out=None, out_dtype=torch.bfloat16, dev_status=None
 def gemm_grouped_k(A, B, plan, out=None, out_dtype=torch.float32, dev_status=None, stream=None):
     """nvfp4_gemm_grouped_k: D_e = A . B^T over expert e's rows, [(E * A.rows) x B.rows]."""
     out = _grouped_out("out", out, plan.experts * A.rows, B.rows, out_dtype, A.codes.device, stream)
-    queue = _queue("nvfp4_gemm_grouped_k", stream, A.codes, B.codes, plan.offsets, out)
+    queue = _queue("nvfp4_gemm_grouped_k", stream, A.codes, B.codes, plan.offsets, out, dev_status)
     oa, ob = A.operand(), B.operand()
     _check(lib().nvfp4_gemm_grouped_k(ctypes.byref(oa), ctypes.byref(ob),
                                       plan.ref, _address(out), _dtype_code(out.dtype),
@@ -676,11 +689,11 @@ def gemm_grouped_k(A, B, plan, out=None, out_dtype=torch.float32, dev_status=Non
 
 
 def _experts_workspace(workspace, plan, I, O, device, stream):
+    need = experts_workspace_bytes(plan, I, O)
     if workspace is None:
         with _allocating(stream):
-            workspace = _workspace(experts_workspace_bytes(plan, I, O), device)
-    elif workspace.numel() * workspace.element_size() < experts_workspace_bytes(plan, I, O):
-        raise ValueError("workspace is smaller than experts_workspace_bytes")
+            return _workspace(need, device)
+    _workspace_size(workspace, need)
     return workspace
 
 
@@ -692,7 +705,7 @@ def experts_fprop(X, W, plan, gather=True, out=None, out_dtype=torch.bfloat16, w
     I, O = W.cols, W.rows // plan.experts
     out = _grouped_out("out", out, plan.rows, O, out_dtype, X.device, stream)
     workspace = _experts_workspace(workspace, plan, I, O, X.device, stream)
-    queue = _queue("nvfp4_experts_fprop", stream, X, W.codes, plan.offsets, out, workspace)
+    queue = _queue("nvfp4_experts_fprop", stream, X, W.codes, plan.offsets, out, workspace, dev_status)
     op = W.operand()
     _check(lib().nvfp4_experts_fprop(_address(X), _row_stride(X), int(bool(gather)), ctypes.byref(op),
                                      plan.ref, I, O, _address(out),
@@ -709,7 +722,7 @@ def experts_dgrad(dY, Wt, plan, seed, offset, out=None, out_dtype=torch.bfloat16
     _matrix("dY", dY, _BF16, plan.rows, O)
     out = _grouped_out("out", out, plan.rows, I, out_dtype, dY.device, stream)
     workspace = _experts_workspace(workspace, plan, I, O, dY.device, stream)
-    queue = _queue("nvfp4_experts_dgrad", stream, dY, Wt.codes, plan.offsets, out, workspace)
+    queue = _queue("nvfp4_experts_dgrad", stream, dY, Wt.codes, plan.offsets, out, workspace, dev_status)
     op = Wt.operand()
     _check(lib().nvfp4_experts_dgrad(_address(dY), _row_stride(dY), ctypes.byref(op),
                                      plan.ref, I, O, seed, offset, _address(out),
@@ -727,7 +740,7 @@ def experts_wgrad(dY, X, plan, sign_mask, seed, offset, gather=True, out=None,
     I, O = X.shape[1], dY.shape[1]
     out = _grouped_out("out", out, plan.experts * O, I, out_dtype, dY.device, stream)
     workspace = _experts_workspace(workspace, plan, I, O, dY.device, stream)
-    queue = _queue("nvfp4_experts_wgrad", stream, dY, X, plan.offsets, out, workspace)
+    queue = _queue("nvfp4_experts_wgrad", stream, dY, X, plan.offsets, out, workspace, dev_status)
     _check(lib().nvfp4_experts_wgrad(_address(dY), _row_stride(dY), _address(X), _row_stride(X),
                                      int(bool(gather)), plan.ref, I, O, sign_mask,
                                      seed, offset, _address(out), _dtype_code(out.dtype),
@@ -742,7 +755,7 @@ def combine(Y, plan, weights=None, out=None, out_dtype=torch.bfloat16, dev_statu
     if weights is not None:
         _dense("weights", weights, torch.float32, (plan.tokens, plan.k))
     out = _grouped_out("out", out, plan.tokens, Y.shape[1], out_dtype, Y.device, stream)
-    queue = _queue("nvfp4_combine", stream, Y, plan.pair_row, weights, out)
+    queue = _queue("nvfp4_combine", stream, Y, plan.pair_row, weights, out, dev_status)
     _check(lib().nvfp4_combine(_address(Y), Y.shape[1], _row_stride(Y), plan.ref,
                                _address(weights), _address(out), _dtype_code(out.dtype), _row_stride(out),
                                _address(dev_status), queue), "nvfp4_combine")
@@ -762,7 +775,7 @@ def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=
             dweights = _poisoned(_new((plan.tokens, plan.k), torch.float32, Y.device))
     _matrix("dy", dy, _BF16, plan.rows, cols)
     _dense("dweights", dweights, torch.float32, (plan.tokens, plan.k))
-    queue = _queue("nvfp4_combine_backward", stream, dout, Y, plan.pair_row, weights, dy, dweights)
+    queue = _queue("nvfp4_combine_backward", stream, dout, Y, plan.pair_row, weights, dy, dweights, dev_status)
     _check(lib().nvfp4_combine_backward(_address(dout), _dtype_code(dout.dtype), _row_stride(dout),
                                         _address(Y), cols, _row_stride(Y), plan.ref,
                                         _address(weights), _address(dy), _row_stride(dy), _address(dweights),

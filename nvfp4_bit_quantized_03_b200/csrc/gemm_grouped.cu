@@ -370,6 +370,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // slot's scales in tensor memory (which they do after the slot's TMA bytes landed);
         // then meet the issuer.  After an abort (or a timeout here) it stops waiting but keeps
         // meeting the issuer, K block for K block.
+        // (every role that waits with a time limit starts its clock when the kernel ahead has ended)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         int stage = 0, it = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -402,6 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // l + 96, so lane l of each quarter's warp loads 16 bytes per tile and stores them.
         // Row groups beyond M or N and K tiles beyond K arrive zero-filled from the scale maps,
         // so padding rows (whose codes are zero-filled too) multiply to zero, never to NaN.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         const int q = warp & 3;
         int stage = 0;
         uint32_t phase = 0;

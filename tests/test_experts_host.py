@@ -255,6 +255,17 @@ def test_binding_refuses_wrong_tensors_before_calling():
         B.QuantizedTensor.from_buffers(W.codes, W.scales[:-1], W.amax)
     with pytest.raises(ValueError):
         B.QuantizedTensor.from_buffers(W.codes.t(), W.scales, W.amax)
+    with pytest.raises(ValueError):  # one device
+        B.QuantizedTensor.from_buffers(W.codes, W.scales, W.amax.to("meta"))
+    with pytest.raises(ValueError):
+        B.ExpertPlan(plan.offsets, plan.pair_row, plan.row_token.to("meta"))
+    big = torch.zeros(2048, 4, dtype=torch.int32)
+    with pytest.raises(ValueError):  # workspaces too small
+        B.expert_plan(big, 4, plan=B.ExpertPlan.empty(2048, 4, 4, device="cpu"),
+                      workspace=torch.zeros(16, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        B.quantize_grouped(y, plan, B.ROWWISE, workspace=torch.zeros(16, dtype=torch.uint8),
+                           out_row=B.QuantizedTensor(plan.rows, 64, device="cpu"))
     q = B.QuantizedTensor.from_buffers(W.codes, W.scales, W.amax)
     assert (q.rows, q.cols) == (W.rows, W.cols)
 

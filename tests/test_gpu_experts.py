@@ -777,3 +777,110 @@ def test_a_plan_of_another_routing_stays_inside_the_buffers():
                        torch.ones(40, 2, device="cuda"), dev_status=st)
     torch.cuda.synchronize()
     assert int(st) & ~B.DEVSTAT_NONFINITE == 0
+
+
+def test_expanded_rows_are_refused():
+    plan = B.expert_plan(torch.zeros(8, 1, dtype=torch.int32, device="cuda"), 2)
+    x = torch.ones(1, 64, dtype=torch.bfloat16, device="cuda").expand(8, 64)
+    with pytest.raises(B.NVFP4Error):
+        B.quantize_grouped(x, plan, B.ROWWISE | B.GATHER)
+    with pytest.raises(B.NVFP4Error):
+        B.route(torch.zeros(1, 4, device="cuda").expand(8, 4), 2)
+    with pytest.raises(ValueError):  # a status word on the host
+        B.route(torch.zeros(8, 4, device="cuda"), 2, dev_status=torch.zeros(1, dtype=torch.int32))
+
+
+def test_matrices_past_2_31_elements():
+    """Expert-ordered matrices of more than 2^31 elements: windows of their last rows against the
+    same rows alone."""
+    T, k, E, C = 70000, 8, 64, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    experts = torch.rand(T, E, generator=g, device="cuda").topk(k).indices.int()
+    plan = B.expert_plan(experts, E)
+    assert plan.rows * C > 2 ** 31
+    used = int(plan.offsets[-1])
+    y = torch.empty(plan.rows, C, dtype=torch.bfloat16, device="cuda")
+    for r in range(0, plan.rows, 65536):
+        n = min(65536, plan.rows - r)
+        y[r:r + n] = torch.randn(n, C, generator=g, device="cuda")
+    y[used:] = float("nan")
+    y[:used][plan.row_token[:used] < 0] = 0
+    assert (used - 128) * C > 2 ** 31
+    window = slice(used - 128, used)
+    # the quantizer, row-wise and column-wise
+    st = _status()
+    q, _ = B.quantize_grouped(y, plan, B.ROWWISE, dev_status=st)
+    ref = B.QuantizedTensor(128, C)
+    ref.amax.copy_(q.amax)
+    B.quantize(y[window], B.ROWWISE | B.AMAX_GIVEN, out_row=ref)
+    assert torch.equal(q.codes[window], ref.codes)
+    at = (used - 128) // 128 * 128 * (C // 16)
+    assert torch.equal(q.scales[at:at + ref.scales.numel()], ref.scales)
+    # a product of these rows
+    w = to_device_bf16(synth.weights((E * 128, C), seed=1))
+    qw, _ = B.quantize(w, B.ROWWISE | B.BLOCK2D)
+    D = B.gemm_grouped(q, qw, plan, dev_status=st)
+    last = int(torch.nonzero(plan.offsets[:-1] < used - 1)[-1])
+    wl = B.QuantizedTensor.from_buffers(
+        qw.codes[last * 128:last * 128 + 128],
+        qw.scales[last * 128 * (C // 16):(last + 1) * 128 * (C // 16)], qw.amax)
+    assert torch.equal(D[window], B.gemm(ref, wl, out_dtype=torch.bfloat16))
+    del q, D, qw, w
+    _, q = B.quantize_grouped(y, plan, B.COLWISE, sign_mask=77, dev_status=st)
+    ref = B.QuantizedTensor(C, 128)
+    ref.amax.copy_(q.amax)
+    B.rht_quantize(y[window], 77, B.AMAX_GIVEN, out_col=ref)
+    assert torch.equal(q.codes[:, (used - 128) // 2:used // 2], ref.codes)
+    del q
+    # the combination and its gradient, at the last tokens of the last expert
+    weights = torch.rand(T, k, generator=g, device="cuda")
+    out = B.combine(y, plan, weights, dev_status=st)
+    tokens = plan.row_token[window][plan.row_token[window] >= 0].long()
+    rows = plan.pair_row[tokens].long()
+    exact = (y[rows].double() * weights[tokens].double()[..., None]).sum(1)
+    size = (y[rows].double().abs() * weights[tokens].double()[..., None]).sum(1)
+    tol = (k + 1) * HALF_F32 * size
+    assert ((out[tokens].double() - exact).abs() <= tol + HALF_BF16 * (exact.abs() + tol)).all()
+    dout = torch.randn(T, C, generator=g, device="cuda").bfloat16()
+    dy, _ = B.combine_backward(dout, y, plan, weights, dev_status=st)
+    exact = (dout[tokens].double()[:, None] * weights[tokens].double()[..., None])
+    err = (dy[rows].double() - exact).abs()
+    assert (err <= (HALF_BF16 * (1 + HALF_F32) + HALF_F32) * exact.abs()).all()
+    assert (dy[window][plan.row_token[window] < 0] == 0).all()
+    torch.cuda.synchronize()
+    assert int(st) == 0
+
+
+_COLD_CAPTURE = """
+import torch
+from nvfp4_bit_quantized_03_b200 import binding as B
+torch.manual_seed(0)
+x, l = torch.randn(40, 256, device="cuda").bfloat16(), torch.randn(40, 6, device="cuda")
+q = B.QuantizedTensor(6 * 128, 256)
+q.codes.random_(0, 255), q.scales.fill_(56), q.amax.fill_(1)
+def run():
+    e, w = B.route(l, 2)
+    p = B.expert_plan(e, 6)
+    y = B.experts_fprop(x, q, p)
+    out = B.combine(y, p, w)
+    dy, dw = B.combine_backward(out, y, p, w)
+    return out, B.experts_wgrad(dy, x, p, 3, 1, 0), B.route_backward(l, e, dw)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _COLD_CAPTURE], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
