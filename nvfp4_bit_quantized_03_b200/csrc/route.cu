@@ -300,7 +300,7 @@ __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[
 
 // The choice in FP64, for groups of any size.  values: the warp's shared buffer of E.
 template <int NPL>
-__device__ __noinline__ int choose_exact(const RouteArgs& a, const float (&x)[NPL], float mx,
+__device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&x)[NPL], float mx,
                                          int lane, double* values, bool& bad)
 {
     double s[NPL], sum = 0.0;
@@ -366,8 +366,9 @@ __device__ __noinline__ int choose_exact(const RouteArgs& a, const float (&x)[NP
 // lowest lane with a value has the lowest index and a row is read in 16-byte loads.  Bound by
 // instruction issue: a token of 256 experts takes 857 instructions (scores 160, sort 40, groups
 // 90, k + 1 rounds of about 20, weights 100).  B200: 16384 x 256 FP32 logits, sigmoid, bias, 4 of 8
-// groups, k 8: 26.5 us (51 us with the rounds searching unsorted keys and exact scores); one
-// token 2.8 us, a launch.
+// groups, k 8: 22 us (51 us with the rounds searching unsorted keys and exact scores; 26 with the
+// FP64 choice in a function of its own, which keeps the logits in local memory); one
+// token 2.6 us, a launch.
 template <int NPL, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
 {
