@@ -391,8 +391,8 @@ enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
  *   offsets   : experts + 1 int32, the regions
  *   pair_row  : tokens * k int32, the row of every pair (-1: the pair has no expert)
  *   row_token : rows int32, the token of every row (-1: none)
- * Limits: 1 <= k <= 32, 1 <= experts <= 512, tokens * k < 2^31; rows a multiple of 128, at least
- * nvfp4_expert_rows(tokens, k, experts) and at most 8388480. */
+ * Limits: tokens >= 1, 1 <= k <= 32, 1 <= experts <= 512, tokens * k < 2^31; rows a multiple of
+ * 128, at least nvfp4_expert_rows(tokens, k, experts) and at most 8388480. */
 typedef struct {
     int32_t* offsets;
     int32_t* pair_row;
@@ -474,8 +474,9 @@ nvfp4_status nvfp4_quantize_grouped(const void* x_bf16, int64_t cols, int64_t ld
                                     void* workspace, int* dev_status, void* stream);
 
 /*
- * Every expert's rows times its matrix: D[r, :] = A[r, :] . B_e^T for the rows r of expert e
- * (rows without a token give zeros, rows behind the last region are not written).
+ * Every expert's rows times its matrix: D[r, :] = A[r, :] . B_e^T for the rows r of expert e.  Rows
+ * behind the last region are not written; rows without a token are multiplied like the others and
+ * give the zeros that nvfp4_quantize_grouped writes for them.
  *   A : rows x K operand in expert order.
  *   B : the E matrices B_e [N x K], stacked (an (E * N) x K operand; N a multiple of 128 if E > 1)
  *       or side by side (an N x (E * K) operand).  For a layer's weights W_e [O x I] stacked in one

@@ -52,7 +52,7 @@ _poison = False
 def set_output_poisoning(enabled: bool):
     """Debug aid for tests: when enabled, every output buffer this module allocates is first
     filled with a pattern no kernel writes (codes and scales 0xFF bytes, FP32 / bf16 results and
-    amax NaN; workspaces 0xFF bytes), so that a kernel that leaves part of its output unwritten,
+    amax NaN, indices -2^31; workspaces 0xFF bytes), so that a kernel that leaves part of its output unwritten,
     or reads scratch it did not write, cannot pass a check by finding an earlier, identical
     result in recycled memory."""
     global _poison
@@ -63,6 +63,8 @@ def _poisoned(t):
     if _poison:
         if t.dtype == torch.uint8:
             t.fill_(0xFF)
+        elif t.dtype == torch.int32:
+            t.fill_(-2 ** 31)
         else:
             t.fill_(float("nan"))
     return t
@@ -558,8 +560,8 @@ class ExpertPlan:
         if rows == 0:
             raise NVFP4Error(ERR_SHAPE, f"expert plan of {tokens} tokens, {k} of {experts} experts")
 
-        return cls(_new((experts + 1,), torch.int32, device), _new((tokens, k), torch.int32, device),
-                   _new((rows,), torch.int32, device))
+        return cls(*(_poisoned(_new(shape, torch.int32, device))
+                     for shape in ((experts + 1,), (tokens, k), (rows,))))
 
 
 def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=True, scale=1.0,
@@ -571,9 +573,9 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=Tr
         _dense("bias", bias, torch.float32, (E,))
     with _allocating(stream):
         if experts is None:
-            experts = _new((T, max(k, 0)), torch.int32, logits.device)
+            experts = _poisoned(_new((T, max(k, 0)), torch.int32, logits.device))
         if weights is None:
-            weights = _new((T, max(k, 0)), torch.float32, logits.device)
+            weights = _poisoned(_new((T, max(k, 0)), torch.float32, logits.device))
     _dense("experts", experts, torch.int32, (T, k))
     _dense("weights", weights, torch.float32, (T, k))
     queue = _queue("nvfp4_route", stream, logits, bias, experts, weights, dev_status)
