@@ -910,7 +910,7 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
 // row and place are kept up to date without dividing.
 //  * SCATTER (gathered, round to nearest): the list is that of x; a span is quantized once and
 //    written to the row of every expert that takes its token.  The rows without a token are zeroed
-//    after.
+//    first.
 //  * otherwise the list is that of the expert-ordered matrix (stochastic rounding draws other bits
 //    for every such row).
 // Rows behind the last region are not written.
@@ -927,7 +927,40 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
 {
     __shared__ float r_tab[128];
     chain_next();
+    const int lane = threadIdx.x & 31;
+    const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    const int64_t wfirst = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int64_t spr = cols >> 5, gpr = cols >> 6;  // lanes' spans and scale words per row
+    const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
+    const int64_t cb = codes_extent(rows, cols), sb = scales_extent(rows, cols);
+    const int64_t used = map.used_rows(rows);
+    // word: four blocks' scales, in the even lanes (rows hold an even number of spans)
+    auto store = [&](int64_t r, int64_t span, const uint4& w, uint32_t word) {
+        st_checked(reinterpret_cast<uint4*>(codes) + r * spr + span, w, codes, cb, dev_status);
+        if ((lane & 1) == 0)
+            st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, span << 1, gpr)), word, scales,
+                       sb, dev_status);
+    };
+    if (SCATTER) {
+        // The rows without a token need no amax: a warp looks at up to 32 rows at once and zeroes
+        // them, while the pass ahead may still run.  The last warps take the first rows: with few
+        // tokens they are not the ones that have spans.
+        const int64_t share = (used + wstride - 1) / wstride;
+        const int at_once = static_cast<int>(share < 32 ? share : 32);
+        for (int64_t r0 = at_once * (wstride - 1 - wfirst); r0 < used; r0 += at_once * wstride) {
+            const bool empty = lane < at_once && r0 + lane < used && map.source(r0 + lane) < 0;
+            for (unsigned left = __ballot_sync(0xFFFFFFFFu, empty); left; left &= left - 1) {
+                const int64_t r = r0 + __ffs(left) - 1;
+                for (int64_t span = lane; span < spr; span += 32)
+                    store(r, span, make_uint4(0, 0, 0, 0), 0u);
+            }
+        }
+    }
     chain_wait();
+    const int64_t list_rows = SCATTER ? map.tokens : used, total = list_rows * spr;
+    const int64_t step = wstride * 32, dq = step / spr, dr = step - dq * spr;
+    // a CTA without spans is done; the first one reports the amax in any case
+    if (blockIdx.x != 0 && static_cast<int64_t>(blockIdx.x) * blockDim.x >= total) return;
     TensorScale ts;
     if (SCATTER && src.n_partials == 0 && !src.amax_given) {
         const uint32_t bits = small_amax(x, rows, cols, ld, map, dev_status);
@@ -944,23 +977,8 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     fill_factor_table(r_tab, ts.s_enc);
     __syncthreads();
     const Philox philox{keys};
-    const int lane = threadIdx.x & 31;
-    const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int64_t wfirst = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t spr = cols >> 5, gpr = cols >> 6;  // lanes' spans and scale words per row
-    const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
-    const int64_t cb = codes_extent(rows, cols), sb = scales_extent(rows, cols);
-    const int64_t used = map.used_rows(rows);
-    // word: four blocks' scales, in the even lanes (rows hold an even number of spans)
-    auto store = [&](int64_t r, int64_t span, const uint4& w, uint32_t word) {
-        st_checked(reinterpret_cast<uint4*>(codes) + r * spr + span, w, codes, cb, dev_status);
-        if ((lane & 1) == 0)
-            st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, span << 1, gpr)), word, scales,
-                       sb, dev_status);
-    };
-    const int64_t list_rows = SCATTER ? map.tokens : used, total = list_rows * spr;
-    const int64_t step = wstride * 32, dq = step / spr, dr = step - dq * spr;
-    int64_t f = wfirst * 32 + lane, row = f / spr, span = f - row * spr;
+    const int64_t f = wfirst * 32 + lane;
+    int64_t row = f / spr, span = f - row * spr;
     for (int64_t first = wfirst * 32; first < total; first += step) {
         const bool in = row < list_rows;
         int64_t from = -1;
@@ -1012,19 +1030,6 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
         if (span >= spr) {
             span -= spr;
             ++row;
-        }
-    }
-    if (SCATTER) {
-        // a warp looks at up to 32 rows at once and zeroes those without a token
-        const int64_t share = (used + wstride - 1) / wstride;
-        const int at_once = static_cast<int>(share < 32 ? share : 32);
-        for (int64_t r0 = at_once * wfirst; r0 < used; r0 += at_once * wstride) {
-            const bool empty = lane < at_once && r0 + lane < used && map.source(r0 + lane) < 0;
-            for (unsigned left = __ballot_sync(0xFFFFFFFFu, empty); left; left &= left - 1) {
-                const int64_t r = r0 + __ffs(left) - 1;
-                for (int64_t span = lane; span < spr; span += 32)
-                    store(r, span, make_uint4(0, 0, 0, 0), 0u);
-            }
         }
     }
 }
