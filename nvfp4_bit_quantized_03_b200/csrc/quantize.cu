@@ -764,8 +764,9 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
 // the row-wise passes have kernels of their own because a row of x may be needed several times.
 // ------------------------------------------------------------------------------------------
 
-// Partial maxima of |x| over the rows of x that some expert takes: a warp per row, four loads in
-// flight per lane.  A row of x is read once, however many experts take it.  Bound by HBM: B200,
+// Partial maxima of |x| over the rows of x that some expert takes: a warp per token, or in expert
+// order per pair, four loads in flight per lane.  A row of x is read once, however many experts
+// take it.  Bound by HBM: B200,
 // 73000 x 4096 in expert order 97 us (6.2 TB/s); 8192 gathered tokens of 4096 16 us.
 __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __restrict__ x,
                                                            int64_t rows, int64_t cols, int64_t ld,
@@ -775,17 +776,18 @@ __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __res
     const int64_t xb = bf16_matrix_bytes(map.x_rows, cols, ld);
     const int lane = threadIdx.x & 31;
     const int64_t wstride = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int64_t n = map.gather ? map.tokens : map.used_rows(rows);
+    const int64_t n = map.gather ? map.tokens : map.tokens * map.k;
     const int64_t cpr = cols >> 3;
     uint32_t m = 0;
-    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < n;
-         r += wstride) {
-        bool used;
-        if (map.gather)
-            used = __any_sync(0xFFFFFFFFu, lane < map.k && map.pair_target(r, lane, rows) >= 0);
-        else
-            used = map.source(r) >= 0;
-        if (!used) continue;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < n;
+         i += wstride) {
+        int64_t r = i;
+        if (map.gather) {
+            if (!__any_sync(0xFFFFFFFFu, lane < map.k && map.pair_target(i, lane, rows) >= 0)) continue;
+        } else {
+            r = map.pair_target(0, i, rows);
+            if (r < 0) continue;
+        }
         const uint4* p = reinterpret_cast<const uint4*>(x + r * ld);
         for (int64_t c = lane; c < cpr; c += 128) {
             uint4 v[4];
@@ -909,11 +911,10 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
 // list that the warps go through 32 at a time, so that rows of any length fill the lanes; a span's
 // row and place are kept up to date without dividing.
 //  * SCATTER (gathered, round to nearest): the list is that of x; a span is quantized once and
-//    written to the row of every expert that takes its token.  The rows without a token are zeroed
-//    first.
-//  * otherwise the list is that of the expert-ordered matrix (stochastic rounding draws other bits
-//    for every such row).
-// Rows behind the last region are not written.
+//    written to the row of every expert that takes its token.
+//  * otherwise the list is that of the pairs, each with a row of the expert-ordered matrix
+//    (stochastic rounding draws other bits for every such row).
+// The rows without a token are zeroed first; rows behind the last region are not written.
 // B200: 8192 tokens of 4096 to 8 experts each (67 MB in, 151 MB out) 62 us.  The stores bound it: with
 // none 32 us, with the codes' alone 50; a token's scale words lie 512 bytes apart in the MMA
 // layout.  Codes sent out as bulk copies from shared memory, or the rows looked up ahead, take the
@@ -941,7 +942,7 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
             st_checked(reinterpret_cast<uint32_t*>(scales + sf_offset(r, span << 1, gpr)), word, scales,
                        sb, dev_status);
     };
-    if (SCATTER) {
+    {
         // The rows without a token need no amax: a warp looks at up to 32 rows at once and zeroes
         // them, while the pass ahead may still run.  The last warps take the first rows: with few
         // tokens they are not the ones that have spans.
@@ -957,7 +958,7 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
         }
     }
     chain_wait();
-    const int64_t list_rows = SCATTER ? map.tokens : used, total = list_rows * spr;
+    const int64_t list_rows = SCATTER ? map.tokens : map.tokens * map.k, total = list_rows * spr;
     const int64_t step = wstride * 32, dq = step / spr, dr = step - dq * spr;
     // a CTA without spans is done; the first one reports the amax in any case
     if (blockIdx.x != 0 && static_cast<int64_t>(blockIdx.x) * blockDim.x >= total) return;
@@ -981,11 +982,11 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     int64_t row = f / spr, span = f - row * spr;
     for (int64_t first = wfirst * 32; first < total; first += step) {
         const bool in = row < list_rows;
-        int64_t from = -1;
-        if (SCATTER) {
-            if (in) from = row;  // a token without an expert is read and stored nowhere
-        } else if (in) {
-            from = map.source(row);
+        // row of x (a token without an expert is read and stored nowhere), and the pair's own row
+        int64_t from = SCATTER && in ? row : -1, to = -1;
+        if (!SCATTER && in) {
+            to = map.pair_target(0, row, used);
+            if (to >= 0) from = map.gather ? row / map.k : to;
         }
         uint4 v[4];
 #pragma unroll
@@ -1005,7 +1006,7 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
                 unpack8(v[2 * b], y);
                 unpack8(v[2 * b + 1], y + 8);
                 const BlockScale bs = block_scale(absmax_f32<16>(y), ts.s_enc, r_tab);
-                encode16<SR>(y, bs, philox, static_cast<uint64_t>(row * cols + 32 * span + 16 * b),
+                encode16<SR>(y, bs, philox, static_cast<uint64_t>(to * cols + 32 * span + 16 * b),
                              offset, out[2 * b], out[2 * b + 1]);
                 sf[b] = bs.sf;
             }
@@ -1022,8 +1023,8 @@ __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
                     if (r >= 0) store(r, span, w, word);
                 }
             }
-        } else if (in) {
-            store(row, span, w, word);
+        } else if (to >= 0) {
+            store(to, span, w, word);
         }
         row += dq;
         span += dr;
@@ -1191,8 +1192,9 @@ int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, i
 {
     static const int resident = resident_ctas(amax_grouped_kernel, 256);
     static const int resident_rht = resident_ctas(amax_rht_grouped_kernel<true>, 256);
-    // a warp per row, or per 16 rows x 128 columns
-    const int64_t items = rht ? rows / 16 * ((cols + 127) / 128) : (map.gather ? map.tokens : rows);
+    // a warp per token or pair, or per 16 rows x 128 columns
+    const int64_t items = rht ? rows / 16 * ((cols + 127) / 128)
+                              : map.tokens * (map.gather ? 1 : map.k);
     int64_t g = static_cast<int64_t>(sm_count) * (rht ? resident_rht : resident);
     if (g > (items + 7) / 8) g = (items + 7) / 8;
     if (g > kMaxPartials) g = kMaxPartials;
@@ -1201,9 +1203,9 @@ int amax_grouped_grid(int64_t rows, int64_t cols, bool rht, const RowMap& map, i
 
 bool grouped_amax_is_small(int64_t cols, const RowMap& map)
 {
-    // Every CTA reads these tokens from L2.  B200, 64 experts, 8 per token, computed here against in
-    // a pass of its own: 1 x 4096 6.0 against 7.8 us, 2 x 4096 7.6 / 9.2, 4 x 4096 9.6 / 9.7, 4 x 2048
-    // 7.3 / 8.0, 8 x 2048 8.8 / 8.4.  Matrices in expert order gain nothing (1 token: 5.9 / 5.3).
+    // Every CTA that has spans reads these tokens from L2.  B200, 64 experts, 8 per token, computed
+    // here against in a pass of its own: 1 x 4096 5.0 against 6.9 us, 2 x 4096 6.0 / 6.8, 4 x 2048 6.0 /
+    // 6.6, 4 x 4096 7.3 / 7.7, 8 x 2048 7.5 / 6.8, 8 x 4096 10.8 / 8.7.
     return map.gather && map.tokens * cols <= kSmallElements;
 }
 
