@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR
 // Partial maxima of |x| over the rows of x that some expert takes: a warp per token, or in expert
 // order per pair, four loads in flight per lane.  A row of x is read once, however many experts
 // take it.  Bound by HBM: B200,
-// 73000 x 4096 in expert order 97 us (6.2 TB/s); 8192 gathered tokens of 4096 16 us.
+// 65536 pairs of 4096 in expert order 97 us (5.5 TB/s); 8192 gathered tokens of 4096 16 us.
 __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __restrict__ x,
                                                            int64_t rows, int64_t cols, int64_t ld,
                                                            uint32_t* __restrict__ partials,
@@ -918,8 +918,8 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
 // B200: 8192 tokens of 4096 to 8 experts each (67 MB in, 151 MB out) 62 us.  The stores bound it: with
 // none 32 us, with the codes' alone 50; a token's scale words lie 512 bytes apart in the MMA
 // layout.  Codes sent out as bulk copies from shared memory, or the rows looked up ahead, take the
-// same time.  Stochastic, bound by issue: 73000 x 4096 294 us (the row-wise pass of the linear layer
-// does as many elements per second), 7000 x 1536 15.6 us.
+// same time.  Stochastic, bound by issue: 65536 pairs of 4096 270 us (the row-wise pass of the linear layer
+// does as many elements per second), 6000 of 1536 15.5 us.
 template <bool SR, bool SCATTER>
 __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, QuantSource src,
