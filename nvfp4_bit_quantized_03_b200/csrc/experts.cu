@@ -103,7 +103,7 @@ size_t nvfp4_expert_plan_workspace_bytes(int64_t T, int64_t k, int64_t E)
 {
     if (!routing_sizes_ok(T, k, E)) return 0;
     const int64_t chunks = (T * k + kPlanPairs - 1) / kPlanPairs;
-    return chunks > 1 ? sizeof(int32_t) * static_cast<size_t>(chunks * E) : 0;
+    return chunks > 1 ? sizeof(int32_t) * static_cast<size_t>((chunks + 1) * E) : 0;
 }
 
 nvfp4_status nvfp4_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld,

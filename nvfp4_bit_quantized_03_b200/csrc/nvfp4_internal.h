@@ -170,6 +170,10 @@ struct GroupedGemmArgs {
 // Routing (route.cu).  The plan's first pass counts each kPlanPairs pairs apart; it needs no
 // workspace when there are no more.
 constexpr int kPlanPairs = 1024;
+// From so many chunks on a pass between adds their counts up, instead of every chunk those of all
+// (B200, 256 experts, with against without: 16 chunks 10.1 / 11.3 us, 128 11.4 / 15.8, 1024 22 / 140, 4096
+// 73 / 1825; 64 experts, 64 chunks 10.0 / 10.1).
+constexpr int kPlanScan = 16;
 cudaError_t launch_route(const void* logits, bool bf16, int64_t T, int64_t E, int64_t ld,
                          const float* bias, bool sigmoid, bool renorm, int groups, int top_groups,
                          int k, float scale, int32_t* experts, float* weights, int* dev_status,

@@ -573,9 +573,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
 // ---- the plan of the expert-ordered rows ---------------------------------------------------
 // A stable counting sort of the pairs (t, j) by expert, regions padded to 128 rows.  A CTA takes
 // kPlanPairs consecutive pairs, a warp an eighth of them in order; more pairs are counted by a pass
-// ahead, and each CTA adds up the counts of the chunks before its own.  Integer counts only, so the
-// order of the atomics does not show.  A chain of short latencies: B200, 131072 pairs of 256
-// experts 3.1 + 10.4 us, one token 3.2 us.
+// ahead, whose counts a scan, or with few chunks each CTA for itself, adds up.  Integer counts only,
+// so the order of the atomics does not show.  A chain of short latencies: B200, 131072 pairs of 256
+// experts 11.4 us in all, one token 3.2 us.
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 
 struct PlanArgs {
@@ -586,7 +586,10 @@ struct PlanArgs {
     int32_t* offsets;
     int32_t* pair_row;
     int32_t* row_token;
-    int32_t* counts;  // [chunks][E] pairs of every chunk and expert (null: one chunk)
+    // [chunks][E] pairs of every chunk and expert (null: one chunk).  With `scanned` those of the
+    // chunks before, and a row more with those of all.
+    int32_t* counts;
+    bool scanned;
     int* dev_status;
 };
 
@@ -614,6 +617,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs
         a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = count[e];
 }
 
+// counts -> those of the chunks before, and the totals behind them: a CTA takes 32 experts (one per
+// lane), its warps consecutive shares of the chunks.
+__global__ void __launch_bounds__(1024) plan_scan_kernel(const PlanArgs a, int chunks)
+{
+    __shared__ int sums[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int share = (chunks + 31) / 32, first = warp * share;
+    const int last = first + share < chunks ? first + share : chunks;
+    int32_t* column = a.counts + e;
+    int sum = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int c = first; c < last; ++c) sum += column[static_cast<int64_t>(c) * a.E];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    int at = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) at += sums[w][lane];
+        all += sums[w][lane];
+    }
+    if (e < a.E) {
+        for (int c = first; c < last; ++c) {
+            const int n = column[static_cast<int64_t>(c) * a.E];
+            column[static_cast<int64_t>(c) * a.E] = at;
+            at += n;
+        }
+        if (warp == 0) column[static_cast<int64_t>(chunks) * a.E] = all;
+    }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs a)
 {
     extern __shared__ int next[];  // [kPlanWarps][E] pairs of each warp, then its next row
@@ -637,9 +671,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
         int sum = 0, prior = 0;
-        if (a.counts) {
-#pragma unroll 32
-            for (int c = 0; c < chunks; ++c) {
+        if (a.scanned) {
+            prior = a.counts[static_cast<int64_t>(chunk) * a.E + e];
+            sum = a.counts[static_cast<int64_t>(chunks) * a.E + e];
+        } else if (a.counts) {
+#pragma unroll
+            for (int c = 0; c < kPlanScan; ++c) {
+                if (c >= chunks) break;
                 const int n = a.counts[static_cast<int64_t>(c) * a.E + e];
                 if (c < chunk) prior += n;
                 sum += n;
@@ -816,11 +854,11 @@ cudaError_t launch_plan(const int32_t* experts, int64_t pairs, int k, int E, int
     a.dev_status = dev_status;
     const int chunks = static_cast<int>((pairs + kPlanPairs - 1) / kPlanPairs);
     a.counts = chunks > 1 ? counts : nullptr;
-    if (chunks > 1) {
-        plan_count_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
+    a.scanned = chunks >= kPlanScan;
+    if (chunks > 1) plan_count_kernel<<<chunks, kPlanThreads, 0, s>>>(a);
+    if (a.scanned) plan_scan_kernel<<<(E + 31) / 32, 1024, 0, s>>>(a, chunks);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     plan_place_kernel<<<chunks, kPlanThreads, sizeof(int) * kPlanWarps * E, s>>>(a);
     return cudaGetLastError();
 }

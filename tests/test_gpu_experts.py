@@ -240,7 +240,8 @@ def _plan(experts, E, rows=None):
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 6, 64), (5, 3, 7), (300, 2, 3), (257, 8, 64),
-                                   (2048, 1, 5), (2049, 1, 512), (1500, 8, 200), (9000, 2, 16)])
+                                   (1024, 1, 5), (1025, 1, 512), (2048, 1, 5), (2049, 1, 512),
+                                   (1500, 8, 200), (9000, 2, 16), (65537, 4, 40), (300001, 1, 3)])
 def test_plan(T, k, E):
     rng = np.random.default_rng(T + E)
     experts = R.routing(rng, T, E, k, pad=T // 4)
