@@ -540,11 +540,13 @@ class ExpertPlan:
     row_token [rows], int32 (nvfp4_expert_plan)."""
 
     def __init__(self, offsets, pair_row, row_token):
-        for name, t, dim in (("offsets", offsets, 1), ("pair_row", pair_row, 2),
-                             ("row_token", row_token, 1)):
-            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
-                raise ValueError(f"plan: {name} must be a contiguous int32 tensor of {dim} dimensions")
-        if pair_row.device != offsets.device or row_token.device != offsets.device:
+        if not (offsets.dtype == pair_row.dtype == row_token.dtype == torch.int32
+                and offsets.dim() == row_token.dim() == 1 and pair_row.dim() == 2
+                and offsets.is_contiguous() and pair_row.is_contiguous()
+                and row_token.is_contiguous()):
+            raise ValueError("plan: offsets [experts + 1], pair_row [tokens, k] and row_token [rows] "
+                             "must be contiguous int32 tensors")
+        if not offsets.device == pair_row.device == row_token.device:
             raise ValueError("plan: its tensors are on one device")
         self.offsets, self.pair_row, self.row_token = offsets, pair_row, row_token
         self.tokens, self.k = pair_row.shape
