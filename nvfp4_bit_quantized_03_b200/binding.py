@@ -506,8 +506,8 @@ def _dense(what, t, dtype, shape):
 
 
 def _row_stride(t):
-    # a one-row view may carry any stride; it is never used
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    # a one-row view may carry any stride, aligned or not; it is never used
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _workspace_size(workspace, need):

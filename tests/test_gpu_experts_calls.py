@@ -1,0 +1,64 @@
+"""Calls of the mixture-of-experts operators that their documentation allows and that lie at the edge
+of it: single rows out of wider buffers, and the like.  Through both libraries."""
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as R
+import synth
+from nvfp4_testlib import need_gpu, to_device_bf16
+
+nv = pytest.importorskip("nvfp4_bit_quantized_03_b200")
+B = nv.binding
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=["release", "checked"], autouse=True)
+def _library(request):
+    need_gpu()
+    if request.param == "release":
+        yield
+    else:
+        with B.bounds_checked():
+            yield
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _row_of(t, width):
+    """The one row of t as a slice of a buffer whose rows are `width` values."""
+    wide = torch.zeros(1, width, dtype=t.dtype, device=t.device)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def test_one_token_out_of_a_wider_buffer():
+    """Decoding: the token's row is a slice of a buffer of odd width, in every argument that has one."""
+    st = _status()
+    E, k, C = 6, 2, 256
+    x = to_device_bf16(synth.activations((1, C), seed=1))
+    logits = torch.from_numpy(np.random.default_rng(2).normal(0, 1, (1, E)).astype(np.float32)).cuda()
+    w, _ = B.quantize(to_device_bf16(synth.weights((E * C, C), seed=3)), B.ROWWISE | B.BLOCK2D)
+
+    def run(cut):
+        l = cut(logits)
+        e, wt = B.route(l, k, dev_status=st)
+        plan = B.expert_plan(e, E, dev_status=st)
+        q, _ = B.quantize_grouped(cut(x), plan, B.ROWWISE | B.GATHER, dev_status=st)
+        y = B.experts_fprop(cut(x), w, plan, dev_status=st)
+        out = B.combine(y, plan, wt, out=cut(torch.zeros(1, C, device="cuda")), dev_status=st)
+        used = int(plan.offsets[-1])
+        y[used:] = 0
+        dy, dw = B.combine_backward(cut(out), y, plan, wt, dev_status=st)
+        dy[used:] = 0
+        dx = B.experts_wgrad(dy, cut(x), plan, 3, 1, 0, dev_status=st)
+        dl = B.route_backward(l, e, dw, dlogits=cut(torch.zeros(1, E, device="cuda")), dev_status=st)
+        return e, wt, q.codes[:used], y, out, dy, dw, dx, dl
+
+    plain = run(lambda t: t)
+    for got, ref in zip(run(lambda t: _row_of(t, t.shape[1] + 5)), plain):
+        assert torch.equal(got, ref)
+    assert int(st) == 0
