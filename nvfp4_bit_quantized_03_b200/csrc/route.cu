@@ -755,7 +755,7 @@ template <typename T>
 cudaError_t launch_route_t(const RouteArgs& a, cudaStream_t s)
 {
     const int warps = kRouteThreads / 32;
-    const int grid = (a.T + warps - 1) / warps;
+    const unsigned grid = (static_cast<unsigned>(a.T) + warps - 1) / warps;  // T up to 2^31 - 1
     const size_t smem = a.groups > 1 ? sizeof(double) * warps * a.E : 0;  // choose_exact's
     if (a.E <= 32)       route_kernel<1, T><<<grid, kRouteThreads, smem, s>>>(a);
     else if (a.E <= 64)  route_kernel<2, T><<<grid, kRouteThreads, smem, s>>>(a);
@@ -769,7 +769,7 @@ template <typename T>
 cudaError_t launch_route_backward_t(const RouteBackwardArgs& a, cudaStream_t s)
 {
     const int warps = kRouteThreads / 32;
-    const int grid = (a.T + warps - 1) / warps;
+    const unsigned grid = (static_cast<unsigned>(a.T) + warps - 1) / warps;  // T up to 2^31 - 1
     if (a.E <= 32)       route_backward_kernel<1, T><<<grid, kRouteThreads, 0, s>>>(a);
     else if (a.E <= 64)  route_backward_kernel<2, T><<<grid, kRouteThreads, 0, s>>>(a);
     else if (a.E <= 128) route_backward_kernel<4, T><<<grid, kRouteThreads, 0, s>>>(a);

@@ -62,3 +62,27 @@ def test_one_token_out_of_a_wider_buffer():
     for got, ref in zip(run(lambda t: _row_of(t, t.shape[1] + 5)), plain):
         assert torch.equal(got, ref)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 3])
+def test_the_router_takes_the_most_tokens(T):
+    """Token counts up to the documented limit; the ends of the outputs against FP64."""
+    logits = torch.full((T, 1), 0.5, dtype=torch.bfloat16, device="cuda")
+    ends = (slice(0, 1000), slice(T - 1000, T))
+    for at in ends:
+        logits[at, 0] = torch.linspace(-4, 4, 1000, device="cuda").bfloat16()
+    st = _status()
+    e, w = B.route(logits, 1, sigmoid=True, renorm=False, dev_status=st)
+    assert not e.any()
+    dl = B.route_backward(logits, e, w, sigmoid=True, renorm=False, dev_status=st)
+    for at in ends:
+        s = torch.sigmoid(logits[at].double())
+        # exp to 2 units of 2^-23 and one rounding each of the sum and the quotient
+        assert ((w[at].double() - s).abs() <= 8 * 2.0 ** -24 * s).all()
+        # three such factors and their products, rounded to bf16
+        ref = s * s * (1 - s)
+        assert ((dl[at].double() - ref).abs() <= (2.0 ** -8 + 40 * 2.0 ** -24) * ref).all()
+    middle = float(torch.sigmoid(torch.tensor(0.5, dtype=torch.float64)))
+    low, high = torch.aminmax(w[1000:T - 1000])
+    assert abs(float(low) - middle) <= 8 * 2.0 ** -24 and abs(float(high) - middle) <= 8 * 2.0 ** -24
+    assert int(st) == 0
