@@ -83,15 +83,58 @@ def lib():
 def bounds_checked():
     """Route every call of this module made inside the block to libnvfp4_checked.so (the
     -DNVFP4_BOUNDS_CHECK build: an out-of-extent global access is skipped and sets
-    NVFP4_DEVSTAT_BOUNDS in the call's status word).  Yields that library.  The switch is
-    process-wide, not per thread: other threads' calls inside the block go there too."""
+    NVFP4_DEVSTAT_BOUNDS in the call's status word).  Calls made without a status word report to
+    one of this module, and the block ends with an NVFP4Error if they refused an access.  Yields
+    that library.  The switch is process-wide, not per thread: other threads' calls inside the
+    block go there too."""
     global _active
     prev = _active
     _active = CHECKED_LIB_PATH
     try:
-        yield lib()
+        L = lib()
+        _report_word()
+        if prev != CHECKED_LIB_PATH:
+            _take_reports()  # of a block that another error ended
+        yield L
+        if _take_reports() & DEVSTAT_BOUNDS:
+            raise NVFP4Error(ERR_ARG, "bounds_checked: a call without a status word refused an "
+                                      "access outside its buffer")
     finally:
         _active = prev
+
+
+_reports = {}  # device -> the status word of checked calls without one, kept for captured graphs
+
+
+def _report_word():
+    """Address of this device's word (None where it cannot be made: no GPU, or while capturing)."""
+    if not torch.cuda.is_available():
+        return None
+    device = torch.cuda.current_device()
+    if device not in _reports:
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        _reports[device] = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.synchronize(device)
+    return _reports[device].data_ptr()
+
+
+def _take_reports():
+    """The bits of all words, which are cleared."""
+    bits = 0
+    for device, word in _reports.items():
+        torch.cuda.synchronize(device)
+        bits |= int(word)
+        word.zero_()
+        torch.cuda.synchronize(device)
+    return bits
+
+
+def _status(dev_status):
+    """Address of a call's status word."""
+    if dev_status is None:
+        return _report_word() if _active == CHECKED_LIB_PATH else None
+    return dev_status.data_ptr()
 
 
 def _open(path):
@@ -284,7 +327,7 @@ def quantize(x, flags, seed=0, offset=0, out_row=None, out_col=None, workspace=N
     st = lib().nvfp4_quantize(_ptr(x), rows, cols, x.stride(0), flags, seed, offset,
                               ctypes.byref(op_r) if op_r is not None else None,
                               ctypes.byref(op_c) if op_c is not None else None,
-                              _ptr(workspace), _ptr(dev_status), _stream(stream))
+                              _ptr(workspace), _status(dev_status), _stream(stream))
     _check(st, "nvfp4_quantize")
     return out_row, out_col
 
@@ -300,7 +343,7 @@ def rht_quantize(x, sign_mask, flags=0, seed=0, offset=0, out_col=None, workspac
         workspace = _workspace(workspace_bytes(rows, cols, flags), x.device)
     op_c = out_col.operand()
     st = lib().nvfp4_rht_quantize(_ptr(x), rows, cols, x.stride(0), sign_mask, flags, seed,
-                                  offset, ctypes.byref(op_c), _ptr(workspace), _ptr(dev_status),
+                                  offset, ctypes.byref(op_c), _ptr(workspace), _status(dev_status),
                                   _stream(stream))
     _check(st, "nvfp4_rht_quantize")
     return out_col
@@ -321,7 +364,7 @@ def quantize_row_rht(x, sign_mask, flags=0, seed=0, offset=0, out_row=None, out_
     op_r, op_c = out_row.operand(), out_col.operand()
     st = lib().nvfp4_quantize_row_rht(_ptr(x), rows, cols, x.stride(0), sign_mask, flags, seed,
                                       offset, ctypes.byref(op_r), ctypes.byref(op_c),
-                                      _ptr(workspace), _ptr(dev_status), _stream(stream))
+                                      _ptr(workspace), _status(dev_status), _stream(stream))
     _check(st, "nvfp4_quantize_row_rht")
     return out_row, out_col
 
@@ -344,7 +387,7 @@ def gemm(A, B, out=None, out_dtype=torch.float32, dev_status=None, stream=None, 
     d_dtype = _dtype_code(out.dtype)
     oa, ob = A.operand(), B.operand()
     st = getattr(lib(), name)(ctypes.byref(oa), ctypes.byref(ob), _ptr(out), d_dtype,
-                              out.stride(0), _ptr(dev_status), _stream(stream))
+                              out.stride(0), _status(dev_status), _stream(stream))
     _check(st, name)
     return out
 
@@ -360,7 +403,7 @@ def gemm_amax(A, B, sign_mask, out=None, amax_out=None, dev_status=None, stream=
         amax_out = _poisoned(torch.empty(2, dtype=torch.float32, device=A.codes.device))
     oa, ob = A.operand(), B.operand()
     st = lib().nvfp4_gemm_amax(ctypes.byref(oa), ctypes.byref(ob), _ptr(out), out.stride(0),
-                               sign_mask, _ptr(amax_out), _ptr(dev_status), _stream(stream))
+                               sign_mask, _ptr(amax_out), _status(dev_status), _stream(stream))
     _check(st, "nvfp4_gemm_amax")
     return out, amax_out
 
@@ -368,7 +411,7 @@ def gemm_amax(A, B, sign_mask, out=None, amax_out=None, dev_status=None, stream=
 def selftest_wait_timeout(dev_status, stream=None):
     """nvfp4_selftest_wait_timeout: a bounded wait that nothing satisfies; after it the device
     status word has NVFP4_DEVSTAT_TIMEOUT set."""
-    _check(lib().nvfp4_selftest_wait_timeout(_ptr(dev_status), _stream(stream)),
+    _check(lib().nvfp4_selftest_wait_timeout(_status(dev_status), _stream(stream)),
            "nvfp4_selftest_wait_timeout")
 
 
@@ -380,7 +423,7 @@ def is_bounds_checked():
 def selftest_bounds(dev_status, stream=None):
     """nvfp4_selftest_bounds (checked build only): one refused store past a buffer's declared
     end; after it the device status word has NVFP4_DEVSTAT_BOUNDS set."""
-    _check(lib().nvfp4_selftest_bounds(_ptr(dev_status), _stream(stream)),
+    _check(lib().nvfp4_selftest_bounds(_status(dev_status), _stream(stream)),
            "nvfp4_selftest_bounds")
 
 
@@ -394,7 +437,7 @@ def linear_fprop(X, W, out=None, out_dtype=torch.float32, workspace=None, dev_st
     if workspace is None:
         workspace = _workspace(linear_workspace_bytes(T, I, O), X.device)
     st = lib().nvfp4_linear_fprop(_ptr(X), _ptr(W), T, I, O, _ptr(out), _dtype_code(out.dtype),
-                                  _ptr(workspace), _ptr(dev_status), _stream(stream))
+                                  _ptr(workspace), _status(dev_status), _stream(stream))
     _check(st, "nvfp4_linear_fprop")
     return out
 
@@ -409,7 +452,7 @@ def linear_dgrad(dY, W, seed, offset, out=None, out_dtype=torch.float32, workspa
     if workspace is None:
         workspace = _workspace(linear_workspace_bytes(T, I, O), dY.device)
     st = lib().nvfp4_linear_dgrad(_ptr(dY), _ptr(W), T, I, O, seed, offset, _ptr(out),
-                                  _dtype_code(out.dtype), _ptr(workspace), _ptr(dev_status),
+                                  _dtype_code(out.dtype), _ptr(workspace), _status(dev_status),
                                   _stream(stream))
     _check(st, "nvfp4_linear_dgrad")
     return out
@@ -437,7 +480,7 @@ def linear_dgrad_quantized(dY, W, seed, offset, sign_mask, next_seed, next_offse
     st = lib().nvfp4_linear_dgrad_quantized(_ptr(dY), _ptr(W), T, I, O, seed, offset, _ptr(out),
                                             sign_mask, next_seed, next_offset,
                                             ctypes.byref(op_r), ctypes.byref(op_c),
-                                            _ptr(workspace), _ptr(dev_status), _stream(stream))
+                                            _ptr(workspace), _status(dev_status), _stream(stream))
     _check(st, "nvfp4_linear_dgrad_quantized")
     return out, out_row, out_col
 
@@ -452,7 +495,7 @@ def linear_wgrad(dY, X, sign_mask, seed, offset, out=None, out_dtype=torch.float
     if workspace is None:
         workspace = _workspace(linear_workspace_bytes(T, I, O), dY.device)
     st = lib().nvfp4_linear_wgrad(_ptr(dY), _ptr(X), T, I, O, sign_mask, seed, offset, _ptr(out),
-                                  _dtype_code(out.dtype), _ptr(workspace), _ptr(dev_status),
+                                  _dtype_code(out.dtype), _ptr(workspace), _status(dev_status),
                                   _stream(stream))
     _check(st, "nvfp4_linear_wgrad")
     return out
@@ -583,7 +626,7 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=Tr
     queue = _queue("nvfp4_route", stream, logits, bias, experts, weights, dev_status)
     _check(lib().nvfp4_route(_address(logits), _dtype_code(logits.dtype), T, E, _row_stride(logits),
                              _address(bias), int(bool(sigmoid)), groups, top_groups, k, int(bool(renorm)),
-                             scale, _address(experts), _address(weights), _address(dev_status),
+                             scale, _address(experts), _address(weights), _status(dev_status),
                              queue), "nvfp4_route")
     return experts, weights
 
@@ -604,7 +647,7 @@ def route_backward(logits, experts, dweights, sigmoid=False, renorm=True, scale=
     _check(lib().nvfp4_route_backward(_address(logits), _dtype_code(logits.dtype), T, E,
                                       _row_stride(logits), _address(experts), _address(dweights),
                                       int(bool(sigmoid)), k, int(bool(renorm)), scale,
-                                      _address(dlogits), _row_stride(dlogits), _address(dev_status),
+                                      _address(dlogits), _row_stride(dlogits), _status(dev_status),
                                       queue), "nvfp4_route_backward")
     return dlogits
 
@@ -624,7 +667,7 @@ def expert_plan(experts, n_experts, plan=None, workspace=None, dev_status=None, 
         raise ValueError(f"plan is for {plan.tokens} tokens, {plan.k} of {plan.experts} experts")
     queue = _queue("nvfp4_plan_experts", stream, experts, plan.offsets, workspace, dev_status)
     _check(lib().nvfp4_plan_experts(_address(experts), plan.ref, _address(workspace),
-                                    _address(dev_status), queue), "nvfp4_plan_experts")
+                                    _status(dev_status), queue), "nvfp4_plan_experts")
     return plan
 
 
@@ -653,7 +696,7 @@ def quantize_grouped(x, plan, flags, sign_mask=0, seed=0, offset=0, out_row=None
     _check(lib().nvfp4_quantize_grouped(
         _address(x), cols, _row_stride(x), plan.ref, sign_mask, flags, seed, offset,
         ctypes.byref(op_r) if op_r is not None else None,
-        ctypes.byref(op_c) if op_c is not None else None, _address(workspace), _address(dev_status),
+        ctypes.byref(op_c) if op_c is not None else None, _address(workspace), _status(dev_status),
         queue), "nvfp4_quantize_grouped")
     return out_row, out_col
 
@@ -676,7 +719,7 @@ def gemm_grouped(A, W, plan, out=None, out_dtype=torch.bfloat16, dev_status=None
     oa, ob = A.operand(), W.operand()
     _check(lib().nvfp4_gemm_grouped(ctypes.byref(oa), ctypes.byref(ob), plan.ref,
                                     _address(out), _dtype_code(out.dtype), _row_stride(out),
-                                    _address(dev_status), queue), "nvfp4_gemm_grouped")
+                                    _status(dev_status), queue), "nvfp4_gemm_grouped")
     return out
 
 
@@ -687,7 +730,7 @@ def gemm_grouped_k(A, B, plan, out=None, out_dtype=torch.float32, dev_status=Non
     oa, ob = A.operand(), B.operand()
     _check(lib().nvfp4_gemm_grouped_k(ctypes.byref(oa), ctypes.byref(ob),
                                       plan.ref, _address(out), _dtype_code(out.dtype),
-                                      _row_stride(out), _address(dev_status), queue),
+                                      _row_stride(out), _status(dev_status), queue),
            "nvfp4_gemm_grouped_k")
     return out
 
@@ -714,7 +757,7 @@ def experts_fprop(X, W, plan, gather=True, out=None, out_dtype=torch.bfloat16, w
     _check(lib().nvfp4_experts_fprop(_address(X), _row_stride(X), int(bool(gather)), ctypes.byref(op),
                                      plan.ref, I, O, _address(out),
                                      _dtype_code(out.dtype), _row_stride(out), _address(workspace),
-                                     _address(dev_status), queue), "nvfp4_experts_fprop")
+                                     _status(dev_status), queue), "nvfp4_experts_fprop")
     return out
 
 
@@ -731,7 +774,7 @@ def experts_dgrad(dY, Wt, plan, seed, offset, out=None, out_dtype=torch.bfloat16
     _check(lib().nvfp4_experts_dgrad(_address(dY), _row_stride(dY), ctypes.byref(op),
                                      plan.ref, I, O, seed, offset, _address(out),
                                      _dtype_code(out.dtype), _row_stride(out), _address(workspace),
-                                     _address(dev_status), queue), "nvfp4_experts_dgrad")
+                                     _status(dev_status), queue), "nvfp4_experts_dgrad")
     return out
 
 
@@ -748,7 +791,7 @@ def experts_wgrad(dY, X, plan, sign_mask, seed, offset, gather=True, out=None,
     _check(lib().nvfp4_experts_wgrad(_address(dY), _row_stride(dY), _address(X), _row_stride(X),
                                      int(bool(gather)), plan.ref, I, O, sign_mask,
                                      seed, offset, _address(out), _dtype_code(out.dtype),
-                                     _row_stride(out), _address(workspace), _address(dev_status),
+                                     _row_stride(out), _address(workspace), _status(dev_status),
                                      queue), "nvfp4_experts_wgrad")
     return out
 
@@ -762,7 +805,7 @@ def combine(Y, plan, weights=None, out=None, out_dtype=torch.bfloat16, dev_statu
     queue = _queue("nvfp4_combine", stream, Y, plan.pair_row, weights, out, dev_status)
     _check(lib().nvfp4_combine(_address(Y), Y.shape[1], _row_stride(Y), plan.ref,
                                _address(weights), _address(out), _dtype_code(out.dtype), _row_stride(out),
-                               _address(dev_status), queue), "nvfp4_combine")
+                               _status(dev_status), queue), "nvfp4_combine")
     return out
 
 
@@ -783,5 +826,5 @@ def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=
     _check(lib().nvfp4_combine_backward(_address(dout), _dtype_code(dout.dtype), _row_stride(dout),
                                         _address(Y), cols, _row_stride(Y), plan.ref,
                                         _address(weights), _address(dy), _row_stride(dy), _address(dweights),
-                                        _address(dev_status), queue), "nvfp4_combine_backward")
+                                        _status(dev_status), queue), "nvfp4_combine_backward")
     return dy, dweights
