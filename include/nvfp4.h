@@ -249,9 +249,9 @@ nvfp4_status nvfp4_selftest_wait_timeout(int* dev_status, void* stream);
 /*
  * Debug build (no counterpart on the pages).  The same sources compiled with
  * -DNVFP4_BOUNDS_CHECK give libnvfp4_checked.so, with this header's API unchanged: every
- * global load and store of the quantizers is checked against the extent of its buffer (the
- * input's rows x ld values, the codes' rows x cols / 2 bytes, the scales' padded size), and
- * every TMA box the GEMM issues against the TMA start rules (non-negative coordinates, a
+ * global load and store of the quantizers, the router, the expert plan and the combination is
+ * checked against the extent of its buffer (the input's rows x ld values, the codes' rows x cols
+ * / 2 bytes, the scales' padded size, the plan's arrays), and every TMA box the GEMM issues against the TMA start rules (non-negative coordinates, a
  * 16-byte aligned innermost start).  An access outside is skipped and NVFP4_DEVSTAT_BOUNDS is
  * OR-ed into *dev_status; the call's outputs are then undefined.  Such a build is slower and
  * meant for tests.

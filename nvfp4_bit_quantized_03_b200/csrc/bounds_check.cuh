@@ -1,8 +1,8 @@
 // Debug bounds checks of the kernels' global-memory accesses.
 //
 // A library compiled with -DNVFP4_BOUNDS_CHECK (libnvfp4_checked.so) checks every global
-// load and store of the quantizers, and every TMA box the GEMM issues, against the extent of
-// its buffer, which the kernel derives from the call's shape.  An access outside it is
+// load and store of the quantizers, the router, the plan and the combination, and every TMA box the
+// GEMM issues, against the extent of its buffer, which the kernel derives from the call's shape.  An access outside it is
 // skipped, and NVFP4_DEVSTAT_BOUNDS is OR-ed into the call's status word: an index mistake
 // shows up as a status bit and a mismatch against the oracle instead of a memory fault.  In
 // the normal build kBoundsCheck is false, every check below is the constant `true`, and the
@@ -56,6 +56,15 @@ __device__ __forceinline__ T ldg_checked(const T* p, const void* base, int64_t s
     return __ldg(p);
 }
 
+// The same by an ordinary load: data that an earlier kernel of a chain may still be writing at launch.
+template <typename T>
+__device__ __forceinline__ T ld_checked(const T* p, const void* base, int64_t size,
+                                        int* dev_status)
+{
+    if (kBoundsCheck && !in_buffer(p, base, size, dev_status)) return T{};
+    return *p;
+}
+
 // Store that is skipped (and recorded) outside the buffer.
 template <typename T>
 __device__ __forceinline__ void st_checked(T* p, const T& v, const void* base, int64_t size,
@@ -65,6 +74,11 @@ __device__ __forceinline__ void st_checked(T* p, const T& v, const void* base, i
     *p = v;
 }
 
+// Bytes of a row-major matrix of `rows` rows of `cols` values of `esize` bytes, `ld` values apart.
+__device__ __forceinline__ int64_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t esize)
+{
+    return rows > 0 ? esize * ((rows - 1) * ld + cols) : 0;
+}
 // Bytes of a row-major bf16 matrix of `rows` rows of `cols` values, `ld` values apart (the
 // last row ends at its last value).
 __device__ __forceinline__ int64_t bf16_matrix_bytes(int64_t rows, int64_t cols, int64_t ld)

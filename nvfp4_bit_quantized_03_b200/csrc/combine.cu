@@ -28,6 +28,11 @@ __device__ __forceinline__ uint4 pack8(const float* f)
                       pack_bf16(f[6], f[7]));
 }
 
+__device__ __forceinline__ float pair_weight(const CombineArgs& a, int64_t t, int j)
+{
+    return ld_checked(a.weights + t * a.map.k + j, a.weights, 4 * a.map.tokens * a.map.k, a.dev_status);
+}
+
 // Pairs whose rows are read together: eight loads in flight per thread.
 constexpr int kTogether = 8;
 
@@ -44,9 +49,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a)
     if (threadIdx.x < kMaxK) {
         const int r = threadIdx.x < k ? static_cast<int>(a.map.pair_target(t, threadIdx.x, a.rows)) : -1;
         row[threadIdx.x] = r;
-        weight[threadIdx.x] = r >= 0 && a.weights ? a.weights[t * k + threadIdx.x] : 1.0f;
+        weight[threadIdx.x] = r >= 0 && a.weights ? pair_weight(a, t, threadIdx.x) : 1.0f;
     }
     __syncthreads();
+    const int64_t ob = matrix_bytes(a.map.tokens, a.cols, a.ldo, F32 ? 4 : 2);
     const int64_t yb = bf16_matrix_bytes(a.rows, a.cols, a.ldy);
     const int64_t vecs = a.cols >> 3;
     for (int64_t v = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x; v < vecs;
@@ -73,10 +79,11 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineArgs a)
         }
         if (F32) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + t * a.ldo) + 2 * v;
-            o[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-            o[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            st_checked(o, make_float4(sum[0], sum[1], sum[2], sum[3]), a.out, ob, a.dev_status);
+            st_checked(o + 1, make_float4(sum[4], sum[5], sum[6], sum[7]), a.out, ob, a.dev_status);
         } else {
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.ldo)[v] = pack8(sum);
+            st_checked(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.ldo) + v,
+                       pack8(sum), a.out, ob, a.dev_status);
         }
     }
 }
@@ -99,7 +106,7 @@ __global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs
         const int64_t used = a.map.used_rows(a.rows);
         const int64_t warps = (gridDim.x - a.map.tokens) * 4;
         for (int64_t r0 = 32 * ((blockIdx.x - a.map.tokens) * 4 + warp); r0 < used; r0 += 32 * warps) {
-            const int64_t token = a.map.row_token[r0 + lane];  // used is a multiple of 128
+            const int64_t token = a.map.token_of(r0 + lane);  // used is a multiple of 128
             for (unsigned left = __ballot_sync(0xFFFFFFFFu, token < 0 || token >= a.map.tokens); left;
                  left &= left - 1) {
                 uint4* d = reinterpret_cast<uint4*>(a.dy + (r0 + __ffs(left) - 1) * a.lddy);
@@ -116,9 +123,10 @@ __global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs
     if (threadIdx.x < kMaxK) {
         const int r = threadIdx.x < k ? static_cast<int>(a.map.pair_target(t, threadIdx.x, a.rows)) : -1;
         row[threadIdx.x] = r;
-        weight[threadIdx.x] = r >= 0 ? a.weights[t * k + threadIdx.x] : 0.0f;
+        weight[threadIdx.x] = r >= 0 ? pair_weight(a, t, threadIdx.x) : 0.0f;
     }
     __syncthreads();
+    const int64_t gb = matrix_bytes(a.map.tokens, a.cols, a.ldo, F32 ? 4 : 2);
     for (int j0 = 0; j0 < k; j0 += kTogether) {
         float dot[kTogether];
 #pragma unroll
@@ -136,12 +144,14 @@ __global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs
             if (F32) {
                 const float4* p = reinterpret_cast<const float4*>(
                     static_cast<const float*>(a.dout) + t * a.ldo) + 2 * v;
-                const float4 lo = __ldg(p), hi = __ldg(p + 1);
+                const float4 lo = ldg_checked(p, a.dout, gb, a.dev_status);
+                const float4 hi = ldg_checked(p + 1, a.dout, gb, a.dev_status);
                 g[0] = lo.x; g[1] = lo.y; g[2] = lo.z; g[3] = lo.w;
                 g[4] = hi.x; g[5] = hi.y; g[6] = hi.z; g[7] = hi.w;
             } else {
-                unpack8(__ldg(reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(a.dout) + t * a.ldo) + v), g);
+                unpack8(ldg_checked(reinterpret_cast<const uint4*>(
+                                        static_cast<const uint16_t*>(a.dout) + t * a.ldo) + v,
+                                    a.dout, gb, a.dev_status), g);
             }
 #pragma unroll
             for (int j = 0; j < kTogether; ++j) {
@@ -167,8 +177,10 @@ __global__ void __launch_bounds__(128) combine_backward_kernel(const CombineArgs
     }
     __syncthreads();
     if (threadIdx.x < k)
-        a.dweights[t * k + threadIdx.x] =
-            (part[threadIdx.x][0] + part[threadIdx.x][1]) + (part[threadIdx.x][2] + part[threadIdx.x][3]);
+        st_checked(a.dweights + t * k + threadIdx.x,
+                   (part[threadIdx.x][0] + part[threadIdx.x][1]) +
+                       (part[threadIdx.x][2] + part[threadIdx.x][3]),
+                   a.dweights, 4 * a.map.tokens * k, a.dev_status);
 }
 
 }  // namespace

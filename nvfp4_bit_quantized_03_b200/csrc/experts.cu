@@ -32,7 +32,7 @@ nvfp4_status check_plan(const nvfp4_expert_plan* p)
     return NVFP4_OK;
 }
 
-RowMap row_map(const nvfp4_expert_plan& p, bool gather)
+RowMap row_map(const nvfp4_expert_plan& p, bool gather, int* dev_status)
 {
     RowMap m;
     m.row_token = p.row_token;
@@ -40,8 +40,10 @@ RowMap row_map(const nvfp4_expert_plan& p, bool gather)
     m.used = p.offsets + p.experts;
     m.tokens = p.tokens;
     m.k = p.k;
+    m.rows = p.rows;
     m.x_rows = gather ? p.tokens : p.rows;
     m.gather = gather;
+    m.dev_status = dev_status;
     return m;
 }
 
@@ -193,7 +195,7 @@ nvfp4_status nvfp4_quantize_grouped(const void* x_bf16, int64_t cols, int64_t ld
     a.rows = rows;
     a.cols = cols;
     a.ld = ld;
-    a.map = row_map(*plan, gather);
+    a.map = row_map(*plan, gather, dev_status);
     if (given) {
         a.src.amax_given = want_row ? out_row->amax : nullptr;
         a.src_col.amax_given = want_col ? out_col->amax : nullptr;
@@ -417,7 +419,7 @@ nvfp4_status nvfp4_combine(const void* Y_bf16, int64_t cols, int64_t ldy,
     int sms = 0;
     if ((st = current_device(&sms)) != NVFP4_OK) return st;
     CombineArgs a{};
-    a.map = row_map(*plan, true);
+    a.map = row_map(*plan, true, dev_status);
     a.rows = plan->rows;
     a.cols = cols;
     a.y = static_cast<const uint16_t*>(Y_bf16);
@@ -448,7 +450,7 @@ nvfp4_status nvfp4_combine_backward(const void* dout, int dout_dtype, int64_t ld
     int sms = 0;
     if ((st = current_device(&sms)) != NVFP4_OK) return st;
     CombineArgs a{};
-    a.map = row_map(*plan, true);
+    a.map = row_map(*plan, true, dev_status);
     a.rows = plan->rows;
     a.cols = cols;
     a.y = static_cast<const uint16_t*>(Y_bf16);

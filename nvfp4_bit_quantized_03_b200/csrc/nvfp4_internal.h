@@ -5,6 +5,10 @@
 
 #include <cstdint>
 
+#ifdef __CUDACC__
+#include "bounds_check.cuh"
+#endif
+
 namespace nvfp4 {
 
 // Upper bound on the CTAs of the amax pass, i.e. on the partial maxima in the workspace.
@@ -44,10 +48,16 @@ struct RowMap {
     const int32_t* pair_row;   // [tokens * k] row of each pair, negative: none
     const int32_t* used;       // rows in use (the last of the region offsets)
     int64_t tokens, k;
+    int64_t rows;              // rows of the expert-ordered matrix
     int64_t x_rows;            // rows of x: tokens when gathering, else the matrix's rows
     bool gather;               // x has a row per token; otherwise it is in expert order itself
+    int* dev_status;           // of the debug build's checks
 
 #ifdef __CUDACC__
+    __device__ __forceinline__ int64_t token_of(int64_t r) const
+    {
+        return ld_checked(row_token + r, row_token, 4 * rows, dev_status);
+    }
     __device__ __forceinline__ int64_t used_rows(int64_t rows) const
     {
         const int64_t n = *used;
@@ -56,14 +66,14 @@ struct RowMap {
     // row of x behind row r, or -1
     __device__ __forceinline__ int64_t source(int64_t r) const
     {
-        const int64_t t = row_token[r];
+        const int64_t t = token_of(r);
         if (t < 0 || t >= tokens) return -1;
         return gather ? t : r;
     }
     // row of the pair (t, j), or -1
     __device__ __forceinline__ int64_t pair_target(int64_t t, int64_t j, int64_t rows) const
     {
-        const int64_t r = pair_row[t * k + j];
+        const int64_t r = ld_checked(pair_row + t * k + j, pair_row, 4 * tokens * k, dev_status);
         return r < rows ? r : -1;
     }
 #endif

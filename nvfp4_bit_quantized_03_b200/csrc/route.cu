@@ -68,20 +68,39 @@ __device__ __forceinline__ float to_float(uint16_t v)
 {
     return __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
+
+// A buffer and its size in bytes, which the debug build holds every access against.
+struct Buffer {
+    const void* base;
+    int64_t bytes;
+    int* dev_status;
+
+    template <typename T>
+    __device__ __forceinline__ T ldg(const T* p) const { return ldg_checked(p, base, bytes, dev_status); }
+    template <typename T>
+    __device__ __forceinline__ T load(const T* p) const { return ld_checked(p, base, bytes, dev_status); }
+    template <typename T>
+    __device__ __forceinline__ void store(T* p, const T& v) const
+    {
+        st_checked(p, v, base, bytes, dev_status);
+    }
+};
+
 template <typename T>
-__device__ __forceinline__ float load_logit(const T* p) { return to_float(__ldg(p)); }
+__device__ __forceinline__ float load_logit(const T* p, const Buffer& in) { return to_float(in.ldg(p)); }
 
 // The lane's NPL values of a row of E (-inf behind its end), in loads of up to 16 bytes when the
 // rows allow them (`wide`).
 template <int NPL, typename T>
-__device__ __forceinline__ void load_values(const T* row, int lane, int E, bool wide, float (&x)[NPL])
+__device__ __forceinline__ void load_values(const T* row, int lane, int E, bool wide, float (&x)[NPL],
+                                            const Buffer& in)
 {
     constexpr int BYTES = NPL * static_cast<int>(sizeof(T));
     if (wide && (lane + 1) * NPL <= E) {
         if constexpr (BYTES >= 16) {
 #pragma unroll
             for (int c = 0; c < BYTES / 16; ++c) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + lane * NPL) + c);
+                const uint4 v = in.ldg(reinterpret_cast<const uint4*>(row + lane * NPL) + c);
                 if constexpr (sizeof(T) == 4) {
                     x[4 * c] = __uint_as_float(v.x);
                     x[4 * c + 1] = __uint_as_float(v.y);
@@ -93,7 +112,7 @@ __device__ __forceinline__ void load_values(const T* row, int lane, int E, bool 
             }
             return;
         } else if constexpr (BYTES == 8) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + lane * NPL));
+            const uint2 v = in.ldg(reinterpret_cast<const uint2*>(row + lane * NPL));
             if constexpr (sizeof(T) == 4) {
                 x[0] = __uint_as_float(v.x);
                 x[1] = __uint_as_float(v.y);
@@ -109,7 +128,7 @@ __device__ __forceinline__ void load_values(const T* row, int lane, int E, bool 
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = lane * NPL + i;
-        x[i] = e < E ? load_logit(row + e) : -INFINITY;
+        x[i] = e < E ? load_logit(row + e, in) : -INFINITY;
     }
 }
 
@@ -218,6 +237,21 @@ struct RouteArgs {
     int32_t* experts;
     float* weights;
     int* dev_status;
+
+    template <typename L>
+    __device__ __forceinline__ Buffer logits_buffer() const
+    {
+        return Buffer{logits, matrix_bytes(T, E, ld, sizeof(L)), dev_status};
+    }
+    __device__ __forceinline__ Buffer bias_buffer() const
+    {
+        return Buffer{bias, static_cast<int64_t>(4) * E, dev_status};
+    }
+    // of a T x k output
+    __device__ __forceinline__ Buffer per_pair(const void* base) const
+    {
+        return Buffer{base, static_cast<int64_t>(4) * T * k, dev_status};
+    }
 };
 
 // Fast choice by FP32 scores s + bias.  close: some comparison was too close to call, and the choice
@@ -250,7 +284,7 @@ __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[
     }
     if (a.bias) {
         float b[NPL];
-        load_values<NPL>(a.bias, lane, a.E, a.wide, b);
+        load_values<NPL>(a.bias, lane, a.E, a.wide, b, a.bias_buffer());
 #pragma unroll
         for (int i = 0; i < NPL; ++i) s[i] += b[i];
     }
@@ -321,7 +355,7 @@ __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&x)
     for (int i = 0; i < NPL; ++i) {
         key[i] = 0;
         if (x[i] > -INFINITY) {  // false behind the last expert too
-            if (a.bias) s[i] += __ldg(a.bias + lane * NPL + i);
+            if (a.bias) s[i] += a.bias_buffer().ldg(a.bias + lane * NPL + i);
             nan |= !(s[i] < INFINITY);
             if (s[i] > -INFINITY) key[i] = order_key(s[i]);
         }
@@ -378,8 +412,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
     const int t = blockIdx.x * (kRouteThreads / 32) + warp;
     if (t >= a.T) return;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const Buffer in = a.logits_buffer<T>();
     float x[NPL];
-    load_values<NPL>(row, lane, a.E, a.wide, x);
+    load_values<NPL>(row, lane, a.E, a.wide, x, in);
     bool bad = false;
     float mx = -INFINITY;
 #pragma unroll
@@ -418,7 +453,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
         if (lane == 0 && a.dev_status) atomicOr(a.dev_status, static_cast<int>(kDevNonfinite));
     }
     const bool chosen = expert >= 0;
-    const float l = chosen ? load_logit(row + expert) : -INFINITY;
+    const float l = chosen ? load_logit(row + expert, in) : -INFINITY;
     float w = 0.0f;
     if (a.renorm) {
         float p = a.sigmoid && chosen ? 1.0f / (1.0f + expf(-l)) : 0.0f;
@@ -442,8 +477,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
         if (chosen) w = a.scale * (expf(l - mx) / sum);
     }
     if (lane < a.k) {
-        a.experts[static_cast<int64_t>(t) * a.k + lane] = expert;
-        a.weights[static_cast<int64_t>(t) * a.k + lane] = w;
+        const int64_t at = static_cast<int64_t>(t) * a.k + lane;
+        a.per_pair(a.experts).store(a.experts + at, expert);
+        a.per_pair(a.weights).store(a.weights + at, w);
     }
 }
 
@@ -476,17 +512,21 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
     const int t = blockIdx.x * (kRouteThreads / 32) + warp;
     if (t >= a.T) return;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const Buffer in{a.logits, matrix_bytes(a.T, a.E, a.ld, sizeof(T)), a.dev_status};
+    const int64_t pairs_bytes = static_cast<int64_t>(4) * a.T * a.k;
     int expert = -1;
     float g = 0.0f, l = -INFINITY;
     if (lane < a.k) {
-        expert = a.experts[static_cast<int64_t>(t) * a.k + lane];
+        expert = ld_checked(a.experts + static_cast<int64_t>(t) * a.k + lane, a.experts, pairs_bytes,
+                            a.dev_status);
         if (expert < -1 || expert >= a.E) {
             if (a.dev_status) atomicOr(a.dev_status, static_cast<int>(kDevIndex));
             expert = -1;
         }
         if (expert >= 0) {
-            l = load_logit(row + expert);
-            g = a.scale * a.dweights[static_cast<int64_t>(t) * a.k + lane];
+            l = load_logit(row + expert, in);
+            g = a.scale * ld_checked(a.dweights + static_cast<int64_t>(t) * a.k + lane, a.dweights,
+                                     pairs_bytes, a.dev_status);
         }
     }
     const bool chosen = expert >= 0;
@@ -509,7 +549,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
             if (chosen) d = g * rest * (1.0f / (1.0f + expf(-l)));
         } else {
             float x[NPL];
-            load_values<NPL>(row, lane, a.E, a.wide, x);
+            load_values<NPL>(row, lane, a.E, a.wide, x, in);
             float mx = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NPL; ++i) mx = fmaxf(mx, x[i]);
@@ -537,6 +577,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
         }
     }
     T* drow = static_cast<T*>(a.dlogits) + t * a.ldd;
+    const Buffer to{a.dlogits, matrix_bytes(a.T, a.E, a.ldd, sizeof(T)), a.dev_status};
     if constexpr (NPL * sizeof(T) >= 16) {
         if (a.wide && (lane + 1) * NPL <= a.E) {
             constexpr int PER = 16 / sizeof(T);
@@ -553,7 +594,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
                         w[h] = *reinterpret_cast<const uint32_t*>(&v);
                     }
                 }
-                reinterpret_cast<uint4*>(drow + lane * NPL)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                to.store(reinterpret_cast<uint4*>(drow + lane * NPL) + c,
+                         make_uint4(w[0], w[1], w[2], w[3]));
             }
             return;
         }
@@ -563,9 +605,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const Rou
         const int e = lane * NPL + i;
         if (e < a.E) {
             if constexpr (sizeof(T) == 4)
-                drow[e] = out[i];
+                to.store(drow + e, out[i]);
             else
-                drow[e] = __bfloat16_as_ushort(__float2bfloat16_rn(out[i]));
+                to.store(drow + e, __bfloat16_as_ushort(__float2bfloat16_rn(out[i])));
         }
     }
 }
@@ -591,11 +633,21 @@ struct PlanArgs {
     int32_t* counts;
     bool scanned;
     int* dev_status;
+
+    __device__ __forceinline__ Buffer pairs_buffer(const void* base) const
+    {
+        return Buffer{base, 4 * pairs, dev_status};
+    }
+    __device__ __forceinline__ Buffer rows_buffer() const { return Buffer{row_token, 4 * rows, dev_status}; }
+    __device__ __forceinline__ Buffer counts_buffer(int chunks) const
+    {
+        return Buffer{counts, static_cast<int64_t>(4) * (chunks + (scanned ? 1 : 0)) * E, dev_status};
+    }
 };
 
 __device__ __forceinline__ int pair_expert(const PlanArgs& a, int64_t i)
 {
-    const int e = a.experts[i];
+    const int e = a.pairs_buffer(a.experts).load(a.experts + i);
     if (e >= 0 && e < a.E) return e;
     if (e != -1 && a.dev_status) atomicOr(a.dev_status, static_cast<int>(kDevIndex));
     return -1;
@@ -614,7 +666,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs
         }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads)
-        a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = count[e];
+        a.counts_buffer(gridDim.x).store(a.counts + static_cast<int64_t>(blockIdx.x) * a.E + e, count[e]);
 }
 
 // counts -> those of the chunks before, and the totals behind them: a CTA takes 32 experts (one per
@@ -626,10 +678,11 @@ __global__ void __launch_bounds__(1024) plan_scan_kernel(const PlanArgs a, int c
     const int share = (chunks + 31) / 32, first = warp * share;
     const int last = first + share < chunks ? first + share : chunks;
     int32_t* column = a.counts + e;
+    const Buffer counts = a.counts_buffer(chunks);
     int sum = 0;
     if (e < a.E) {
 #pragma unroll 8
-        for (int c = first; c < last; ++c) sum += column[static_cast<int64_t>(c) * a.E];
+        for (int c = first; c < last; ++c) sum += counts.load(column + static_cast<int64_t>(c) * a.E);
     }
     sums[warp][lane] = sum;
     __syncthreads();
@@ -640,11 +693,12 @@ __global__ void __launch_bounds__(1024) plan_scan_kernel(const PlanArgs a, int c
     }
     if (e < a.E) {
         for (int c = first; c < last; ++c) {
-            const int n = column[static_cast<int64_t>(c) * a.E];
-            column[static_cast<int64_t>(c) * a.E] = at;
+            int32_t* p = column + static_cast<int64_t>(c) * a.E;
+            const int n = counts.load(p);
+            counts.store(p, at);
             at += n;
         }
-        if (warp == 0) column[static_cast<int64_t>(chunks) * a.E] = all;
+        if (warp == 0) counts.store(column + static_cast<int64_t>(chunks) * a.E, all);
     }
 }
 
@@ -655,6 +709,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     __shared__ int warp_sums[kPlanWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = blockIdx.x, chunks = gridDim.x;
+    const Buffer counts = a.counts_buffer(chunks), tokens = a.rows_buffer();
     int* warp_next = next + warp * a.E;
     for (int i = threadIdx.x; i < kPlanWarps * a.E; i += kPlanThreads) next[i] = 0;
     __syncthreads();
@@ -672,13 +727,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
         int sum = 0, prior = 0;
         if (a.scanned) {
-            prior = a.counts[static_cast<int64_t>(chunk) * a.E + e];
-            sum = a.counts[static_cast<int64_t>(chunks) * a.E + e];
+            prior = counts.load(a.counts + static_cast<int64_t>(chunk) * a.E + e);
+            sum = counts.load(a.counts + static_cast<int64_t>(chunks) * a.E + e);
         } else if (a.counts) {
 #pragma unroll
             for (int c = 0; c < kPlanScan; ++c) {
                 if (c >= chunks) break;
-                const int n = a.counts[static_cast<int64_t>(c) * a.E + e];
+                const int n = counts.load(a.counts + static_cast<int64_t>(c) * a.E + e);
                 if (c < chunk) prior += n;
                 sum += n;
             }
@@ -717,7 +772,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     if (threadIdx.x == kPlanThreads - 1 && a.E == kMaxExperts) start[a.E] = at;
     __syncthreads();
     if (chunk == 0)
-        for (int e = threadIdx.x; e <= a.E; e += kPlanThreads) a.offsets[e] = start[e];
+        for (int e = threadIdx.x; e <= a.E; e += kPlanThreads)
+            st_checked(a.offsets + e, start[e], a.offsets, static_cast<int64_t>(4) * (a.E + 1),
+                       a.dev_status);
     for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
         int row = start[e] + before[e];
         for (int w = 0; w < kPlanWarps; ++w) {
@@ -739,16 +796,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
         if (mine[i] >= 0 && lane == 31 - __clz(same)) warp_next[mine[i]] = row + 1;
         __syncwarp();
         if (p < a.pairs) {
-            a.pair_row[p] = row;
-            if (row >= 0 && row < a.rows) a.row_token[row] = static_cast<int32_t>(p / a.k);
+            a.pairs_buffer(a.pair_row).store(a.pair_row + p, row);
+            if (row >= 0 && row < a.rows) tokens.store(a.row_token + row, static_cast<int32_t>(p / a.k));
         }
     }
     // rows without a token: the ends of the regions, and everything behind the last
     for (int e = chunk * kPlanWarps + warp; e < a.E; e += chunks * kPlanWarps)
-        for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 32) a.row_token[r] = -1;
+        for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 32) tokens.store(a.row_token + r, -1);
     for (int64_t r = start[a.E] + static_cast<int64_t>(chunk) * kPlanThreads + threadIdx.x; r < a.rows;
          r += static_cast<int64_t>(chunks) * kPlanThreads)
-        a.row_token[r] = -1;
+        tokens.store(a.row_token + r, -1);
 }
 
 template <typename T>
