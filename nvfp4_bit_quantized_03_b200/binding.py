@@ -554,6 +554,8 @@ def _row_stride(t):
 
 
 def _workspace_size(workspace, need):
+    if workspace is not None and not workspace.is_contiguous():  # an expanded one has less behind it
+        raise ValueError("the workspace must be contiguous")
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if have < need:
         raise ValueError(f"the workspace has {have} bytes, the call needs {need}")

@@ -15,3 +15,21 @@ def test_the_stride_of_a_single_row_does_not_matter(width):
     assert B._row_stride(torch.empty(64).expand(1, 64)) == 64
     assert B._row_stride(wide[:, :64]) == width        # with more rows it is the tensor's
     assert B._row_stride(wide[::2, :64]) == 2 * width
+
+
+def test_a_workspace_whose_bytes_repeat_is_refused():
+    """An expanded tensor has many elements and one byte behind them."""
+    one = torch.zeros(1, dtype=torch.uint8).expand(1 << 24)
+    experts = torch.zeros(2048, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        B.expert_plan(experts, 4, plan=B.ExpertPlan.empty(2048, 4, 4, device="cpu"), workspace=one)
+    plan = B.ExpertPlan.empty(10, 2, 4, device="cpu")
+    x = torch.zeros(plan.rows, 128, dtype=torch.bfloat16)
+    W, Wt = (B.QuantizedTensor(*s, device="cpu") for s in ((4 * 128, 128), (128, 4 * 128)))
+    for call in (lambda: B.quantize_grouped(x, plan, B.ROWWISE, workspace=one,
+                                            out_row=B.QuantizedTensor(plan.rows, 128, device="cpu")),
+                 lambda: B.experts_fprop(x, W, plan, gather=False, workspace=one),
+                 lambda: B.experts_dgrad(x, Wt, plan, 0, 0, workspace=one),
+                 lambda: B.experts_wgrad(x, x, plan, 0, 0, 0, gather=False, workspace=one)):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            call()
