@@ -527,6 +527,12 @@ def _queue(what, stream, *tensors):
     return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
 
+def _status_word(t):
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise TypeError(f"dev_status must hold an int32, got {t.numel()} of {t.dtype}")
+    return _status(t)
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -628,7 +634,7 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, top_groups=1, renorm=Tr
     queue = _queue("nvfp4_route", stream, logits, bias, experts, weights, dev_status)
     _check(lib().nvfp4_route(_address(logits), _dtype_code(logits.dtype), T, E, _row_stride(logits),
                              _address(bias), int(bool(sigmoid)), groups, top_groups, k, int(bool(renorm)),
-                             scale, _address(experts), _address(weights), _status(dev_status),
+                             scale, _address(experts), _address(weights), _status_word(dev_status),
                              queue), "nvfp4_route")
     return experts, weights
 
@@ -649,7 +655,7 @@ def route_backward(logits, experts, dweights, sigmoid=False, renorm=True, scale=
     _check(lib().nvfp4_route_backward(_address(logits), _dtype_code(logits.dtype), T, E,
                                       _row_stride(logits), _address(experts), _address(dweights),
                                       int(bool(sigmoid)), k, int(bool(renorm)), scale,
-                                      _address(dlogits), _row_stride(dlogits), _status(dev_status),
+                                      _address(dlogits), _row_stride(dlogits), _status_word(dev_status),
                                       queue), "nvfp4_route_backward")
     return dlogits
 
@@ -669,7 +675,7 @@ def expert_plan(experts, n_experts, plan=None, workspace=None, dev_status=None, 
         raise ValueError(f"plan is for {plan.tokens} tokens, {plan.k} of {plan.experts} experts")
     queue = _queue("nvfp4_plan_experts", stream, experts, plan.offsets, workspace, dev_status)
     _check(lib().nvfp4_plan_experts(_address(experts), plan.ref, _address(workspace),
-                                    _status(dev_status), queue), "nvfp4_plan_experts")
+                                    _status_word(dev_status), queue), "nvfp4_plan_experts")
     return plan
 
 
@@ -698,7 +704,7 @@ def quantize_grouped(x, plan, flags, sign_mask=0, seed=0, offset=0, out_row=None
     _check(lib().nvfp4_quantize_grouped(
         _address(x), cols, _row_stride(x), plan.ref, sign_mask, flags, seed, offset,
         ctypes.byref(op_r) if op_r is not None else None,
-        ctypes.byref(op_c) if op_c is not None else None, _address(workspace), _status(dev_status),
+        ctypes.byref(op_c) if op_c is not None else None, _address(workspace), _status_word(dev_status),
         queue), "nvfp4_quantize_grouped")
     return out_row, out_col
 
@@ -721,7 +727,7 @@ def gemm_grouped(A, W, plan, out=None, out_dtype=torch.bfloat16, dev_status=None
     oa, ob = A.operand(), W.operand()
     _check(lib().nvfp4_gemm_grouped(ctypes.byref(oa), ctypes.byref(ob), plan.ref,
                                     _address(out), _dtype_code(out.dtype), _row_stride(out),
-                                    _status(dev_status), queue), "nvfp4_gemm_grouped")
+                                    _status_word(dev_status), queue), "nvfp4_gemm_grouped")
     return out
 
 
@@ -732,7 +738,7 @@ def gemm_grouped_k(A, B, plan, out=None, out_dtype=torch.float32, dev_status=Non
     oa, ob = A.operand(), B.operand()
     _check(lib().nvfp4_gemm_grouped_k(ctypes.byref(oa), ctypes.byref(ob),
                                       plan.ref, _address(out), _dtype_code(out.dtype),
-                                      _row_stride(out), _status(dev_status), queue),
+                                      _row_stride(out), _status_word(dev_status), queue),
            "nvfp4_gemm_grouped_k")
     return out
 
@@ -759,7 +765,7 @@ def experts_fprop(X, W, plan, gather=True, out=None, out_dtype=torch.bfloat16, w
     _check(lib().nvfp4_experts_fprop(_address(X), _row_stride(X), int(bool(gather)), ctypes.byref(op),
                                      plan.ref, I, O, _address(out),
                                      _dtype_code(out.dtype), _row_stride(out), _address(workspace),
-                                     _status(dev_status), queue), "nvfp4_experts_fprop")
+                                     _status_word(dev_status), queue), "nvfp4_experts_fprop")
     return out
 
 
@@ -776,7 +782,7 @@ def experts_dgrad(dY, Wt, plan, seed, offset, out=None, out_dtype=torch.bfloat16
     _check(lib().nvfp4_experts_dgrad(_address(dY), _row_stride(dY), ctypes.byref(op),
                                      plan.ref, I, O, seed, offset, _address(out),
                                      _dtype_code(out.dtype), _row_stride(out), _address(workspace),
-                                     _status(dev_status), queue), "nvfp4_experts_dgrad")
+                                     _status_word(dev_status), queue), "nvfp4_experts_dgrad")
     return out
 
 
@@ -793,7 +799,7 @@ def experts_wgrad(dY, X, plan, sign_mask, seed, offset, gather=True, out=None,
     _check(lib().nvfp4_experts_wgrad(_address(dY), _row_stride(dY), _address(X), _row_stride(X),
                                      int(bool(gather)), plan.ref, I, O, sign_mask,
                                      seed, offset, _address(out), _dtype_code(out.dtype),
-                                     _row_stride(out), _address(workspace), _status(dev_status),
+                                     _row_stride(out), _address(workspace), _status_word(dev_status),
                                      queue), "nvfp4_experts_wgrad")
     return out
 
@@ -807,7 +813,7 @@ def combine(Y, plan, weights=None, out=None, out_dtype=torch.bfloat16, dev_statu
     queue = _queue("nvfp4_combine", stream, Y, plan.pair_row, weights, out, dev_status)
     _check(lib().nvfp4_combine(_address(Y), Y.shape[1], _row_stride(Y), plan.ref,
                                _address(weights), _address(out), _dtype_code(out.dtype), _row_stride(out),
-                               _status(dev_status), queue), "nvfp4_combine")
+                               _status_word(dev_status), queue), "nvfp4_combine")
     return out
 
 
@@ -828,5 +834,5 @@ def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=
     _check(lib().nvfp4_combine_backward(_address(dout), _dtype_code(dout.dtype), _row_stride(dout),
                                         _address(Y), cols, _row_stride(Y), plan.ref,
                                         _address(weights), _address(dy), _row_stride(dy), _address(dweights),
-                                        _status(dev_status), queue), "nvfp4_combine_backward")
+                                        _status_word(dev_status), queue), "nvfp4_combine_backward")
     return dy, dweights

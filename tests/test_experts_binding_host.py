@@ -33,3 +33,30 @@ def test_a_workspace_whose_bytes_repeat_is_refused():
                  lambda: B.experts_wgrad(x, x, plan, 0, 0, 0, gather=False, workspace=one)):
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             call()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="passes host tensors as the device's")
+@pytest.mark.parametrize("status", [torch.zeros(4, dtype=torch.uint8)[1:2],
+                                    torch.zeros(1, dtype=torch.int64), torch.zeros(1),
+                                    torch.zeros(0, dtype=torch.int32)])
+def test_a_status_word_is_an_int32(monkeypatch, status):
+    """A kernel writes four bytes there, on a 4-byte boundary."""
+    monkeypatch.setattr(B, "_queue", lambda *a: None)  # the tensors here are the host's
+    plan = B.ExpertPlan.empty(10, 2, 4, device="cpu")
+    x, dw = torch.zeros(plan.rows, 128, dtype=torch.bfloat16), torch.zeros(10, 2)
+    W, Wt = (B.QuantizedTensor(*s, device="cpu") for s in ((4 * 128, 128), (128, 4 * 128)))
+    A, At = (B.QuantizedTensor(*s, device="cpu") for s in ((plan.rows, 128), (128, plan.rows)))
+    experts, logits = torch.zeros(10, 2, dtype=torch.int32), torch.zeros(10, 4)
+    for call in (lambda st: B.route(logits, 2, dev_status=st),
+                 lambda st: B.route_backward(logits, experts, dw, dev_status=st),
+                 lambda st: B.expert_plan(experts, 4, dev_status=st),
+                 lambda st: B.quantize_grouped(x, plan, B.ROWWISE, out_row=A, dev_status=st),
+                 lambda st: B.gemm_grouped(A, W, plan, dev_status=st),
+                 lambda st: B.gemm_grouped_k(At, At, plan, dev_status=st),
+                 lambda st: B.experts_fprop(x, W, plan, gather=False, dev_status=st),
+                 lambda st: B.experts_dgrad(x, Wt, plan, 0, 0, dev_status=st),
+                 lambda st: B.experts_wgrad(x, x, plan, 0, 0, 0, gather=False, dev_status=st),
+                 lambda st: B.combine(x, plan, dev_status=st),
+                 lambda st: B.combine_backward(torch.zeros(10, 128), x, plan, dw, dev_status=st)):
+        with pytest.raises(TypeError, match="dev_status"):
+            call(status)
