@@ -588,7 +588,16 @@ def _allocating(stream):
 
 class ExpertPlan:
     """The expert-ordered rows of a routing: offsets [experts + 1], pair_row [tokens, k] and
-    row_token [rows], int32 (nvfp4_expert_plan)."""
+    row_token [rows], int32 (nvfp4_expert_plan).  The tensors' contents may change, not the tensors:
+    the calls use the addresses taken here."""
+
+    _FIXED = frozenset(("offsets", "pair_row", "row_token", "tokens", "k", "experts", "rows",
+                        "_struct", "ref"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and "ref" in self.__dict__:
+            raise AttributeError(f"ExpertPlan.{name} cannot be replaced; make a plan of the new tensors")
+        super().__setattr__(name, value)
 
     def __init__(self, offsets, pair_row, row_token):
         if not (offsets.dtype == pair_row.dtype == row_token.dtype == torch.int32

@@ -60,3 +60,16 @@ def test_a_status_word_is_an_int32(monkeypatch, status):
                  lambda st: B.combine_backward(torch.zeros(10, 128), x, plan, dw, dev_status=st)):
         with pytest.raises(TypeError, match="dev_status"):
             call(status)
+
+
+def test_a_plans_tensors_cannot_be_replaced():
+    """The calls use the addresses that the plan was made with: a replaced tensor would leave them
+    reading memory that has been given back."""
+    plan = B.ExpertPlan.empty(10, 2, 4, device="cpu")
+    for name in ("offsets", "pair_row", "row_token", "tokens", "k", "experts", "rows", "ref"):
+        with pytest.raises(AttributeError, match=name):
+            setattr(plan, name, getattr(plan, name))
+    plan.offsets.zero_()    # their contents are the caller's
+    plan.note = "first layer"
+    other = B.ExpertPlan(plan.offsets.clone(), plan.pair_row, plan.row_token)
+    assert other._struct.offsets == other.offsets.data_ptr() != plan.offsets.data_ptr()
