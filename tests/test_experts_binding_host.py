@@ -73,3 +73,25 @@ def test_a_plans_tensors_cannot_be_replaced():
     plan.note = "first layer"
     other = B.ExpertPlan(plan.offsets.clone(), plan.pair_row, plan.row_token)
     assert other._struct.offsets == other.offsets.data_ptr() != plan.offsets.data_ptr()
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (64, 2, 4), (1000, 8, 64)])
+@pytest.mark.parametrize("I,O", [(1024, 128), (64, 2048), (1088, 1024), (64, 128)])
+def test_experts_workspaces_hold_what_the_calls_put_there(T, k, E, I, O):
+    """Codes, scales and amax of every operand a call quantizes, and both arrays of partial maxima:
+    fprop rows x I, dgrad rows x O, wgrad O x rows and I x rows."""
+    rows = B.expert_rows(T, k, E)
+
+    def operand(r, c):
+        assert B.codes_bytes(r, c) == r * c // 2
+        assert B.scales_bytes(r, c) == -(-r // 128) * 128 * (c // 16)
+        return r * c // 2 + -(-r // 128) * 128 * (c // 16) + 4
+    partials = B.workspace_bytes(rows, max(I, O))
+    assert partials >= 2 * 4 * 148
+    need = max(operand(rows, I), operand(rows, O), operand(O, rows) + operand(I, rows)) + partials
+    have = B.lib().nvfp4_experts_workspace_bytes(T, k, E, rows, I, O)
+    # every piece starts on a 256-byte boundary: less than 256 bytes of padding each
+    assert need <= have < need + 7 * 256
+    chunks = -(-T * k // 1024)
+    plan = B.lib().nvfp4_expert_plan_workspace_bytes(T, k, E)
+    assert plan == 0 if chunks == 1 else plan >= 4 * chunks * E

@@ -86,3 +86,35 @@ def test_the_router_takes_the_most_tokens(T):
     low, high = torch.aminmax(w[1000:T - 1000])
     assert abs(float(low) - middle) <= 8 * 2.0 ** -24 and abs(float(high) - middle) <= 8 * 2.0 ** -24
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("T,k,E,I,O", [(50, 2, 4, 1088, 128), (50, 2, 4, 64, 1024),
+                                       (5000, 4, 24, 320, 256)])
+def test_calls_stay_inside_their_workspaces(T, k, E, I, O):
+    """What lies behind a workspace of the documented size is left as it was."""
+    guards = []
+
+    def workspace(need):
+        w = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        guards.append(w[need:])
+        return w[:need] if need else None
+    rng = np.random.default_rng(T)
+    experts = torch.from_numpy(R.routing(rng, T, E, k)).cuda()
+    plan = B.expert_plan(experts, E, workspace=workspace(
+        B.lib().nvfp4_expert_plan_workspace_bytes(T, k, E)))
+    x, xe, dy = (to_device_bf16(synth.activations(s, seed=1))
+                 for s in ((T, I), (plan.rows, I), (plan.rows, O)))
+    w = B.quantize(to_device_bf16(synth.weights((E * O, I), seed=2)),
+                   B.ROWWISE | B.COLWISE | B.BLOCK2D)
+    need = B.experts_workspace_bytes(plan, I, O)
+    both = B.ROWWISE | B.COLWISE
+    for flags in (B.ROWWISE, B.COLWISE, both, both | B.SR):
+        B.quantize_grouped(xe, plan, flags, sign_mask=3,
+                           workspace=workspace(B.workspace_bytes(plan.rows, I, flags)))
+    for gather, a in ((True, x), (False, xe)):
+        B.experts_fprop(a, w[0], plan, gather=gather, workspace=workspace(need))
+        B.experts_wgrad(dy, a, plan, 5, 1, 0, gather=gather, workspace=workspace(need))
+    B.experts_dgrad(dy, w[1], plan, 1, 0, workspace=workspace(need))
+    torch.cuda.synchronize()
+    for g in guards:
+        assert (g == 0xA5).all()
