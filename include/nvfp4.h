@@ -421,8 +421,9 @@ size_t nvfp4_expert_plan_workspace_bytes(int64_t T, int64_t k, int64_t E);
  *             the top_groups ranges with the largest sum of their two best values (score + bias; of
  *             the one if only one is not excluded) are candidates.  groups <= 32.
  *   k       : experts per token, k <= E / groups * top_groups; chosen in falling order of score +
- *             bias.  Equal values go to the lower index.  The choice is that of scores in FP64
- *             (comparisons closer than FP32's error are decided there).
+ *             bias.  Equal values go to the lower index.  With a bias or groups the choice is that of
+ *             scores in FP64 (comparisons closer than FP32's error are decided there); with neither
+ *             the logits themselves are compared, also where their scores are equal in FP64.
  *   experts : T x k int32 out; -1 where fewer than k experts can be chosen.
  *   weights : T x k FP32 out: scale * score, divided by the sum of the chosen scores with
  *             `renormalize`; 0 where the expert is -1.

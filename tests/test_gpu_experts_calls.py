@@ -118,3 +118,24 @@ def test_calls_stay_inside_their_workspaces(T, k, E, I, O):
     torch.cuda.synchronize()
     for g in guards:
         assert (g == 0xA5).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_scores_that_fp64_cannot_tell_apart(sigmoid):
+    """Without a bias or groups the logits are compared, with either the scores: sigmoids of 40 and 50
+    are both 1 in FP64, softmax scores 800 below the largest both 0."""
+    l = torch.tensor([[40.0, 50.0, 40.0, -3.0], [50.0, 40.0, 50.0, -3.0], [0.0, -800.0, -790.0, -810.0]],
+                     device="cuda")
+    by_logit = [[1, 0, 2], [0, 2, 1], [0, 2, 1]]
+    if sigmoid:
+        by_score = [[0, 1, 2], [0, 1, 2], [0, 1, 2]]
+    else:        # exp(-10) it can, exp(-790) it cannot
+        by_score = [[1, 0, 2], [0, 2, 1], [0, 1, 2]]
+    st = _status()
+    e, _ = B.route(l, 3, sigmoid=sigmoid, dev_status=st)
+    assert e.tolist() == by_logit
+    e, _ = B.route(l, 3, sigmoid=sigmoid, bias=torch.zeros(4, device="cuda"), dev_status=st)
+    assert e.tolist() == by_score
+    e, _ = B.route(l, 3, sigmoid=sigmoid, groups=2, top_groups=2, dev_status=st)
+    assert e.tolist() == by_score
+    assert int(st) == 0
