@@ -16,10 +16,10 @@
 // tiles of 256) and a K block columns of it: such rows are computed and not stored, such columns are
 // loaded and not multiplied.
 //
-// B200, by rows: 8192 tokens to 8 of 64 experts, 4096 -> 2048, bf16 out: 265-290 us (1.1 PFLOP, 3.8-4.1
+// B200, by rows: 8192 tokens to 8 of 64 experts, 4096 -> 2048, bf16 out: 265-290 us (1.1 TFLOP, 3.8-4.1
 // PFLOP/s, the single product's rate at such K less the half tiles); one token to 8 experts, 4096
-// -> 4096: 23 us against 11.6 for its weights' bytes.  By K: 36700 rows, 32 x 2048 x 4096 FP32 out, 250
-// us; the 2.1 GB output of 64 experts alone takes 390 us (5.5 TB/s), with 1024 rows each 475.
+// -> 4096: 23 us against 11.6 for its weights' bytes.  By K: 36700 rows, 32 x 2048 x 4096 FP32 out,
+// 250-290 us; the 2.1 GB output of 64 experts alone takes 390 us (5.5 TB/s), with 1024 rows each 475.
 // Tried on both ends and not kept (same results):
 //  * loading only the 32-row quarters of A with tokens: 16 K blocks 14.4 against 12.1 us, the
 //    smaller boxes land later; skipping the empty half of a tile: the same time;

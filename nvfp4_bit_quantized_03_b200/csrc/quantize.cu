@@ -440,6 +440,9 @@ constexpr int tile_min_ctas()
     return tile_buffers<COL, BLOCK2D, RHT, SR, MX>() == 1 ? 8 : tile_ctas_per_sm<SR>();
 }
 
+// GROUPED, column-wise with the transform, B200, 65536 pairs of 4096: RTN 231 us, SR 385.  As above the
+// transform and the rounding take the time (issue slots 66 and 60 % busy at a third and a fifth of the
+// warps, HBM 34 and 20 %); both outputs, SR, 637 us.
 template <bool ROW, bool COL, bool BLOCK2D, bool RHT, bool SR, bool MX, bool GROUPED = false>
 __global__ void __launch_bounds__(128, (tile_min_ctas<ROW, COL, BLOCK2D, RHT, SR, MX>()))
     quant_tile_kernel(TileArgs a)
@@ -805,8 +808,9 @@ __global__ void __launch_bounds__(256) amax_grouped_kernel(const uint16_t* __res
 
 // The same of the random Hadamard transform along the expert-ordered rows (and, with PLAIN, of the
 // rows themselves): a warp takes 16 rows x 128 columns; its lanes look up one row each and pass
-// the places on.  Bound by instruction issue (the transform and its unpacking).  B200, 36700 rows:
-// of 4096 columns 63 us, of 2048 31 us; four CTAs per SM instead of three, with spills, 7 % more.
+// the places on.  B200, 36700 rows: of 4096 columns 63 us, of 2048 31 us; four CTAs per SM instead of
+// three, with spills, 7 % more.  No limit is reached (69400 rows of 4096: issue slots 63 % busy, HBM 54 %,
+// a third of the warps): a warp transforms its rows only when all have come, and loads none meanwhile.
 template <bool PLAIN>
 __global__ void __launch_bounds__(256) amax_rht_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, uint32_t sign_mask,
@@ -918,8 +922,9 @@ __device__ __forceinline__ uint32_t small_amax(const uint16_t* x, int64_t rows, 
 // B200: 8192 tokens of 4096 to 8 experts each (67 MB in, 151 MB out) 62 us.  The stores bound it: with
 // none 32 us, with the codes' alone 50; a token's scale words lie 512 bytes apart in the MMA
 // layout.  Codes sent out as bulk copies from shared memory, or the rows looked up ahead, take the
-// same time.  Stochastic, bound by issue: 65536 pairs of 4096 270 us (the row-wise pass of the linear layer
-// does as many elements per second), 6000 of 1536 15.5 us.
+// same time.  In expert order (65536 pairs of 4096, 537 MB in) 122 us, 5.6 TB/s.  Stochastic 268 us (the
+// row-wise pass of the linear layer does as many elements per second), 6000 of 1536 15.5 us: issue slots 61
+// % busy at a third of the warps, which 80 registers leave, HBM 30 %; nothing else is near a limit.
 template <bool SR, bool SCATTER>
 __global__ void __launch_bounds__(256, SR ? 3 : 5) quant_grouped_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld, QuantSource src,

@@ -332,7 +332,10 @@ __device__ __forceinline__ int choose_fast(const RouteArgs& a, const float (&x)[
     return mine;
 }
 
-// The choice in FP64, for groups of any size.  values: the warp's shared buffer of E.
+// The choice in FP64, for groups of any size: for comparisons too close for FP32, and for every token
+// where groups end inside lanes.  values: the warp's shared buffer of E.  Bound by instruction issue
+// (73 % of the slots): 2785 instructions a token of 160 experts.  B200, 16384 tokens, sigmoid, bias, 4 of 8 groups, k 8, FP64
+// for all: 160 experts 56 us, 192 57, 320 133, 384 140 (against the fast choice at 128 16, at 256 21).
 template <int NPL>
 __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&x)[NPL], float mx,
                                          int lane, double* values, bool& bad)
@@ -397,12 +400,14 @@ __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&x)
 }
 
 // A warp per token; lane l holds the logits of experts l * NPL .. l * NPL + NPL - 1, so that the
-// lowest lane with a value has the lowest index and a row is read in 16-byte loads.  Bound by
-// instruction issue: a token of 256 experts takes 857 instructions (scores 160, sort 40, groups
-// 90, k + 1 rounds of about 20, weights 100).  B200: 16384 x 256 FP32 logits, sigmoid, bias, 4 of 8
-// groups, k 8: 22 us (51 us with the rounds searching unsorted keys and exact scores; 26 with the
-// FP64 choice in a function of its own, which keeps the logits in local memory); one
-// token 2.6 us, a launch.
+// lowest lane with a value has the lowest index and a row is read in 16-byte loads.  B200: 16384 x
+// 256 FP32 logits, sigmoid, bias, 4 of 8 groups, k 8: 21-22 us (51 us with the rounds searching unsorted
+// keys and exact scores; 26 with the FP64 choice in a function of its own, which keeps the logits in
+// local memory).  A token takes 848 instructions (scores 160, sort 40, groups 90, k + 1 rounds of about
+// 20, weights 100), together 12 us of issue: the slots are 77 % busy for the 16.5 us that an SM has
+// work, the rest of them waits in the rounds' chain of reduce, ballot and shift; launch, first loads and
+// the last CTAs are the other 5 us.  Without bias and groups, k 8: FP32 11.6 us, bf16 11.0; one token 2.6
+// us, a launch.
 template <int NPL, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a)
 {
@@ -504,7 +509,7 @@ struct RouteBackwardArgs {
 //   sigmoid:               dl_i = g_i s_i (1 - s_i)               on S
 // A warp per token; lane j holds the j-th chosen expert.  A row without one has zero gradient.
 // Renormalised weights need only the chosen logits, so a row is written and, but for them, not
-// read.  B200: 8192 x 128 bf16 4.2 us, of which a launch is 2.
+// read.  B200, 8192 x 128 bf16, k 8: 4.2 us (softmax; not renormalised 4.6), of which a launch is 2.
 template <int NPL, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_backward_kernel(const RouteBackwardArgs a)
 {
