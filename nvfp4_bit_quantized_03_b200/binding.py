@@ -608,12 +608,14 @@ class ExpertPlan:
                              "must be contiguous int32 tensors")
         if not offsets.device == pair_row.device == row_token.device:
             raise ValueError("plan: its tensors are on one device")
-        self.offsets, self.pair_row, self.row_token = offsets, pair_row, row_token
-        self.tokens, self.k = pair_row.shape
-        self.experts, self.rows = offsets.shape[0] - 1, row_token.shape[0]
-        self._struct = PlanStruct(offsets.data_ptr(), pair_row.data_ptr(), row_token.data_ptr(),
-                                  self.tokens, self.k, self.experts, self.rows)
-        self.ref = ctypes.byref(self._struct)  # what the C calls take
+        tokens, k = pair_row.shape
+        experts, rows = offsets.shape[0] - 1, row_token.shape[0]
+        struct = PlanStruct(offsets.data_ptr(), pair_row.data_ptr(), row_token.data_ptr(), tokens, k,
+                            experts, rows)
+        # at once, not through __setattr__ (half of a plan's time on the host)
+        self.__dict__.update(offsets=offsets, pair_row=pair_row, row_token=row_token, tokens=tokens, k=k,
+                             experts=experts, rows=rows, _struct=struct,
+                             ref=ctypes.byref(struct))  # what the C calls take
 
     @classmethod
     def empty(cls, tokens, k, experts, rows=None, device="cuda"):
