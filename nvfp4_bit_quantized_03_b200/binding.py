@@ -528,9 +528,11 @@ def _queue(what, stream, *tensors):
 
 
 def _status_word(t):
-    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+    if t is None:
+        return None if _active is LIB_PATH else _status(None)
+    if t.dtype != torch.int32 or t.numel() < 1:
         raise TypeError(f"dev_status must hold an int32, got {t.numel()} of {t.dtype}")
-    return _status(t)
+    return t.data_ptr()
 
 
 def _address(t):
@@ -600,7 +602,7 @@ class ExpertPlan:
         super().__setattr__(name, value)
 
     def __init__(self, offsets, pair_row, row_token):
-        if not (offsets.dtype == pair_row.dtype == row_token.dtype == torch.int32
+        if not (offsets.dtype is pair_row.dtype is row_token.dtype is torch.int32
                 and offsets.dim() == row_token.dim() == 1 and pair_row.dim() == 2
                 and offsets.is_contiguous() and pair_row.is_contiguous()
                 and row_token.is_contiguous()):
@@ -609,7 +611,7 @@ class ExpertPlan:
         if not offsets.device == pair_row.device == row_token.device:
             raise ValueError("plan: its tensors are on one device")
         tokens, k = pair_row.shape
-        experts, rows = offsets.shape[0] - 1, row_token.shape[0]
+        experts, rows = offsets.numel() - 1, row_token.numel()
         struct = PlanStruct(offsets.data_ptr(), pair_row.data_ptr(), row_token.data_ptr(), tokens, k,
                             experts, rows)
         # at once, not through __setattr__ (half of a plan's time on the host)
