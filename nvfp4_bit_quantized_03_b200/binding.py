@@ -120,7 +120,10 @@ def _report_word():
 
 
 def _take_reports():
-    """The bits of all words, which are cleared."""
+    """The bits of all words, which are cleared.  (None while capturing: nothing runs then, and the
+    device cannot be waited for.)"""
+    if _reports and torch.cuda.is_current_stream_capturing():
+        return 0
     bits = 0
     for device, word in _reports.items():
         torch.cuda.synchronize(device)

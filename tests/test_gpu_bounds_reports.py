@@ -48,3 +48,23 @@ def test_a_report_made_while_capturing_is_seen_after_the_replay():
             with torch.cuda.graph(graph):
                 B.selftest_bounds(None)
             graph.replay()
+
+
+def test_a_block_may_lie_inside_a_capture():
+    need_gpu()
+    x = torch.randn(3, 4, device="cuda")
+    with B.bounds_checked():
+        ref = B.route(x, 2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with B.bounds_checked():
+            got = B.route(x, 2)
+    graph.replay()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    with pytest.raises(B.NVFP4Error, match="outside its buffer"):
+        with B.bounds_checked():
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                with B.bounds_checked():
+                    B.selftest_bounds(None)
+            graph.replay()
