@@ -551,6 +551,74 @@ nvfp4_status nvfp4_combine_backward(const void* dout, int dout_dtype, int64_t ld
                                     void* dY_bf16, int64_t lddy, float* dweights, int* dev_status,
                                     void* stream);
 
+/*
+ * ---- Around a layer's products -----------------------------------------------------------
+ * What stands directly behind the query-key-value product of an attention layer, its gradient, and
+ * what the weight gradients become before they update the weights.  The pages have no counterpart
+ * to these calls.
+ */
+
+/* Heads of a batch of tokens: value d of head h of token t is data[t * token_stride + h *
+ * head_stride + d] (strides in elements), whatever lies between: a part of the product's output
+ * rows, or an array by token or by head.  Device pointers, 16-byte aligned; strides multiples of 16
+ * bytes.  Heads that are written must not overlap; those that are read may (a stride of 0).  The stride
+ * of a single token or head is not used. */
+typedef struct {
+    void* data;
+    int64_t heads;
+    int64_t token_stride;
+    int64_t head_stride;
+} nvfp4_heads;
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the same pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight over the head's head_dim values, then the first `rotary`
+ *   values of y turned in pairs (a, b) -> (a cos - b sin, b cos + a sin) by the angles of the token's
+ *   position.
+ *   q, k      : heads before, FP32 or bf16 (in_dtype: NVFP4_OUT_F32 / NVFP4_OUT_BF16).  k may be NULL or
+ *               have no heads.
+ *   q_weight, k_weight : head_dim FP32, or NULL for ones.
+ *   positions : tokens int32, or NULL: token t has position t.  A token with a negative position is
+ *               padding: its heads are not looked at and its outputs are zeros.  A position beyond
+ *               the table counts as padding too and sets NVFP4_DEVSTAT_INDEX.
+ *   table     : table_rows x rotary FP32, row p the rotary / 2 cosines and then the sines of position
+ *               p's angles (NULL with rotary 0: no rotation).
+ *   interleaved : the pairs are (2 i, 2 i + 1) instead of (i, i + rotary / 2).
+ *   q_out, k_out : heads after, FP32 or bf16 (out_dtype).  They may be q and k themselves (the same
+ *               addresses, strides and type).
+ * Computed in FP32 and rounded once to the output type; heads with NaN or Inf give NaN of their own.
+ * Shape rules: tokens >= 1, head_dim a multiple of 16 up to 512, rotary a multiple of 16 up to
+ * head_dim, table_rows >= tokens without positions; 1e-30 <= eps <= 1e30.
+ */
+nvfp4_status nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, int in_dtype, int64_t tokens,
+                                int64_t head_dim, const float* q_weight, const float* k_weight, float eps,
+                                const int32_t* positions, const float* table, int64_t table_rows,
+                                int64_t rotary, int interleaved, const nvfp4_heads* q_out,
+                                const nvfp4_heads* k_out, int out_dtype, int* dev_status, void* stream);
+
+/* Device workspace of nvfp4_qk_norm_rope_backward (0 for sizes outside the rules). */
+size_t nvfp4_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t head_dim);
+
+/*
+ * Gradient of nvfp4_qk_norm_rope.
+ *   dq, dk       : gradients of q_out and k_out (grad_dtype).
+ *   q, k, q_weight, k_weight, eps, positions, table, table_rows, rotary, interleaved : as in the
+ *                  forward call (q and k before the norm; in_dtype).
+ *   dq_in, dk_in : gradients of q and k (dx_dtype), all written: zeros for padding, whose gradients are
+ *                  not looked at.  They may be dq and dk, or q and k, themselves.
+ *   dq_weight, dk_weight : head_dim FP32, gradients of the weights, summed over tokens and heads in a
+ *                  fixed order; NULL where not wanted.
+ *   workspace    : nvfp4_qk_norm_rope_workspace_bytes(...) device bytes.
+ */
+nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads* dq, const nvfp4_heads* dk, int grad_dtype,
+                                         const nvfp4_heads* q, const nvfp4_heads* k, int in_dtype,
+                                         int64_t tokens, int64_t head_dim, const float* q_weight,
+                                         const float* k_weight, float eps, const int32_t* positions,
+                                         const float* table, int64_t table_rows, int64_t rotary,
+                                         int interleaved, const nvfp4_heads* dq_in, const nvfp4_heads* dk_in,
+                                         int dx_dtype, float* dq_weight, float* dk_weight, void* workspace,
+                                         int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

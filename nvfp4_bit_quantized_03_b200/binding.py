@@ -38,6 +38,11 @@ class Operand(ctypes.Structure):
                 ("amax", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class HeadsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 class PlanStruct(ctypes.Structure):
     _fields_ = [("offsets", ctypes.c_void_p), ("pair_row", ctypes.c_void_p),
                 ("row_token", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("k", ctypes.c_int64),
@@ -193,7 +198,14 @@ def _open(path):
     L.nvfp4_expert_plan_workspace_bytes.restype = sz
     L.nvfp4_experts_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
     L.nvfp4_experts_workspace_bytes.restype = sz
+    L.nvfp4_qk_norm_rope_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.nvfp4_qk_norm_rope_workspace_bytes.restype = sz
+    hd = ctypes.POINTER(HeadsStruct)
     for name, argtypes in {
+            "qk_norm_rope": [hd, hd, i32, i64, i64, vp, vp, f32, vp, vp, i64, i64, i32, hd, hd, i32, vp,
+                             vp],
+            "qk_norm_rope_backward": [hd, hd, i32, hd, hd, i32, i64, i64, vp, vp, f32, vp, vp, i64, i64,
+                                      i32, hd, hd, i32, vp, vp, vp, vp, vp],
             "route": [vp, i32, i64, i64, i64, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp],
             "route_backward": [vp, i32, i64, i64, i64, vp, vp, i32, i32, i32, f32, vp, i64, vp, vp],
             "plan_experts": [vp, pl, vp, vp, vp],
@@ -852,3 +864,125 @@ def combine_backward(dout, Y, plan, weights, dy=None, dweights=None, dev_status=
                                         _address(weights), _address(dy), _row_stride(dy), _address(dweights),
                                         _status_word(dev_status), queue), "nvfp4_combine_backward")
     return dy, dweights
+
+
+# ---- around a layer's products ------------------------------------------------------------
+
+def rope_table(positions, rotary, base=10000.0, device="cuda"):
+    """The table of qk_norm_rope for positions 0 .. positions - 1 (float32 [positions, rotary]): cosines,
+    then sines, of p base^(-2 i / rotary), taken in float64."""
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"rotary must be even and at least 2, got {rotary}")
+    i = torch.arange(rotary // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * base ** (-2 * i / rotary)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def _heads(what, t, dtypes, tokens, heads, dim):
+    """The nvfp4_heads of a tensor [tokens, heads, dim] and the reference a call takes."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) or (
+            t.shape[2] != dim) or t.stride(2) != 1:
+        raise ValueError(f"{what} must be [{tokens}, {'heads' if heads is None else heads}, {dim}] with unit "
+                         f"stride in a head, got {tuple(t.shape)} strides {t.stride()}")
+    return HeadsStruct(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _rotation(positions, table, tokens):
+    """rows and width of the table (0, 0 without one)."""
+    if positions is not None:
+        _dense("positions", positions, torch.int32, (tokens,))
+    if table is None:
+        return 0, 0
+    _dense("table", table, torch.float32, table.shape)
+    if table.dim() != 2:
+        raise ValueError(f"table must be [positions, rotary], got {tuple(table.shape)}")
+    return table.shape
+
+
+def _head_weights(dim, **weights):
+    for name, w in weights.items():
+        if w is not None:
+            _dense(name, w, torch.float32, (dim,))
+
+
+def qk_norm_rope(q, k, positions=None, table=None, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, out_dtype=torch.bfloat16, dev_status=None,
+                 stream=None):
+    """nvfp4_qk_norm_rope: every head of q [T, Hq, D] and k [T, Hk, D] (k may be None) normalised, times
+    its weight, and rotated by its token's position (table: rope_table; None: no rotation).  The
+    outputs' type is that of q_out and k_out when given, else out_dtype."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, dim], got {tuple(q.shape)}")
+    T, Hq, D = q.shape
+    rows, rotary = _rotation(positions, table, T)
+    _head_weights(D, q_weight=q_weight, k_weight=k_weight)
+    xq = _heads("q", q, _F32_BF16, T, Hq, D)
+    xk = None if k is None else _heads("k", k, (q.dtype,), T, None, D)
+    with _allocating(stream):
+        if q_out is None:
+            q_out = _poisoned(torch.empty((T, Hq, D), dtype=out_dtype if k_out is None else k_out.dtype,
+                                          device=q.device))
+        if k_out is None and k is not None:
+            k_out = _poisoned(torch.empty((T, k.shape[1], D), dtype=q_out.dtype, device=q.device))
+    zq = _heads("q_out", q_out, _F32_BF16, T, Hq, D)
+    zk = None if k is None else _heads("k_out", k_out, (q_out.dtype,), T, k.shape[1], D)
+    queue = _queue("nvfp4_qk_norm_rope", stream, q, k, positions, table, q_weight, k_weight, q_out,
+                   k_out if k is not None else None, dev_status)
+    _check(lib().nvfp4_qk_norm_rope(
+        ctypes.byref(xq), _ref(xk), _dtype_code(q.dtype), T, D, _address(q_weight), _address(k_weight), eps,
+        _address(positions), _address(table), rows, rotary, int(bool(interleaved)), ctypes.byref(zq),
+        _ref(zk), _dtype_code(q_out.dtype), _status_word(dev_status), queue), "nvfp4_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq, dk, q, k, positions=None, table=None, q_weight=None, k_weight=None, eps=1e-6,
+                          interleaved=False, dq_in=None, dk_in=None, dx_dtype=torch.bfloat16,
+                          dq_weight=None, dk_weight=None, workspace=None, dev_status=None, stream=None):
+    """nvfp4_qk_norm_rope_backward: (dq_in, dk_in, dq_weight, dk_weight), the gradients of q, k (before
+    the norm) and of the weights (float32 [D], also where a weight is None)."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, dim], got {tuple(q.shape)}")
+    T, Hq, D = q.shape
+    if (k is None) != (dk is None):
+        raise ValueError("dk must be given with k and only with it")
+    Hk = 0 if k is None else k.shape[1]
+    rows, rotary = _rotation(positions, table, T)
+    _head_weights(D, q_weight=q_weight, k_weight=k_weight)
+    xq = _heads("q", q, _F32_BF16, T, Hq, D)
+    xk = None if k is None else _heads("k", k, (q.dtype,), T, None, D)
+    zq = _heads("dq", dq, _F32_BF16, T, Hq, D)
+    zk = None if k is None else _heads("dk", dk, (dq.dtype,), T, Hk, D)
+    with _allocating(stream):
+        if dq_in is None:
+            dq_in = _poisoned(torch.empty((T, Hq, D), dtype=dx_dtype if dk_in is None else dk_in.dtype,
+                                          device=q.device))
+        if dk_in is None and k is not None:
+            dk_in = _poisoned(torch.empty((T, Hk, D), dtype=dq_in.dtype, device=q.device))
+        if dq_weight is None:
+            dq_weight = _poisoned(_new((D,), torch.float32, q.device))
+        if dk_weight is None and k is not None:
+            dk_weight = _poisoned(_new((D,), torch.float32, q.device))
+        need = lib().nvfp4_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
+        if workspace is None:
+            workspace = _workspace(need, q.device)
+    _workspace_size(workspace, need)
+    _head_weights(D, dq_weight=dq_weight, dk_weight=dk_weight)
+    gq = _heads("dq_in", dq_in, _F32_BF16, T, Hq, D)
+    gk = None if k is None else _heads("dk_in", dk_in, (dq_in.dtype,), T, Hk, D)
+    if k is None:
+        dk_in = dk_weight = None
+    queue = _queue("nvfp4_qk_norm_rope_backward", stream, dq, dk, q, k, positions, table, q_weight, k_weight,
+                   dq_in, dk_in, dq_weight, dk_weight, workspace, dev_status)
+    _check(lib().nvfp4_qk_norm_rope_backward(
+        ctypes.byref(zq), _ref(zk), _dtype_code(dq.dtype), ctypes.byref(xq), _ref(xk), _dtype_code(q.dtype),
+        T, D, _address(q_weight), _address(k_weight), eps, _address(positions), _address(table), rows, rotary,
+        int(bool(interleaved)), ctypes.byref(gq), _ref(gk), _dtype_code(dq_in.dtype), _address(dq_weight),
+        _address(dk_weight), _address(workspace), _status_word(dev_status), queue),
+        "nvfp4_qk_norm_rope_backward")
+    return dq_in, dk_in, dq_weight, dk_weight

@@ -29,6 +29,8 @@ UNITS = {
     "route.cu": [],
     "combine.cu": [],
     "experts.cu": [],
+    "qk_norm.cu": [],
+    "layer.cu": [],
     "noalloc.cu": [],
 }
 # library path, object folder and extra defines of each variant

@@ -1,0 +1,165 @@
+// C entry points of the operators around a layer's products (include/nvfp4.h): argument checks,
+// workspace carving and dispatch to qk_norm.cu.  As everywhere in the library: no allocation, no
+// synchronization, and nothing queued when an argument is invalid.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "api_common.h"
+
+using namespace nvfp4;
+
+namespace {
+
+constexpr int64_t kMaxHeads = 1 << 20;
+constexpr int64_t kMaxTokens = 1 << 30;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+bool known_type(int dtype) { return dtype == NVFP4_OUT_F32 || dtype == NVFP4_OUT_BF16; }
+
+bool heads_sizes_ok(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t head_dim)
+{
+    return tokens >= 1 && tokens <= kMaxTokens && heads_q >= 1 && heads_q <= kMaxHeads && heads_k >= 0 &&
+           heads_k <= kMaxHeads && head_dim >= 16 && head_dim <= kMaxHeadDim && head_dim % 16 == 0;
+}
+
+// A view of `heads` heads; `written`: no two of its values share a place.
+nvfp4_status check_heads(const nvfp4_heads& v, int64_t heads, int64_t tokens, int64_t D, int dtype,
+                         bool written)
+{
+    if (!v.data) return NVFP4_ERR_NULL;
+    if (v.heads != heads || v.token_stride < 0 || v.head_stride < 0 || v.token_stride > kMaxStride ||
+        v.head_stride > kMaxStride)
+        return NVFP4_ERR_SHAPE;
+    const int64_t per16 = dtype == NVFP4_OUT_F32 ? 4 : 8;
+    if (!aligned16(v.data) || (tokens > 1 && v.token_stride % per16) || (heads > 1 && v.head_stride % per16))
+        return NVFP4_ERR_ALIGN;
+    if (written) {
+        const int64_t across_heads = heads > 1 ? (heads - 1) * v.head_stride + D : D;
+        const int64_t across_tokens = tokens > 1 ? (tokens - 1) * v.token_stride + D : D;
+        const bool by_token = (heads == 1 || v.head_stride >= D) &&
+                              (tokens == 1 || v.token_stride >= across_heads);
+        const bool by_head = (tokens == 1 || v.token_stride >= D) &&
+                             (heads == 1 || v.head_stride >= across_tokens);
+        if (!by_token && !by_head) return NVFP4_ERR_SHAPE;
+    }
+    return NVFP4_OK;
+}
+
+struct HeadsPair {  // a view of the queries' and of the keys' heads
+    const nvfp4_heads* q;
+    const nvfp4_heads* k;
+    int dtype;
+    bool written;
+};
+
+nvfp4_status take_heads(const HeadsPair& in, int64_t heads_q, int64_t heads_k, int64_t tokens, int64_t D,
+                        HeadsView* out)
+{
+    if (!in.q || (heads_k > 0 && !in.k)) return NVFP4_ERR_NULL;
+    if (!known_type(in.dtype)) return NVFP4_ERR_ARG;
+    nvfp4_status st = check_heads(*in.q, heads_q, tokens, D, in.dtype, in.written);
+    if (st != NVFP4_OK) return st;
+    if (heads_k > 0 && (st = check_heads(*in.k, heads_k, tokens, D, in.dtype, in.written)) != NVFP4_OK)
+        return st;
+    const nvfp4_heads none = {nullptr, 0, 0, 0};
+    for (int i = 0; i < 2; ++i) {
+        const nvfp4_heads& v = i == 0 ? *in.q : (heads_k > 0 ? *in.k : none);
+        // a single token's or head's stride is never used
+        out[i] = HeadsView{v.data, v.heads, tokens > 1 ? v.token_stride : 0, v.heads > 1 ? v.head_stride : 0};
+    }
+    return NVFP4_OK;
+}
+
+// What both directions share; in[0] is x.
+nvfp4_status head_args(HeadsArgs& a, const HeadsPair* in, HeadsView* const* views, int n, int64_t tokens,
+                       int64_t D, const float* q_weight, const float* k_weight, float eps,
+                       const int32_t* positions, const float* table, int64_t table_rows, int64_t rotary,
+                       int* dev_status)
+{
+    if (!in[0].q) return NVFP4_ERR_NULL;
+    const int64_t hq = in[0].q->heads, hk = in[0].k ? in[0].k->heads : 0;
+    if (!heads_sizes_ok(tokens, hq, hk, D)) return NVFP4_ERR_SHAPE;
+    if (rotary < 0 || rotary > D || rotary % 16) return NVFP4_ERR_SHAPE;
+    if (rotary > 0 && (table_rows < 1 || table_rows >= kMaxDim)) return NVFP4_ERR_SHAPE;
+    if (rotary > 0 && !table) return NVFP4_ERR_NULL;
+    if (rotary > 0 && !positions && table_rows < tokens) return NVFP4_ERR_SHAPE;
+    // squares below FP32's smallest are zeros, which a smaller eps would show
+    if (!(eps >= 1e-30f) || !(eps <= 1e30f)) return NVFP4_ERR_ARG;
+    for (int i = 0; i < n; ++i) {
+        const nvfp4_status st = take_heads(in[i], hq, hk, tokens, D, views[i]);
+        if (st != NVFP4_OK) return st;
+    }
+    if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned16(table) || !aligned4(positions))
+        return NVFP4_ERR_ALIGN;
+    a.weight[0] = q_weight;
+    a.weight[1] = k_weight;
+    a.positions = positions;
+    a.table = table;
+    a.tokens = tokens;
+    a.table_rows = table_rows;
+    a.D = static_cast<int>(D);
+    a.rotary = static_cast<int>(rotary);
+    a.eps = eps;
+    a.dev_status = dev_status;
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, int in_dtype, int64_t tokens,
+                                int64_t head_dim, const float* q_weight, const float* k_weight, float eps,
+                                const int32_t* positions, const float* table, int64_t table_rows,
+                                int64_t rotary, int interleaved, const nvfp4_heads* q_out,
+                                const nvfp4_heads* k_out, int out_dtype, int* dev_status, void* stream)
+{
+    HeadsArgs a = {};
+    const HeadsPair in[2] = {{q, k, in_dtype, false}, {q_out, k_out, out_dtype, true}};
+    HeadsView* const views[2] = {a.x, a.z};
+    nvfp4_status st = head_args(a, in, views, 2, tokens, head_dim, q_weight, k_weight, eps, positions, table,
+                                table_rows, rotary, dev_status);
+    if (st != NVFP4_OK) return st;
+    int sms = 0;
+    if ((st = current_device(&sms)) != NVFP4_OK) return st;
+    return from_cuda(launch_qk_norm_rope(a, in_dtype == NVFP4_OUT_F32, out_dtype == NVFP4_OUT_F32,
+                                         interleaved != 0, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t head_dim)
+{
+    if (!heads_sizes_ok(tokens, heads_q, heads_k, head_dim)) return 0;
+    return sizeof(float) * static_cast<size_t>(head_dim) *
+           static_cast<size_t>(qk_backward_ctas(tokens, heads_q, heads_k, head_dim));
+}
+
+nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads* dq, const nvfp4_heads* dk, int grad_dtype,
+                                         const nvfp4_heads* q, const nvfp4_heads* k, int in_dtype,
+                                         int64_t tokens, int64_t head_dim, const float* q_weight,
+                                         const float* k_weight, float eps, const int32_t* positions,
+                                         const float* table, int64_t table_rows, int64_t rotary,
+                                         int interleaved, const nvfp4_heads* dq_in, const nvfp4_heads* dk_in,
+                                         int dx_dtype, float* dq_weight, float* dk_weight, void* workspace,
+                                         int* dev_status, void* stream)
+{
+    HeadsArgs a = {};
+    const HeadsPair in[3] = {{q, k, in_dtype, false}, {dq, dk, grad_dtype, false}, {dq_in, dk_in, dx_dtype, true}};
+    HeadsView* const views[3] = {a.x, a.z, a.dx};
+    nvfp4_status st = head_args(a, in, views, 3, tokens, head_dim, q_weight, k_weight, eps, positions, table,
+                                table_rows, rotary, dev_status);
+    if (st != NVFP4_OK) return st;
+    if (!workspace) return NVFP4_ERR_NULL;
+    if (!aligned16(workspace) || !aligned4(dq_weight) || !aligned4(dk_weight)) return NVFP4_ERR_ALIGN;
+    a.partials = static_cast<float*>(workspace);
+    a.dweight[0] = dq_weight;
+    a.dweight[1] = dk_weight;
+    int sms = 0;
+    if ((st = current_device(&sms)) != NVFP4_OK) return st;
+    return from_cuda(launch_qk_norm_rope_backward(a, in_dtype == NVFP4_OUT_F32, grad_dtype == NVFP4_OUT_F32,
+                                                  dx_dtype == NVFP4_OUT_F32, interleaved != 0,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -214,6 +214,36 @@ struct CombineArgs {
 cudaError_t launch_combine(const CombineArgs& a, bool f32, int sm_count, cudaStream_t s);
 cudaError_t launch_combine_backward(const CombineArgs& a, bool f32, int sm_count, cudaStream_t s);
 
+// Norms and rotation of queries and keys (qk_norm.cu): index 0 the queries, 1 the keys.
+constexpr int kMaxHeadDim = 512;     // a head's units of 16 values fill at most one warp
+constexpr int kMaxHeadCtas = 1776;   // CTAs of the gradient (12 per SM), i.e. rows of its partial sums
+struct HeadsView {
+    void* data;
+    int64_t heads, token_stride, head_stride;  // strides in elements
+};
+struct HeadsArgs {
+    HeadsView x[2];       // heads before the norm
+    HeadsView z[2];       // after the rotation (backward: its gradients)
+    HeadsView dx[2];      // backward: gradients of x
+    const float* weight[2];
+    float* dweight[2];
+    float* partials;      // backward: a row of D sums per CTA
+    const int32_t* positions;
+    const float* table;   // table_rows x rotary: cosines, then sines
+    int64_t tokens, table_rows;
+    int D, rotary;
+    float eps, inv_D;
+    int lanes;            // lanes per head (set by the launch, as below)
+    int slices;           // items a token's heads are split into
+    int q_ctas;           // backward: the CTAs of the queries
+    int* dev_status;
+};
+cudaError_t launch_qk_norm_rope(HeadsArgs a, bool in_f32, bool out_f32, bool interleaved, int sm_count,
+                                cudaStream_t s);
+int qk_backward_ctas(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t D);
+cudaError_t launch_qk_norm_rope_backward(HeadsArgs a, bool x_f32, bool z_f32, bool dx_f32, bool interleaved,
+                                         cudaStream_t s);
+
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, int sm_count, cudaStream_t s);
 // A kernel whose only thread waits, with the GEMM's bounded-wait routine, on an mbarrier that
 // nothing completes; it records NVFP4_DEVSTAT_TIMEOUT after limit_ns and returns.
