@@ -619,6 +619,34 @@ nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads* dq, const nvfp4_head
                                          int dx_dtype, float* dq_weight, float* dk_weight, void* workspace,
                                          int* dev_status, void* stream);
 
+/* Device workspace of nvfp4_orthogonalize (0 for sizes outside the rules). */
+size_t nvfp4_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+/*
+ * Newton-Schulz orthogonalisation of weight gradients (or their momentum): the update of the Muon
+ * optimiser, for every matrix of a batch by itself (the gradients of a layer of experts are a batch of E).
+ *   X = G / (|G|_F + eps);  per step (a, b, c):  A = X X^T,  X <- a X + (b A + c A^2) X;  out = X
+ * (from the other side, X^T X, where G has more rows than columns: the same in exact arithmetic).  Singular
+ * values s of X become a s + b s^3 + c s^5 in every step; with the usual (3.4445, -4.7750, 2.0315) five
+ * steps bring those above about 0.01 into 0.68 .. 1.2.
+ *   G           : batch matrices rows x cols, FP32 or bf16 (g_dtype), row stride ldg, matrix stride
+ *                 g_stride (elements, any alignment; 0 is allowed: one matrix or row for all).
+ *   coefficients : HOST memory, steps x (a, b, c); read before the call returns.  Singular values must stay
+ *                 below 4 and |b s^2 + c s^4| below 64 throughout: FP16 copies of A and B overflow beyond.
+ *   out_bf16    : batch matrices rows x cols, row stride ldo >= cols, matrices apart.  With a 16-byte
+ *                 aligned address and cols, ldo and out_stride multiples of 8 it is written by tensor
+ *                 copies, otherwise value by value.  It may be G itself if that is bf16 with the same strides.
+ *   workspace   : nvfp4_orthogonalize_workspace_bytes(...) device bytes.
+ * Products take FP16 operands (11 significant bits) and FP32 accumulators, X stays in FP32 between steps:
+ * the error is about that of the final rounding to bf16.  A matrix of zeros gives zeros, one with NaN or Inf
+ * too (and sets NVFP4_DEVSTAT_NONFINITE).
+ * Limits: rows, cols <= 2^18, batch <= 65535, batch * rows * cols <= 2^36, 1 <= steps <= 32,
+ * 0 <= eps <= 1e30, |coefficients| <= 1e6.
+ */
+nvfp4_status nvfp4_orthogonalize(const void* G, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                 int64_t g_stride, int steps, const float* coefficients, double eps, void* out_bf16,
+                                 int64_t ldo, int64_t out_stride, void* workspace, int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,7 +10,7 @@ from .binding import (AMAX_GIVEN, BLOCK2D, COLWISE, GATHER, OUT_BF16, OUT_F32, R
                       DEVSTAT_BOUNDS, DEVSTAT_INDEX, DEVSTAT_NONFINITE, DEVSTAT_TIMEOUT,
                       ExpertPlan, NVFP4Error, QuantizedTensor, bounds_checked, combine,
                       combine_backward, expert_plan, experts_dgrad, experts_fprop, experts_wgrad,
-                      gemm, gemm_grouped, gemm_grouped_k, linear_dgrad, linear_fprop, linear_wgrad,
+                      gemm, gemm_grouped, gemm_grouped_k, linear_dgrad, linear_fprop, linear_wgrad, orthogonalize,
                       qk_norm_rope, qk_norm_rope_backward, quantize, quantize_grouped,
                       rht_quantize, rope_table, route, route_backward, sign_mask_from_seed)
 
@@ -19,6 +19,6 @@ __all__ = ["binding", "AMAX_GIVEN", "BLOCK2D", "COLWISE", "GATHER", "OUT_BF16", 
            "DEVSTAT_TIMEOUT", "ExpertPlan", "NVFP4Error", "QuantizedTensor", "bounds_checked",
            "combine", "combine_backward", "expert_plan", "experts_dgrad", "experts_fprop",
            "experts_wgrad", "gemm", "gemm_grouped", "gemm_grouped_k", "linear_dgrad",
-           "linear_fprop", "linear_wgrad", "qk_norm_rope", "qk_norm_rope_backward", "quantize",
-           "quantize_grouped", "rht_quantize", "rope_table", "route", "route_backward",
+           "linear_fprop", "linear_wgrad", "orthogonalize", "qk_norm_rope",
+           "qk_norm_rope_backward", "quantize", "quantize_grouped", "rht_quantize", "rope_table", "route", "route_backward",
            "sign_mask_from_seed"]

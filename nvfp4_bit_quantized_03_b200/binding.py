@@ -200,12 +200,16 @@ def _open(path):
     L.nvfp4_experts_workspace_bytes.restype = sz
     L.nvfp4_qk_norm_rope_workspace_bytes.argtypes = [i64, i64, i64, i64]
     L.nvfp4_qk_norm_rope_workspace_bytes.restype = sz
+    L.nvfp4_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
+    L.nvfp4_orthogonalize_workspace_bytes.restype = sz
     hd = ctypes.POINTER(HeadsStruct)
     for name, argtypes in {
             "qk_norm_rope": [hd, hd, i32, i64, i64, vp, vp, f32, vp, vp, i64, i64, i32, hd, hd, i32, vp,
                              vp],
             "qk_norm_rope_backward": [hd, hd, i32, hd, hd, i32, i64, i64, vp, vp, f32, vp, vp, i64, i64,
                                       i32, hd, hd, i32, vp, vp, vp, vp, vp],
+            "orthogonalize": [vp, i32, i64, i64, i64, i64, i64, i32, vp, ctypes.c_double, vp, i64, i64, vp, vp,
+                              vp],
             "route": [vp, i32, i64, i64, i64, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp],
             "route_backward": [vp, i32, i64, i64, i64, vp, vp, i32, i32, i32, f32, vp, i64, vp, vp],
             "plan_experts": [vp, pl, vp, vp, vp],
@@ -986,3 +990,49 @@ def qk_norm_rope_backward(dq, dk, q, k, positions=None, table=None, q_weight=Non
         _address(dk_weight), _address(workspace), _status_word(dev_status), queue),
         "nvfp4_qk_norm_rope_backward")
     return dq_in, dk_in, dq_weight, dk_weight
+
+
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _coefficient_array(coefficients, steps):
+    """(a, b, c), or a triple for each step, as the C array of `steps` triples."""
+    rows = [coefficients] * steps if not hasattr(coefficients[0], "__len__") else list(coefficients)
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError(f"coefficients must be (a, b, c) or {steps} such triples")
+    return (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
+
+
+def orthogonalize(g, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None, workspace=None,
+                  dev_status=None, stream=None):
+    """nvfp4_orthogonalize: the Newton-Schulz update (bf16) of a weight gradient [rows, cols], or of each
+    matrix of a batch [batch, rows, cols].  coefficients: (a, b, c), or a triple for each step."""
+    if g.dtype not in _F32_BF16:
+        raise TypeError(f"g must be float32 or bfloat16, got {g.dtype}")
+    if g.dim() not in (2, 3) or (g.shape[-1] > 1 and g.stride(-1) != 1):
+        raise ValueError(f"g must be [rows, cols] or [batch, rows, cols] with unit column stride, got "
+                         f"{tuple(g.shape)} strides {g.stride()}")
+    if steps < 1:
+        raise ValueError(f"steps must be at least 1, got {steps}")
+    table = _coefficient_array(coefficients, steps)
+    batch, rows, cols = g.shape if g.dim() == 3 else (1, *g.shape)
+    with _allocating(stream):
+        if out is None:
+            out = _poisoned(torch.empty(g.shape, dtype=torch.bfloat16, device=g.device))
+        need = lib().nvfp4_orthogonalize_workspace_bytes(batch, rows, cols)
+        if need == 0:
+            raise NVFP4Error(ERR_SHAPE, f"nvfp4_orthogonalize of {batch} matrices {rows} x {cols}")
+        if workspace is None:
+            workspace = _workspace(need, g.device)
+    _workspace_size(workspace, need)
+    if out.dtype != torch.bfloat16:
+        raise TypeError(f"out must be bfloat16, got {out.dtype}")
+    if out.shape != g.shape or (cols > 1 and out.stride(-1) != 1):
+        raise ValueError(f"out must be {tuple(g.shape)} with unit column stride, got {tuple(out.shape)} strides "
+                         f"{out.stride()}")
+    queue = _queue("nvfp4_orthogonalize", stream, g, out, workspace, dev_status)
+    _check(lib().nvfp4_orthogonalize(
+        _address(g), _dtype_code(g.dtype), batch, rows, cols, g.stride(-2), g.stride(0) if g.dim() == 3 else 0,
+        steps, table, eps, _address(out), out.stride(-2), out.stride(0) if g.dim() == 3 else 0,
+        _address(workspace), _status_word(dev_status), queue), "nvfp4_orthogonalize")
+    return out

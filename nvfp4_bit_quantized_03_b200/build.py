@@ -30,6 +30,7 @@ UNITS = {
     "combine.cu": [],
     "experts.cu": [],
     "qk_norm.cu": [],
+    "orthogonalize.cu": [],
     "layer.cu": [],
     "noalloc.cu": [],
 }

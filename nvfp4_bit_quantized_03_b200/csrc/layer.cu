@@ -1,5 +1,5 @@
 // C entry points of the operators around a layer's products (include/nvfp4.h): argument checks,
-// workspace carving and dispatch to qk_norm.cu.  As everywhere in the library: no allocation, no
+// workspace sizes and dispatch to qk_norm.cu and orthogonalize.cu.  As everywhere in the library: no allocation, no
 // synchronization, and nothing queued when an argument is invalid.
 #include <cuda_runtime.h>
 
@@ -106,6 +106,17 @@ nvfp4_status head_args(HeadsArgs& a, const HeadsPair* in, HeadsView* const* view
     return NVFP4_OK;
 }
 
+constexpr int64_t kMaxSide = 1 << 18;     // FP16 copies times ~ sqrt(side) stay far inside their range
+constexpr int64_t kMaxBatch = 65535;
+constexpr int64_t kMaxValues = int64_t(1) << 36;
+constexpr int kMaxSteps = 32;
+
+bool matrices_ok(int64_t batch, int64_t rows, int64_t cols)
+{
+    return batch >= 1 && batch <= kMaxBatch && rows >= 1 && rows <= kMaxSide && cols >= 1 && cols <= kMaxSide &&
+           batch * rows * cols <= kMaxValues;
+}
+
 }  // namespace
 
 extern "C" {
@@ -160,6 +171,53 @@ nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads* dq, const nvfp4_head
     return from_cuda(launch_qk_norm_rope_backward(a, in_dtype == NVFP4_OUT_F32, grad_dtype == NVFP4_OUT_F32,
                                                   dx_dtype == NVFP4_OUT_F32, interleaved != 0,
                                                   static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols)
+{
+    return matrices_ok(batch, rows, cols) ? orthogonalize_workspace(batch, rows, cols) : 0;
+}
+
+nvfp4_status nvfp4_orthogonalize(const void* G, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                 int64_t g_stride, int steps, const float* coefficients, double eps, void* out_bf16,
+                                 int64_t ldo, int64_t out_stride, void* workspace, int* dev_status, void* stream)
+{
+    if (!G || !coefficients || !out_bf16 || !workspace) return NVFP4_ERR_NULL;
+    if (!known_type(g_dtype)) return NVFP4_ERR_ARG;
+    if (!matrices_ok(batch, rows, cols)) return NVFP4_ERR_SHAPE;
+    if (steps < 1 || steps > kMaxSteps || !(eps >= 0.0) || !(eps <= 1e30)) return NVFP4_ERR_ARG;
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!(std::fabs(coefficients[i]) <= 1e6f)) return NVFP4_ERR_ARG;
+    // a single row's or matrix's stride is never used
+    if (rows == 1) ldg = cols, ldo = (cols + 7) / 8 * 8;
+    if (batch == 1) g_stride = rows * ldg, out_stride = (rows * ldo + 7) / 8 * 8;
+    if (ldg < 0 || ldg > kMaxStride || g_stride < 0 || g_stride > kMaxStride) return NVFP4_ERR_SHAPE;
+    if (ldo < cols || ldo > kMaxStride || out_stride < (rows - 1) * ldo + cols || out_stride > kMaxStride)
+        return NVFP4_ERR_SHAPE;
+    const uintptr_t mask = g_dtype == NVFP4_OUT_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(G) & mask) || (reinterpret_cast<uintptr_t>(out_bf16) & 1u) ||
+        !aligned16(workspace))
+        return NVFP4_ERR_ALIGN;
+    int sms = 0;
+    const nvfp4_status st = current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    OrthogonalizeArgs a = {};
+    a.g = G;
+    a.f32 = g_dtype == NVFP4_OUT_F32;
+    a.batch = batch;
+    a.rows = rows;
+    a.cols = cols;
+    a.ldg = ldg;
+    a.g_stride = g_stride;
+    a.steps = steps;
+    a.coefficients = coefficients;
+    a.eps = eps;
+    a.out = out_bf16;
+    a.ldo = ldo;
+    a.out_stride = out_stride;
+    a.workspace = workspace;
+    a.dev_status = dev_status;
+    return from_cuda(launch_orthogonalize(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -244,6 +244,22 @@ int qk_backward_ctas(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t D
 cudaError_t launch_qk_norm_rope_backward(HeadsArgs a, bool x_f32, bool z_f32, bool dx_f32, bool interleaved,
                                          cudaStream_t s);
 
+// Newton-Schulz orthogonalisation (orthogonalize.cu).
+struct OrthogonalizeArgs {
+    const void* g;            // batch matrices rows x cols
+    bool f32;                 // FP32, otherwise bf16
+    int64_t batch, rows, cols, ldg, g_stride;
+    int steps;
+    const float* coefficients;  // host: steps x (a, b, c)
+    double eps;
+    void* out;                // bf16, as g
+    int64_t ldo, out_stride;
+    void* workspace;
+    int* dev_status;
+};
+size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);
+cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaStream_t s);
+
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, int sm_count, cudaStream_t s);
 // A kernel whose only thread waits, with the GEMM's bounded-wait routine, on an mbarrier that
 // nothing completes; it records NVFP4_DEVSTAT_TIMEOUT after limit_ns and returns.

@@ -70,3 +70,42 @@ def qk_backward(d, x, w, eps, positions, table, interleaved):
     first = r * size * w.abs()
     second = r * n.abs() * (size * w.abs() * n.abs()).mean(-1, keepdim=True)
     return dx, (dy * n).sum((0, 1)), (first, second, (size * n.abs()).sum((0, 1)))
+
+
+MUON = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(g, steps=5, coefficients=MUON, eps=1e-7):
+    """X after the steps, FP64, from the side with fewer rows."""
+    x = g.double()
+    turned = x.shape[-2] > x.shape[-1]
+    x = x.mT if turned else x
+    x = x / (x.square().sum((-2, -1), keepdim=True).sqrt() + eps)
+    for i in range(steps):
+        a, b, c = coefficients[i] if hasattr(coefficients[0], "__len__") else coefficients
+        gram = x @ x.mT
+        x = a * x + (b * gram + c * gram @ gram) @ x
+    return x.mT if turned else x
+
+
+def orthogonalize_rounded(g, steps=5, coefficients=MUON, eps=1e-7, seed=0):
+    """The same with every operand of a product (values that the kernels round to FP16, 11 significant bits)
+    moved up or down, at random, by the most that rounding can: half a step, 2^-11 relative."""
+    gen = torch.Generator(device=g.device).manual_seed(seed)
+
+    def off(t):
+        up = torch.rand(t.shape, generator=gen, device=t.device) < 0.5
+        return t * torch.where(up, 1 + 2.0 ** -11, 1 - 2.0 ** -11).to(t.dtype)
+
+    def off_symmetric(t):
+        low = off(t).tril()
+        return low + low.tril(-1).mT
+    x = g.double()
+    x = x.mT if x.shape[-2] > x.shape[-1] else x
+    x = x / (x.square().sum((-2, -1), keepdim=True).sqrt() + eps)
+    for i in range(steps):
+        a, b, c = coefficients[i] if hasattr(coefficients[0], "__len__") else coefficients
+        copy = off(x)
+        gram = off_symmetric(copy @ copy.mT)
+        x = a * x + off_symmetric(b * gram + c * gram @ gram) @ copy
+    return x.mT if g.shape[-2] > g.shape[-1] else x

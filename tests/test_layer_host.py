@@ -165,3 +165,90 @@ def test_binding_refusals(monkeypatch):
         for call in (B.qk_norm_rope, lambda q, k, **kw: B.qk_norm_rope_backward(q, k, q, k, **kw)):
             with pytest.raises(TypeError, match="dev_status"):
                 call(q, k, dev_status=torch.zeros(1))
+
+
+# ---- orthogonalisation ---------------------------------------------------------------------
+
+def test_orthogonalize_reference():
+    """Singular vectors stay, singular values go through the polynomial of every step."""
+    torch.manual_seed(0)
+    for shape in ((5, 9), (9, 5), (6, 6)):
+        g = torch.randn(shape).double()
+        u, s, vt = torch.linalg.svd(g, full_matrices=False)
+        s = s / (s.square().sum().sqrt() + 1e-7)
+        for a, b, c in [R.MUON] * 5:
+            s = a * s + b * s ** 3 + c * s ** 5
+        assert torch.allclose(R.orthogonalize(g), (u * s) @ vt, atol=1e-12)
+    g = torch.randn(50, 80).double()
+    off = R.orthogonalize_rounded(g) - R.orthogonalize(g)
+    assert 1e-4 < off.norm() / R.orthogonalize(g).norm() < 1e-2
+
+
+def test_orthogonalize_workspace_sizes():
+    f = B.lib().nvfp4_orthogonalize_workspace_bytes
+    for batch, rows, cols in ((1, 1, 1), (3, 1000, 333), (32, 1408, 2048), (1, 20480, 5120), (65535, 16, 16)):
+        m, n = sorted((rows, cols))
+        pad = -(-m // 128) * -(-n // 128) * 128 * 128
+        need = batch * (4 * pad + 2 * 2 * m * n + 2 * 2 * m * m)
+        assert need <= f(batch, rows, cols) <= need + batch * (2 * 2 * 63 * m + 2 * 2 * 63 * m + 8 * 592) + 6 * 256
+    for bad in ((0, 4, 4), (65536, 4, 4), (1, 0, 4), (1, 4, 0), (1, (1 << 18) + 1, 4), (1, 4, (1 << 18) + 1),
+                (2, 1 << 18, 1 << 18), (-1, 4, 4)):
+        assert f(*bad) == 0
+
+
+def _orthogonalize(over):
+    a = dict(G=0x10000, dtype=0, batch=2, rows=30, cols=50, ldg=50, gs=1500, steps=5, coef=R.MUON * 5, eps=1e-7,
+             out=0x20000, ldo=50, os=1500, ws=P)
+    a.update(over)
+    coef = None if a["coef"] is None else (ctypes.c_float * len(a["coef"]))(*a["coef"])
+    return B.lib().nvfp4_orthogonalize(
+        a["G"], a["dtype"], a["batch"], a["rows"], a["cols"], a["ldg"], a["gs"], a["steps"], coef, a["eps"],
+        a["out"], a["ldo"], a["os"], a["ws"], None, None)
+
+
+@pytest.mark.parametrize("over,expected", [
+    (dict(G=None), B.ERR_NULL), (dict(out=None), B.ERR_NULL), (dict(coef=None), B.ERR_NULL),
+    (dict(ws=None), B.ERR_NULL), (dict(dtype=2), B.ERR_ARG), (dict(steps=0), B.ERR_ARG),
+    (dict(steps=33, coef=R.MUON * 33), B.ERR_ARG), (dict(eps=-1.0), B.ERR_ARG),
+    (dict(eps=float("nan")), B.ERR_ARG), (dict(eps=float("inf")), B.ERR_ARG),
+    (dict(coef=R.MUON * 4 + (1.0, float("nan"), 1.0)), B.ERR_ARG),
+    (dict(coef=(float("inf"), 0.0, 0.0) + R.MUON * 4), B.ERR_ARG),
+    (dict(batch=0), B.ERR_SHAPE), (dict(rows=0), B.ERR_SHAPE), (dict(cols=0), B.ERR_SHAPE),
+    (dict(rows=(1 << 18) + 1, os=1 << 30), B.ERR_SHAPE), (dict(ldg=-1), B.ERR_SHAPE),
+    (dict(gs=-1), B.ERR_SHAPE), (dict(ldo=49), B.ERR_SHAPE), (dict(os=1499), B.ERR_SHAPE),
+    (dict(os=0), B.ERR_SHAPE), (dict(G=0x10002), B.ERR_ALIGN), (dict(G=0x10001, dtype=1), B.ERR_ALIGN),
+    (dict(out=0x20001), B.ERR_ALIGN), (dict(ws=BAD), B.ERR_ALIGN)])
+def test_orthogonalize_refusals(over, expected):
+    assert _orthogonalize(over) == expected
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="no work may be queued with these addresses")
+@pytest.mark.parametrize("over", [dict(), dict(ldg=0, gs=0), dict(ldg=7), dict(batch=1, gs=-5, os=-5),
+                                  dict(batch=1, rows=1, ldg=-3, ldo=-3, gs=0, os=0), dict(eps=0.0),
+                                  dict(G=0x10002, dtype=1, out=0x20002)])
+def test_orthogonalize_calls_that_are_accepted(over):
+    assert _orthogonalize(over) in (B.ERR_DEVICE, B.ERR_CUDA)
+
+
+def test_orthogonalize_binding_refusals(monkeypatch):
+    g = torch.zeros(2, 30, 50)
+    out = torch.zeros(2, 30, 50, dtype=torch.bfloat16)
+    for error, match, args in (
+            (ValueError, "current CUDA device", dict()), (TypeError, "g must be", dict(g=g.double())),
+            (ValueError, "g must be", dict(g=g[0, 0])), (ValueError, "g must be", dict(g=g[None])),
+            (ValueError, "unit column stride", dict(g=g[..., ::2])), (ValueError, "steps", dict(steps=0)),
+            (ValueError, "coefficients", dict(coefficients=(1.0, 2.0))),
+            (ValueError, "coefficients", dict(coefficients=[R.MUON] * 4)),
+            (ValueError, "coefficients", dict(coefficients=[(1.0, 2.0)] * 5)),
+            (TypeError, "out must be", dict(out=out.float())), (ValueError, "out must be", dict(out=out[:1])),
+            (ValueError, "unit column stride", dict(out=torch.zeros(2, 50, 30, dtype=torch.bfloat16).mT)),
+            (B.NVFP4Error, "orthogonalize of", dict(g=g[:, :0])),
+            (ValueError, "workspace has", dict(workspace=torch.zeros(8, dtype=torch.uint8))),
+            (ValueError, "contiguous", dict(workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24)))):
+        args = dict(args)
+        with pytest.raises(error, match=match):
+            B.orthogonalize(args.pop("g", g), **args)
+    if not torch.cuda.is_available():
+        monkeypatch.setattr(B, "_queue", lambda *a: None)
+        with pytest.raises(TypeError, match="dev_status"):
+            B.orthogonalize(g, dev_status=torch.zeros(1))
