@@ -37,6 +37,7 @@ using gemm::mbar_arrive_cluster;
 using gemm::mbar_expect_tx;
 using gemm::mbar_init;
 using gemm::mma_commit_pair;
+using gemm::named_sync;
 using gemm::smem_u32;
 using gemm::tc_fence_after;
 using gemm::tc_fence_before;
@@ -58,7 +59,9 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;                   // two per lane quarter, half of the columns each
 constexpr int kFirstEpi = 2;
-constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+constexpr int kGateWarp = kFirstEpi + kEpiWarps;
+constexpr int kThreads = 32 * (kGateWarp + 1);
+constexpr int kGateBar = 1;                    // named barriers 1 .. 6: issuer and gate, one per stage
 constexpr int kStaging = 4096;                 // per epilogue warp: 32 rows of 64 FP16
 constexpr int kBarBytes = 256;
 constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kStaging + kBarBytes + 1024;
@@ -323,18 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            const uint32_t s0 = smem_u32(smem);
-            int stage = 0, it = 0;
-            uint32_t phase = 0;
-            bool ok = true, any = false;
-            for (int64_t t = worker; t < total && ok; t += workers, ++it) {
-                const int buf = it & 1;
-                ok = wait_bounded(bar(kBarAccEmpty + buf), ((it >> 1) & 1) ^ 1, abort_flag, p.dev_status);
-                const uint32_t acc = tmem + buf * ACC_COLS;
-                for (int d = 0; d < depth && ok; ++d) {
-                    ok = wait_bounded(bar(kBarFull + stage), phase, abort_flag, p.dev_status);
-                    if (!ok) break;
+        // It polls no barrier: the gate has seen the stage's bytes land (and, at a tile's first stage, the
+        // accumulator drained) when both meet at the stage's named barrier.  After an abort the gate keeps
+        // meeting the issuer, which runs its schedule on stale operands (in bounds, results discarded).
+        const uint32_t s0 = smem_u32(smem);
+        int stage = 0, it = 0;
+        for (int64_t t = worker; t < total; t += workers, ++it) {
+            const uint32_t acc = tmem + (it & 1) * ACC_COLS;
+            for (int d = 0; d < depth; ++d) {
+                named_sync(kGateBar + stage, 64);
+                if (lane == 0) {
                     tc_fence_after();
                     const uint64_t da = desc_sw128(s0 + stage * kStageBytes);
                     const uint64_t db = ACROSS ? desc_across(s0 + stage * kStageBytes + kOperandBytes)
@@ -343,21 +344,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < kDepth / 16; ++k)  // 32 bytes of a row, or 16 rows, further on
                         mma_f16<CG>(acc, da + 2 * k, db + (ACROSS ? 128 : 2) * k, IDESC, (d | k) != 0 ? 1u : 0u);
                     mma_commit<CG>(bar(kBarEmpty + stage));
-                    any = true;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    if (d + 1 == depth) mma_commit<CG>(bar(kBarAccFull + (it & 1)));
                 }
-                if (ok) mma_commit<CG>(bar(kBarAccFull + buf));
-            }
-            // every MMA completes before the tensor memory can be freed
-            if (any) {
-                mma_commit<CG>(bar(kBarDrain));
-                wait_bounded(bar(kBarDrain), 0, abort_flag, nullptr, true);
+                __syncwarp();
+                if (++stage == kStages) stage = 0;
             }
         }
-    } else if (warp >= kFirstEpi) {
+        // every MMA completes before the tensor memory can be freed
+        if (lane == 0 && it > 0) {
+            mma_commit<CG>(bar(kBarDrain));
+            wait_bounded(bar(kBarDrain), 0, abort_flag, nullptr, true);
+        }
+    } else if (warp == kGateWarp && rank == 0) {
+        // ---------------- the issuer's gate ----------------
+        int stage = 0, it = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t t = worker; t < total; t += workers, ++it) {
+            for (int d = 0; d < depth; ++d) {
+                if (lane == 0 && ok) {
+                    if (d == 0)
+                        ok = wait_bounded(bar(kBarAccEmpty + (it & 1)), ((it >> 1) & 1) ^ 1, abort_flag,
+                                          p.dev_status);
+                    if (ok) ok = wait_bounded(bar(kBarFull + stage), phase, abort_flag, p.dev_status);
+                }
+                __syncwarp();
+                named_sync(kGateBar + stage, 64);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp >= kFirstEpi && warp < kFirstEpi + kEpiWarps) {
         // ---------------- epilogue ----------------
         constexpr int SLICE = 64 * CG;  // columns of a warp
         const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
