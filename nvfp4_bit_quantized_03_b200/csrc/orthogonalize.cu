@@ -5,15 +5,17 @@
 // vectors.
 //
 // Precision.  Every product takes FP16 operands (11 significant bits) with FP32 accumulation; X itself stays
-// in FP32 between steps, and only its copy for the products is rounded.  A, B and the copy are held times
-// powers of two that keep their values inside FP16's normal range: X times S ~ sqrt(columns), A times
-// 2^12, B times 2^10.  The error of the result is then about that of its own rounding to bf16 (emulated in
+// in 32 bits between steps, as an FP16 value, which is the products' operand, and the rest to it in FP16 times
+// 2^11: 22 bits and more.  A, B and X are held times powers of two that keep their values inside FP16's
+// normal range: X times S ~ sqrt(columns), A times 2^12, B times 2^10.  The error of the result is then about that of its own rounding to bf16 (emulated in
 // FP64, rms of error over rms of result: 1.2e-3 .. 1.9e-3 against 1.7e-3 for the rounding).  With X
 // itself in FP16 a gradient of low rank is lost (1.5e-1: rounding noise of the directions that are not there
 // is raised like everything else), with bf16 operands the error is 1e-2 and more.
 //
 // Kernels: the sum of squares (FP64), the scaled copies of X, then three products per step, one
-// kernel each, chained by programmatic launches.
+// kernel each, chained by programmatic launches.  (One kernel that stays on the SMs for all steps, its products
+// behind a counter in memory: 512 x 512 145 against 114 us, 4096 x 4096 1.27 against 1.16 ms.  What a launch costs
+// less than the counter is the time of the fences around it.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -48,44 +50,48 @@ using gemm::wait_bounded;
 constexpr float kScaleA = 4096.0f;  // A is held times this,
 constexpr float kScaleB = 1024.0f;  // B times this
 
-// ---- the product kernels -----------------------------------------------------------------
+// ---- the steps ---------------------------------------------------------------------------
 
 enum Product { kGram = 0, kSquare = 1, kUpdate = 2, kLast = 3 };
 
-constexpr int kBlock = 128;                    // rows a CTA loads of either operand; its tensor-memory lanes
+constexpr int kBlock = 128;                    // rows of a CTA's left operand; its tensor-memory lanes
 constexpr int kDepth = 64;                     // K per pipeline stage (128 bytes of FP16)
-constexpr int kOperandBytes = kBlock * 128;    // 16 KB
-constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 6;
+constexpr int kLeftBytes = kBlock * 128;       // 16 KB
+constexpr int kBoxBytes = 64 * 128;            // a box of the right operand
 constexpr int kEpiWarps = 8;                   // two per lane quarter, half of the columns each
 constexpr int kFirstEpi = 2;
 constexpr int kGateWarp = kFirstEpi + kEpiWarps;
 constexpr int kThreads = 32 * (kGateWarp + 1);
-constexpr int kGateBar = 1;                    // named barriers 1 .. 6: issuer and gate, one per stage
-constexpr int kStaging = 4096;                 // per epilogue warp: 32 rows of 64 FP16
+constexpr int kGateBar = 1;                    // named barriers from 1: issuer and gate, one per stage
+constexpr int kStaging = 4096;                 // per epilogue warp: 32 rows of 64 values of 2 bytes
 constexpr int kBarBytes = 256;
-constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kStaging + kBarBytes + 1024;
-constexpr int kStateBlock = kBlock * kBlock;   // FP32 values of X per block of the state
-static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr int kRestBlock = kBlock * kBlock;    // values per block of X's rest
+constexpr float kRestUnit = 1.0f / 2048.0f;
 
+// A CTA takes tiles of 128 x 128, a pair of CTAs (CG 2) of 256 x 256; the right operand's rows are split
+// between them as the left one's are.
+constexpr int kStageBytes = 2 * kLeftBytes;
+constexpr int kStages = 6;
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kStaging + kBarBytes + 1024;
+static_assert(kSmem <= 232448, "shared memory per CTA");
 // barriers (the same offsets in both CTAs of a pair)
-constexpr int kBarFull = 0;                       // [stages] leader: the stage's bytes of both CTAs landed
-constexpr int kBarEmpty = kBarFull + kStages;     // [stages] the stage's MMAs completed
-constexpr int kBarAccFull = kBarEmpty + kStages;  // [2] the accumulator is complete
-constexpr int kBarAccEmpty = kBarAccFull + 2;     // [2] leader: the epilogues have drained it
-constexpr int kBarDrain = kBarAccEmpty + 2;
-constexpr int kBars = kBarDrain + 1;
+constexpr int kFull = 0;                   // [stages] leader: the stage's bytes of both CTAs landed
+constexpr int kEmpty = kFull + kStages;    // [stages] the stage's MMAs completed
+constexpr int kAccFull = kEmpty + kStages; // [2] the accumulator is complete
+constexpr int kAccEmpty = kAccFull + 2;    // [2] leader: the epilogues have drained it
+constexpr int kDrain = kAccEmpty + 2;
+constexpr int kBars = kDrain + 1;
 static_assert(kBars * 8 + 16 <= kBarBytes, "barrier area");
 
 struct ProductArgs {
     int m, n, k;           // rows and columns of the result, length of the products
     int batch;
     float alpha, beta;     // result = alpha * (A or X) + beta * accumulator
-    const __half* addend;  // square: A [batch][m][pitch]
+    const __half* addend;  // square: A; update: X [batch][m][pitch]
     int64_t pitch;
-    float* state;          // update: X in FP32, blocks of 128 x 128 in the order of the epilogue's lanes
-    int state_rows, state_cols;  // blocks of a matrix
-    uint16_t* out;         // last: the result, bf16
+    __half* rest;          // update: X's rest, blocks of 128 x 128 in the order of the epilogue's lanes
+    int rest_rows, rest_cols;  // blocks of a matrix
+    uint16_t* out;         // where the results go: last: bf16; small products: also A, B or X
     int64_t ldo, out_stride;
     int transposed;        // last: out is X^T
     int by_tma;            // last: out's addresses suit tensor stores
@@ -178,49 +184,70 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 }
 
 struct Tile {
-    int e, i, j;  // matrix, row and column of tiles
+    int e, row, col;  // matrix, first row and column
 };
 // The symmetric products (gram, square) have tiles on and below the diagonal only, row by row; the others go
-// down the columns, so that the left operand (m x m) stays in L2 and X is read once.
-template <int OP>
-__device__ __forceinline__ Tile tile_at(int64_t t, int rows, int cols)
+// down the columns, so that the left operand (m x m) stays in L2 and X is read once.  (Tiles of 256 x 128 by
+// pairs: 3.25 against 2.82 ms for 32 of 1408 x 2048, 9.4 against 6.8 for 20480 x 5120; their stages want
+// 96 bytes per cycle and SM of L2 where 256 x 256 want 64.)
+template <int SIDE>
+__host__ __device__ __forceinline__ int64_t tiles_of(bool symmetric, int64_t m, int64_t n)
+{
+    const int64_t rows = (m + SIDE - 1) / SIDE;
+    return symmetric ? rows * (rows + 1) / 2 : rows * ((n + SIDE - 1) / SIDE);
+}
+template <int SIDE, bool SYMMETRIC>
+__device__ __forceinline__ Tile tile_at(int64_t t, int per, int m)
 {
     Tile r;
-    if (OP == kGram || OP == kSquare) {
-        const int per = rows * (rows + 1) / 2;
-        r.e = static_cast<int>(t / per);
-        const int l = static_cast<int>(t - static_cast<int64_t>(r.e) * per);
-        int i = static_cast<int>((sqrtf(8.0f * l + 1.0f) - 1.0f) * 0.5f);
-        while (i * (i + 1) / 2 > l) --i;
-        while ((i + 1) * (i + 2) / 2 <= l) ++i;
-        r.i = i;
-        r.j = l - i * (i + 1) / 2;
+    r.e = static_cast<int>(t / per);
+    const int l = static_cast<int>(t - static_cast<int64_t>(r.e) * per);
+    if (SYMMETRIC) {
+        int k = static_cast<int>((sqrtf(8.0f * l + 1.0f) - 1.0f) * 0.5f);
+        while (k * (k + 1) / 2 > l) --k;
+        while ((k + 1) * (k + 2) / 2 <= l) ++k;
+        r.row = k * SIDE;
+        r.col = (l - k * (k + 1) / 2) * SIDE;
     } else {
-        const int per = rows * cols;
-        r.e = static_cast<int>(t / per);
-        const int l = static_cast<int>(t - static_cast<int64_t>(r.e) * per);
-        r.i = l % rows;
-        r.j = l / rows;
+        const int rows = (m + SIDE - 1) / SIDE;
+        r.row = l % rows * SIDE;
+        r.col = l / rows * SIDE;
     }
     return r;
 }
 
-// One tile of 128 CG x 128 CG per CTA (CG 1) or pair of CTAs (CG 2: cta_group::2, each CTA holds half of
-// either operand's rows and the accumulator of its 128 rows).  Warp 0 loads, warp 1 issues the MMAs, warps
-// 2..9 turn accumulators into results; two accumulators, so that a tile's results are written while the next
-// one is multiplied.
+// 16 values of 2 bytes, 32-byte aligned: one load of a whole sector.
+__device__ __forceinline__ void load16(const __half* src, const void* base, int64_t bytes, int* status, uint32_t* v)
+{
+    if (kBoundsCheck && !(in_buffer(reinterpret_cast<const uint4*>(src), base, bytes, status) &&
+                          in_buffer(reinterpret_cast<const uint4*>(src) + 1, base, bytes, status))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0;
+        return;
+    }
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(src));
+}
+__device__ __forceinline__ float2 halves(uint32_t v)
+{
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// Warp 0 loads, warp 1 issues the MMAs behind the gate warp, warps 2..9 turn accumulators into results; two
+// accumulators, so that a tile's results are written while the next one is multiplied.  In a pair
+// (cta_group::2) each CTA holds half of either operand's rows and the accumulator of its 128 rows.
 template <int CG, int OP>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_t,
                    const ProductArgs p)
 {
-    constexpr int TILE = kBlock * CG;
-    constexpr int ACC_COLS = TILE;           // tensor-memory columns of an accumulator
+    constexpr int SIDE = kBlock * CG, SLICE = SIDE / 2;  // of a tile; columns of an epilogue warp
     constexpr bool SYMMETRIC = OP == kGram || OP == kSquare;
     constexpr bool ACROSS = OP == kUpdate || OP == kLast;  // the right operand's rows run along K
-    constexpr uint32_t IDESC = (1u << 4) | (ACROSS ? 1u << 16 : 0u) | (static_cast<uint32_t>(TILE >> 3) << 17) |
-                               (static_cast<uint32_t>(TILE >> 4) << 24);
+    constexpr uint32_t IDESC = (1u << 4) | (ACROSS ? 1u << 16 : 0u) | (static_cast<uint32_t>(SIDE >> 3) << 17) |
+                               (static_cast<uint32_t>(SIDE >> 4) << 24);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -233,20 +260,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
     const int64_t worker = blockIdx.x / CG, workers = gridDim.x / CG;
-    const int rows = (p.m + TILE - 1) / TILE, cols = (p.n + TILE - 1) / TILE;
-    const int64_t total = static_cast<int64_t>(p.batch) * (SYMMETRIC ? rows * (rows + 1) / 2 : rows * cols);
+    const int per = static_cast<int>(tiles_of<SIDE>(SYMMETRIC, p.m, p.n));
+    const int64_t total = static_cast<int64_t>(p.batch) * per;
     const int depth = (p.k + kDepth - 1) / kDepth;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(bar(kBarFull + s), 1);
-            mbar_init(bar(kBarEmpty + s), 1);
+            mbar_init(bar(kFull + s), 1);
+            mbar_init(bar(kEmpty + s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(bar(kBarAccFull + b), 1);
-            mbar_init(bar(kBarAccEmpty + b), CG * kEpiWarps);
+            mbar_init(bar(kAccFull + b), 1);
+            mbar_init(bar(kAccEmpty + b), CG * kEpiWarps);
         }
-        mbar_init(bar(kBarDrain), 1);
+        mbar_init(bar(kDrain), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
@@ -255,12 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         if (CG == 2) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                         "r"(2 * ACC_COLS)
+                         "r"(2 * SIDE)
                          : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         } else {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                         "r"(2 * ACC_COLS)
+                         "r"(2 * SIDE)
                          : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
@@ -281,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, fills = 0;
         bool ok = true;
         for (int64_t t = worker; t < total && ok; t += workers) {
-            const Tile c = tile_at<OP>(t, rows, cols);
-            const int ya = c.i * TILE + rank * kBlock, yb = c.j * TILE + rank * kBlock;
+            const Tile c = tile_at<SIDE, SYMMETRIC>(t, per, p.m);
+            const int ya = c.row + rank * kBlock, yb = c.col + rank * kBlock;
             for (int d = 0; d < depth; ++d) {
-                if (!wait_bounded(bar(kBarEmpty + stage), phase ^ 1, abort_flag, p.dev_status)) {
+                if (!wait_bounded(bar(kEmpty + stage), phase ^ 1, abort_flag, p.dev_status)) {
                     ok = false;
                     break;
                 }
@@ -295,15 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t full = CG == 2 ? leader_address(bar(kBarFull + stage)) : bar(kBarFull + stage);
+                const uint32_t full = CG == 2 ? leader_address(bar(kFull + stage)) : bar(kFull + stage);
                 const uint32_t at = smem_u32(smem + stage * kStageBytes);
-                if (rank == 0) mbar_expect_tx(bar(kBarFull + stage), CG * kStageBytes);
+                if (rank == 0) mbar_expect_tx(bar(kFull + stage), CG * kStageBytes);
                 load_3d<CG>(at, &map_a, d * kDepth, ya, c.e, full);
                 if (ACROSS) {
-                    load_3d<CG>(at + kOperandBytes, &map_b, yb, d * kDepth, c.e, full);
-                    load_3d<CG>(at + kOperandBytes + kOperandBytes / 2, &map_b, yb + 64, d * kDepth, c.e, full);
+                    load_3d<CG>(at + kLeftBytes, &map_b, yb, d * kDepth, c.e, full);
+                    load_3d<CG>(at + kLeftBytes + kBoxBytes, &map_b, yb + 64, d * kDepth, c.e, full);
                 } else {
-                    load_3d<CG>(at + kOperandBytes, &map_b, d * kDepth, yb, c.e, full);
+                    load_3d<CG>(at + kLeftBytes, &map_b, d * kDepth, yb, c.e, full);
+                    load_3d<CG>(at + kLeftBytes + kBoxBytes, &map_b, d * kDepth, yb + 64, c.e, full);
                 }
                 ++fills;
                 if (++stage == kStages) {
@@ -318,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank == 0) {
                 for (uint32_t s = 0; s < kStages; ++s) {
                     const uint32_t n = fills > s ? (fills - s + kStages - 1) / kStages : 0u;
-                    if (n) wait_bounded(bar(kBarFull + s), (n - 1) & 1, abort_flag, nullptr, true, 100000000ull);
+                    if (n) wait_bounded(bar(kFull + s), (n - 1) & 1, abort_flag, nullptr, true, 100000000ull);
                 }
             }
             const uint64_t t0 = gemm::globaltimer();
@@ -332,19 +360,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s0 = smem_u32(smem);
         int stage = 0, it = 0;
         for (int64_t t = worker; t < total; t += workers, ++it) {
-            const uint32_t acc = tmem + (it & 1) * ACC_COLS;
+            const uint32_t acc = tmem + (it & 1) * SIDE;
             for (int d = 0; d < depth; ++d) {
                 named_sync(kGateBar + stage, 64);
                 if (lane == 0) {
                     tc_fence_after();
                     const uint64_t da = desc_sw128(s0 + stage * kStageBytes);
-                    const uint64_t db = ACROSS ? desc_across(s0 + stage * kStageBytes + kOperandBytes)
-                                               : desc_sw128(s0 + stage * kStageBytes + kOperandBytes);
+                    const uint64_t db = ACROSS ? desc_across(s0 + stage * kStageBytes + kLeftBytes)
+                                               : desc_sw128(s0 + stage * kStageBytes + kLeftBytes);
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k)  // 32 bytes of a row, or 16 rows, further on
                         mma_f16<CG>(acc, da + 2 * k, db + (ACROSS ? 128 : 2) * k, IDESC, (d | k) != 0 ? 1u : 0u);
-                    mma_commit<CG>(bar(kBarEmpty + stage));
-                    if (d + 1 == depth) mma_commit<CG>(bar(kBarAccFull + (it & 1)));
+                    mma_commit<CG>(bar(kEmpty + stage));
+                    if (d + 1 == depth) mma_commit<CG>(bar(kAccFull + (it & 1)));
                 }
                 __syncwarp();
                 if (++stage == kStages) stage = 0;
@@ -352,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA completes before the tensor memory can be freed
         if (lane == 0 && it > 0) {
-            mma_commit<CG>(bar(kBarDrain));
-            wait_bounded(bar(kBarDrain), 0, abort_flag, nullptr, true);
+            mma_commit<CG>(bar(kDrain));
+            wait_bounded(bar(kDrain), 0, abort_flag, nullptr, true);
         }
     } else if (warp == kGateWarp && rank == 0) {
         // ---------------- the issuer's gate ----------------
@@ -364,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int d = 0; d < depth; ++d) {
                 if (lane == 0 && ok) {
                     if (d == 0)
-                        ok = wait_bounded(bar(kBarAccEmpty + (it & 1)), ((it >> 1) & 1) ^ 1, abort_flag,
+                        ok = wait_bounded(bar(kAccEmpty + (it & 1)), ((it >> 1) & 1) ^ 1, abort_flag,
                                           p.dev_status);
-                    if (ok) ok = wait_bounded(bar(kBarFull + stage), phase, abort_flag, p.dev_status);
+                    if (ok) ok = wait_bounded(bar(kFull + stage), phase, abort_flag, p.dev_status);
                 }
                 __syncwarp();
                 named_sync(kGateBar + stage, 64);
@@ -378,98 +406,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kFirstEpi && warp < kFirstEpi + kEpiWarps) {
         // ---------------- epilogue ----------------
-        constexpr int SLICE = 64 * CG;  // columns of a warp
         const int q = warp & 3, half = (warp - kFirstEpi) >> 2;
         const uint32_t stage_buf = smem_u32(staging + (warp - kFirstEpi) * kStaging);
+        const int64_t addend_bytes = 2 * static_cast<int64_t>(p.batch) * p.m * p.pitch;
+        const int64_t rest_bytes = 2LL * kRestBlock * p.batch * p.rest_rows * p.rest_cols;
         int it = 0;
         for (int64_t t = worker; t < total; t += workers, ++it) {
-            const Tile c = tile_at<OP>(t, rows, cols);
+            const Tile c = tile_at<SIDE, SYMMETRIC>(t, per, p.m);
             const int buf = it & 1;
-            const int r0 = c.i * TILE + rank * kBlock + 32 * q;  // the warp's rows (one per lane)
-            const int c0 = c.j * TILE + half * SLICE;            // its columns
-            bool ready = lane == 0 ? wait_bounded(bar(kBarAccFull + buf), (it >> 1) & 1, abort_flag, p.dev_status)
-                                   : false;
+            const int r0 = c.row + rank * kBlock + 32 * q;  // the warp's rows (one per lane)
+            const int row = r0 + lane;
+            const int c0 = c.col + half * SLICE;            // its columns
+            // what the accumulator is added to, 64 columns at a time: A or X of the lane's row, and X's rest
+            uint32_t add[OP == kGram ? 1 : 32], rest[ACROSS ? 32 : 1];
+            __half* rest_at = nullptr;
+            auto fetch = [&](int col) {
+                if (OP != kGram) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        if (row < p.m && col + 16 * g < p.pitch)
+                            load16(p.addend + (static_cast<int64_t>(c.e) * p.m + row) * p.pitch + col + 16 * g, p.addend,
+                                   addend_bytes, p.dev_status, add + 8 * g);
+                        else
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) add[8 * g + i] = 0;
+                    }
+                }
+                if (ACROSS) {
+                    const int br = r0 / kBlock, bc = col / kBlock;
+                    rest_at = nullptr;
+                    if (br < p.rest_rows && bc < p.rest_cols)
+                        rest_at = p.rest + ((static_cast<int64_t>(c.e) * p.rest_rows + br) * p.rest_cols + bc) * kRestBlock +
+                                  ((q * 16 + (col % kBlock) / 8) * 32 + lane) * 8;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (rest_at)
+                            v = ld_checked(reinterpret_cast<const uint4*>(rest_at) + 32 * g, p.rest, rest_bytes, p.dev_status);
+                        rest[4 * g] = v.x; rest[4 * g + 1] = v.y; rest[4 * g + 2] = v.z; rest[4 * g + 3] = v.w;
+                    }
+                }
+            };
+            fetch(c0);  // on its way while the products are summed
+            bool ready = lane == 0 ? wait_bounded(bar(kAccFull + buf), (it >> 1) & 1, abort_flag, p.dev_status) : false;
             ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
             if (!ready) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int w = 0; w < CG; ++w) {  // 64 columns at a time
-                const int col = c0 + 64 * w;
-                uint32_t packed[32];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float f[32];
-                    const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * ACC_COLS +
-                                           half * SLICE + 64 * w + 32 * h;
-                    uint32_t v[32];
-                    tmem_ld32(taddr, v);
-                    if (OP == kGram) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) f[i] = 0.0f;
-                    } else if (OP == kSquare) {
-                        const int row = r0 + lane;
-                        const __half* src = p.addend + (static_cast<int64_t>(c.e) * p.m + row) * p.pitch + col + 32 * h;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (row < p.m && col + 32 * h + 8 * g < p.pitch)
-                                x = ld_checked(reinterpret_cast<const uint4*>(src) + g, p.addend,
-                                               2 * static_cast<int64_t>(p.batch) * p.m * p.pitch, p.dev_status);
-                            const __half2* hx = reinterpret_cast<const __half2*>(&x);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 two = __half22float2(hx[i]);
-                                f[8 * g + 2 * i] = two.x;
-                                f[8 * g + 2 * i + 1] = two.y;
-                            }
-                        }
-                    } else {
-                        const int cc = col + 32 * h;
-                        const int64_t block = (static_cast<int64_t>(c.e) * p.state_rows + r0 / kBlock) * p.state_cols +
-                                              cc / kBlock;
-                        if (r0 / kBlock < p.state_rows && cc / kBlock < p.state_cols) {
-                            float4* src = reinterpret_cast<float4*>(p.state + block * kStateBlock) +
-                                          (q * 32 + (cc % kBlock) / 4) * 32 + lane;
-                            const int64_t bytes = 4LL * kStateBlock * p.batch * p.state_rows * p.state_cols;
-#pragma unroll
-                            for (int g = 0; g < 8; ++g) {
-                                const float4 x = ld_checked(src + 32 * g, p.state, bytes, p.dev_status);
-                                f[4 * g] = x.x; f[4 * g + 1] = x.y; f[4 * g + 2] = x.z; f[4 * g + 3] = x.w;
-                            }
-                        }
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        f[i] = OP == kGram ? p.beta * __uint_as_float(v[i])
-                                           : p.alpha * f[i] + p.beta * __uint_as_float(v[i]);
-                    if (OP == kUpdate) {
-                        const int cc = col + 32 * h;
-                        const int64_t block = (static_cast<int64_t>(c.e) * p.state_rows + r0 / kBlock) * p.state_cols +
-                                              cc / kBlock;
-                        if (r0 / kBlock < p.state_rows && cc / kBlock < p.state_cols) {
-                            float4* dst = reinterpret_cast<float4*>(p.state + block * kStateBlock) +
-                                          (q * 32 + (cc % kBlock) / 4) * 32 + lane;
-                            const int64_t bytes = 4LL * kStateBlock * p.batch * p.state_rows * p.state_cols;
-#pragma unroll
-                            for (int g = 0; g < 8; ++g)
-                                st_checked(dst + 32 * g, make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]),
-                                           p.state, bytes, p.dev_status);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        packed[16 * h + i] = OP == kLast ? pack_bf16(f[2 * i], f[2 * i + 1])
-                                                         : pack_half(f[2 * i], f[2 * i + 1]);
-                }
-                if (w == CG - 1) {  // the last of the warp's slice is in registers
+            // 32 columns of the accumulator
+            auto accumulator = [&](int at, uint32_t* v) {
+                tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + buf * SIDE + half * SLICE + 32 * at, v);
+                tmem_wait_ld();
+                if (at == SLICE / 32 - 1) {  // the last of the warp's slice is in registers
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(bar(kBarAccEmpty + buf));
+                    if (lane == 0) arrive_leader<CG>(bar(kAccEmpty + buf));
                 }
+            };
+#pragma unroll 1
+            for (int w = 0; w < SLICE / 64; ++w) {
+                const int col = c0 + 64 * w;
+                uint32_t packed[32];
+                __half* const rest_out = rest_at;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+                    accumulator(2 * w + h, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int i = 16 * h + j;
+                        float2 f = make_float2(p.beta * __uint_as_float(v[2 * j]), p.beta * __uint_as_float(v[2 * j + 1]));
+                        if (OP != kGram) {
+                            float2 x = halves(add[i]);
+                            if (ACROSS) {
+                                const float2 r = halves(rest[i]);
+                                x.x += r.x * kRestUnit;
+                                x.y += r.y * kRestUnit;
+                            }
+                            f.x += p.alpha * x.x;
+                            f.y += p.alpha * x.y;
+                        }
+                        packed[i] = OP == kLast ? pack_bf16(f.x, f.y) : pack_half(f.x, f.y);
+                        if (OP == kUpdate) {
+                            const float2 o = halves(packed[i]);
+                            rest[i] = pack_half((f.x - o.x) * (1.0f / kRestUnit), (f.y - o.y) * (1.0f / kRestUnit));
+                        }
+                    }
+                }
+                if (OP == kUpdate && rest_out) {
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        st_checked(reinterpret_cast<uint4*>(rest_out) + 32 * g,
+                                   make_uint4(rest[4 * g], rest[4 * g + 1], rest[4 * g + 2], rest[4 * g + 3]), p.rest,
+                                   rest_bytes, p.dev_status);
+                }
+                if (w + 1 < SLICE / 64) fetch(col + 64);
                 const bool inside = r0 < p.m && col < p.n;
                 const bool direct = OP != kLast || !p.transposed;
-                const bool turned = SYMMETRIC ? c.i != c.j : (OP == kLast && p.transposed);
+                // a symmetric result's other half; a tile on the diagonal holds both
+                const bool turned = SYMMETRIC ? c.row != c.col : (OP == kLast && p.transposed);
                 if (direct) {
                     // row `lane`: 128 bytes, its 16-byte chunks permuted by the 128-byte swizzle
                     if (lane == 0) bulk_wait_read();
@@ -548,12 +582,302 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
         if (CG == 2)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * ACC_COLS)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * SIDE)
                          : "memory");
         else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * ACC_COLS)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * SIDE)
                          : "memory");
     }
+}
+
+// ---- the steps' small products ---------------------------------------------------------------
+//
+// Where larger tiles are too few for the SMs, CTAs take one of 128 x 64 each; or a cluster of 2 or 4 takes one: each
+// CTA sums a part of K, copies to every other CTA of the cluster the sums of that one's columns (bulk copies
+// between shared memories), and writes the results of its own.  The order of the additions is that of the parts.
+
+constexpr int kNarrow = 64;                     // columns of a tile
+constexpr int kNarrowStage = kLeftBytes + kBoxBytes;
+constexpr int kNarrowStages = 6;
+constexpr int kExchange = kBlock * kNarrow * 4; // the sums of a CTA's columns from all parts
+constexpr int kNarrowEpi = 8;                   // epilogue warps, two per lane quarter, half of the columns each
+constexpr int kNarrowThreads = 32 * (2 + kNarrowEpi);
+constexpr int kNarrowSmem = kNarrowStages * kNarrowStage + kExchange + kBarBytes + 1024;
+static_assert(kNarrowSmem <= 232448 && (2 * kNarrowStages + 2) * 8 + 16 <= kBarBytes, "shared memory per CTA");
+
+__host__ __device__ __forceinline__ int64_t narrow_tiles(bool symmetric, int64_t m, int64_t n)
+{
+    const int64_t rows = (m + kBlock - 1) / kBlock;
+    // below the diagonal and in its blocks
+    return symmetric ? rows * (rows - 1) + (m - (rows - 1) * kBlock + kNarrow - 1) / kNarrow
+                           + 2 * (rows - 1) : rows * ((n + kNarrow - 1) / kNarrow);
+}
+template <bool SYMMETRIC>
+__device__ __forceinline__ Tile narrow_tile_at(int t, int per, int m)
+{
+    Tile r;
+    r.e = t / per;
+    const int l = t - r.e * per;
+    if (SYMMETRIC) {  // 2 k + 2 tiles in row k of tiles (the last row may lack its last one)
+        int k = static_cast<int>((sqrtf(4.0f * l + 1.0f) - 1.0f) * 0.5f);
+        while (k * (k + 1) > l) --k;
+        while ((k + 1) * (k + 2) <= l) ++k;
+        r.row = k * kBlock;
+        r.col = (l - k * (k + 1)) * kNarrow;
+    } else {
+        const int rows = (m + kBlock - 1) / kBlock;
+        r.row = l % rows * kBlock;
+        r.col = l / rows * kNarrow;
+    }
+    return r;
+}
+
+// `bytes` of this CTA's shared memory to the same place of CTA `cta`, whose barrier counts them.
+__device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar, uint32_t cta)
+{
+    asm volatile(
+        "{\n\t.reg .b32 to, there;\n\t"
+        "mapa.shared::cluster.u32 to, %0, %4;\n\t"
+        "mapa.shared::cluster.u32 there, %3, %4;\n\t"
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [to], [%1], %2, [there];\n\t}" ::"r"(dst),
+        "r"(src), "r"(bytes), "r"(bar), "r"(cta)
+        : "memory");
+}
+
+template <int OP, int PARTS>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+    narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const ProductArgs p)
+{
+    constexpr bool SYMMETRIC = OP == kGram || OP == kSquare;
+    constexpr bool ACROSS = OP == kUpdate || OP == kLast;
+    constexpr uint32_t IDESC = (1u << 4) | (ACROSS ? 1u << 16 : 0u) | (static_cast<uint32_t>(kNarrow >> 3) << 17) |
+                               (static_cast<uint32_t>(kBlock >> 4) << 24);
+    constexpr int FULL = 0, EMPTY = kNarrowStages, ACC_FULL = 2 * kNarrowStages, SUMS = ACC_FULL + 1;
+    constexpr int WIDTH = kNarrow / PARTS;                 // columns that a CTA writes
+    constexpr int SHARE = WIDTH * kBlock;                  // their sums from one part
+    constexpr int GROUPS = WIDTH / 16;                     // of 8 columns of a warp
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    float4* exchange = reinterpret_cast<float4*>(smem + kNarrowStages * kNarrowStage);
+    // the shares for the others take the stages' place when the products are summed
+    float4* shares = reinterpret_cast<float4*>(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kNarrowStages * kNarrowStage + kExchange);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kNarrowStages + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PARTS > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const Tile c = narrow_tile_at<SYMMETRIC>(static_cast<int>(blockIdx.x) / PARTS,
+                                             static_cast<int>(narrow_tiles(SYMMETRIC, p.m, p.n)), p.m);
+    const int depth = (p.k + kDepth - 1) / kDepth;
+    const int first = depth * rank / PARTS, last = depth * (rank + 1) / PARTS;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * kNarrowStages + 2; ++i) mbar_init(bar(i), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
+    }
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kNarrow)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (PARTS > 1 && threadIdx.x == 0) mbar_expect_tx(bar(SUMS), (PARTS - 1) * SHARE * 4);
+    if (PARTS > 1) cluster_sync();  // the cluster's CTAs run, and count, before one copies to another
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // everything this kernel reads is the work of the kernels ahead
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // the epilogue's rows and, in groups of 8, columns; what the sums are added to
+    const int q = warp & 3, half = warp >= 6 ? 1 : 0;
+    const int row = c.row + 32 * q + lane, col0 = c.col + rank * WIDTH + half * (WIDTH / 2);
+    const bool writes = warp >= 2 && row < p.m;
+    uint32_t v[32];  // sums of the lane's row, 32 columns
+    const int64_t plane = static_cast<int64_t>(c.e) * p.m;
+    const int64_t matrix_values = static_cast<int64_t>(p.batch) * p.m * p.pitch;
+    uint4 add[GROUPS], rest[GROUPS];
+    uint4* rest_at = nullptr;
+    const int64_t rest_bytes = 2LL * kRestBlock * p.batch * p.rest_rows * p.rest_cols;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- loads ----------------
+            asm volatile("fence.proxy.async;" ::: "memory");  // copies written by ordinary stores
+            uint32_t fills = 0;
+            for (int d = first; d < last; ++d, ++fills) {
+                const int stage = static_cast<int>(fills % kNarrowStages);
+                if (!wait_bounded(bar(EMPTY + stage), (fills / kNarrowStages & 1) ^ 1, abort_flag, p.dev_status)) break;
+                if (kBoundsCheck && !(gemm::tma_box_start_ok(d * kDepth, c.row, 2, p.dev_status) &&
+                                      gemm::tma_box_start_ok(c.col, d * kDepth, 2, p.dev_status) && c.e < p.batch)) {
+                    record_bounds_error(p.dev_status);
+                    *abort_flag = 1;
+                    break;
+                }
+                const uint32_t full = bar(FULL + stage), at = smem_u32(smem + stage * kNarrowStage);
+                mbar_expect_tx(full, kNarrowStage);
+                load_3d<1>(at, &map_a, d * kDepth, c.row, c.e, full);
+                load_3d<1>(at + kLeftBytes, &map_b, ACROSS ? c.col : d * kDepth, ACROSS ? d * kDepth : c.col, c.e, full);
+            }
+            if (*abort_flag)  // copies already issued land before the CTA can exit
+                for (uint32_t s = 0; s < kNarrowStages; ++s) {
+                    const uint32_t n = fills > s ? (fills - s + kNarrowStages - 1) / kNarrowStages : 0u;
+                    if (n) wait_bounded(bar(FULL + s), (n - 1) & 1, abort_flag, nullptr, true);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer ----------------
+            uint32_t fills = 0;
+            for (int d = first; d < last; ++d, ++fills) {
+                const int stage = static_cast<int>(fills % kNarrowStages);
+                if (!wait_bounded(bar(FULL + stage), fills / kNarrowStages & 1, abort_flag, p.dev_status)) break;
+                tc_fence_after();
+                const uint32_t at = smem_u32(smem + stage * kNarrowStage);
+                const uint64_t da = desc_sw128(at), db = ACROSS ? desc_across(at + kLeftBytes) : desc_sw128(at + kLeftBytes);
+#pragma unroll
+                for (int k = 0; k < kDepth / 16; ++k)
+                    mma_f16<1>(tmem, da + 2 * k, db + (ACROSS ? 128 : 2) * k, IDESC, fills != 0 || k != 0 ? 1u : 0u);
+                mma_commit<1>(bar(EMPTY + stage));
+            }
+            mma_commit<1>(bar(ACC_FULL));  // after an abort too: the tensor memory is freed behind it
+            wait_bounded(bar(ACC_FULL), 0, abort_flag, nullptr, true);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- sums to the CTAs that write them ----------------
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            add[g] = rest[g] = make_uint4(0, 0, 0, 0);
+            const int col = col0 + 8 * g;
+            if (OP != kGram && writes && col < p.pitch)
+                add[g] = ld_checked(reinterpret_cast<const uint4*>(p.addend + (plane + row) * p.pitch + col), p.addend,
+                                    2 * matrix_values, p.dev_status);
+            if (ACROSS) {
+                rest_at = reinterpret_cast<uint4*>(p.rest) +
+                          (((static_cast<int64_t>(c.e) * p.rest_rows + c.row / kBlock) * p.rest_cols + c.col / kBlock) *
+                               (kRestBlock / 8) + (q * 16 + col0 % kBlock / 8) * 32 + lane);
+                rest[g] = ld_checked(rest_at + 32 * g, p.rest, rest_bytes, p.dev_status);
+            }
+        }
+        bool ready = lane == 0 ? wait_bounded(bar(ACC_FULL), 0, abort_flag, p.dev_status) : false;
+        ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
+        if (ready) {
+            tc_fence_after();
+            tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + 32 * half, v);
+            tmem_wait_ld();
+            if (PARTS > 1) {
+                float4* dst = shares + 8 * half * kBlock + 32 * q + lane;  // [owner][4 columns][row]
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dst[i * kBlock] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                  __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                fence_async_smem();
+            }
+        }
+        if (PARTS > 1) {
+            named_sync(1, 32 * kNarrowEpi);
+            const int owner = static_cast<int>(threadIdx.x) - 64;
+            if (ready && owner < PARTS && owner != rank)
+                copy_to_cta(smem_u32(exchange + rank * (SHARE / 4)), smem_u32(shares + owner * (SHARE / 4)), SHARE * 4,
+                            bar(SUMS), static_cast<uint32_t>(owner));
+            if (lane == 0) wait_bounded(bar(SUMS), 0, abort_flag, p.dev_status);
+            __syncwarp();
+        }
+    }
+    // the cluster's CTAs stay until each has what the others sent
+    if (PARTS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (writes) {
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int col = col0 + 8 * g;
+            if (col >= p.n) break;
+            float f[8];
+            if (PARTS == 1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * g + i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    const float4* src = (i == rank ? shares : exchange) + i * (SHARE / 4) +
+                                        (half * (WIDTH / 8) + 2 * g) * kBlock + 32 * q + lane;
+                    const float4 lo = src[0], hi = src[kBlock];
+                    f[0] += lo.x; f[1] += lo.y; f[2] += lo.z; f[3] += lo.w;
+                    f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
+                }
+            }
+            const uint32_t aw[4] = {add[g].x, add[g].y, add[g].z, add[g].w};
+            const uint32_t rw[4] = {rest[g].x, rest[g].y, rest[g].z, rest[g].w};
+            uint32_t o[4], r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 x = make_float2(p.beta * f[2 * i], p.beta * f[2 * i + 1]);
+                if (OP != kGram) {
+                    float2 a = halves(aw[i]);
+                    if (ACROSS) {
+                        const float2 s = halves(rw[i]);
+                        a.x += s.x * kRestUnit;
+                        a.y += s.y * kRestUnit;
+                    }
+                    x.x += p.alpha * a.x;
+                    x.y += p.alpha * a.y;
+                }
+                o[i] = OP == kLast ? pack_bf16(x.x, x.y) : pack_half(x.x, x.y);
+                if (OP == kUpdate) {
+                    const float2 w = halves(o[i]);
+                    r[i] = pack_half((x.x - w.x) * (1.0f / kRestUnit), (x.y - w.y) * (1.0f / kRestUnit));
+                }
+            }
+            if (OP == kUpdate) st_checked(rest_at + 32 * g, make_uint4(r[0], r[1], r[2], r[3]), p.rest, rest_bytes, p.dev_status);
+            // rows of the intermediate matrices end on 128 bytes
+            const int64_t out_values = OP == kLast ? (p.batch - 1) * p.out_stride + ((p.transposed ? p.n : p.m) - 1) * p.ldo +
+                                                         (p.transposed ? p.m : p.n)
+                                                   : static_cast<int64_t>(p.batch) * p.m * p.ldo;
+            uint16_t* const out = p.out + c.e * p.out_stride;
+            if (OP != kLast || !p.transposed) {
+                uint16_t* dst = out + static_cast<int64_t>(row) * p.ldo + col;
+                if (OP != kLast || p.by_tma) {
+                    st_checked(reinterpret_cast<uint4*>(dst), make_uint4(o[0], o[1], o[2], o[3]), p.out, 2 * out_values,
+                               p.dev_status);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (col + i < p.n)
+                            st_checked(dst + i, static_cast<uint16_t>(o[i / 2] >> (16 * (i & 1))), p.out, 2 * out_values,
+                                       p.dev_status);
+                }
+            }
+            if (SYMMETRIC ? c.row / kBlock != c.col / kBlock : (OP == kLast && p.transposed)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (col + i < p.n)
+                        st_checked(out + static_cast<int64_t>(col + i) * p.ldo + row,
+                                   static_cast<uint16_t>(o[i / 2] >> (16 * (i & 1))), p.out, 2 * out_values, p.dev_status);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kNarrow) : "memory");
+    }
+    __syncwarp();
+    if (PARTS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---- the norm and the scaled copies --------------------------------------------------------
@@ -567,8 +891,8 @@ struct PrepareArgs {
     int batch, transposed;
     int parts;                          // partial sums per matrix
     double* partials;                   // [batch][parts]
-    float* state;
-    int state_rows, state_cols;
+    __half* rest;
+    int rest_rows, rest_cols;
     __half* x;
     double scale, eps;
     int* dev_status;
@@ -624,7 +948,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const PrepareArgs a)
                    8 * static_cast<int64_t>(a.batch) * a.parts, a.dev_status);
 }
 
-// X times the scale over the norm: in FP32 in the order of the products' epilogue, and in FP16 row by row.
+// X times the scale over the norm: in FP16 row by row, and the rest to it in the order of the products' epilogue.
 // A CTA takes pieces of 32 rows x 128 columns of X through shared memory (G^T: both sides stay coalesced).
 template <bool F32>
 __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs a)
@@ -679,12 +1003,19 @@ __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs
                 }
         }
         __syncthreads();
-        const int64_t block = (e * a.state_rows + r0 / kBlock) * a.state_cols + c0 / kBlock;
-        float4* dst = reinterpret_cast<float4*>(a.state + block * kStateBlock) + (r0 % kBlock) / 32 * 32 * 32;
-        const int64_t state_bytes = 4LL * kStateBlock * a.batch * a.state_rows * a.state_cols;
-        for (int c4 = warp; c4 < 32; c4 += kNormThreads / 32)
-            st_checked(dst + c4 * 32 + lane, *reinterpret_cast<const float4*>(&tile[lane][4 * c4]), a.state,
-                       state_bytes, a.dev_status);
+        const int64_t block = (e * a.rest_rows + r0 / kBlock) * a.rest_cols + c0 / kBlock;
+        uint4* dst = reinterpret_cast<uint4*>(a.rest + block * kRestBlock) + (r0 % kBlock) / 32 * 16 * 32;
+        const int64_t rest_bytes = 2LL * kRestBlock * a.batch * a.rest_rows * a.rest_cols;
+        for (int c8 = warp; c8 < 16; c8 += kNormThreads / 32) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = *reinterpret_cast<const float2*>(&tile[lane][8 * c8 + 2 * i]);
+                const float2 h = halves(pack_half(f.x, f.y));
+                o[i] = pack_half((f.x - h.x) * (1.0f / kRestUnit), (f.y - h.y) * (1.0f / kRestUnit));
+            }
+            st_checked(dst + c8 * 32 + lane, make_uint4(o[0], o[1], o[2], o[3]), a.rest, rest_bytes, a.dev_status);
+        }
         for (int r = warp; r < 32; r += kNormThreads / 32) {
             if (r0 + r >= a.m || c0 + 4 * lane >= a.pitch) continue;
             const float4 v = *reinterpret_cast<const float4*>(&tile[r][4 * lane]);
@@ -716,11 +1047,8 @@ bool make_map(CUtensorMap* map, void* data, int64_t cols, int64_t rows, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-using ProductKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-                               const ProductArgs);
-
 template <int CG>
-ProductKernel product_of(int op)
+auto product_of(int op)
 {
     switch (op) {
         case kGram: return product_kernel<CG, kGram>;
@@ -729,23 +1057,98 @@ ProductKernel product_of(int op)
         default: return product_kernel<CG, kLast>;
     }
 }
+template <int PARTS>
+auto narrow_of(int op)
+{
+    switch (op) {
+        case kGram: return narrow_kernel<kGram, PARTS>;
+        case kSquare: return narrow_kernel<kSquare, PARTS>;
+        case kUpdate: return narrow_kernel<kUpdate, PARTS>;
+        default: return narrow_kernel<kLast, PARTS>;
+    }
+}
+auto narrow_of(int op, int parts)
+{
+    return parts == 1 ? narrow_of<1>(op) : (parts == 2 ? narrow_of<2>(op) : narrow_of<4>(op));
+}
 
-cudaError_t configure_once(int* device)
+// Once per device: the kernels' shared memory, and how many pairs and clusters of 1, 2, 4 can run at once.
+struct Resident {
+    int singles, pairs, clusters[3];  // clusters of 2^i CTAs
+};
+cudaError_t resident_on_device(int sm_count, Resident* out)
 {
     constexpr int kDevices = 64;
-    static bool done[kDevices] = {};
+    static Resident known[kDevices] = {};
     static std::mutex mutex;
-    if (cudaGetDevice(device) != cudaSuccess || *device < 0 || *device >= kDevices) return cudaErrorInvalidDevice;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mutex);
-    if (done[*device]) return cudaSuccess;
-    for (int op = 0; op < 4; ++op)
-        for (int cg = 1; cg <= 2; ++cg) {
-            const void* f = reinterpret_cast<const void*>(cg == 1 ? product_of<1>(op) : product_of<2>(op));
-            const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-            if (e != cudaSuccess) return e;
+    Resident& r = known[device];
+    if (r.singles == 0) {
+        cudaError_t e = cudaSuccess;
+        for (int op = 0; op < 4; ++op) {
+            const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+            if ((e = cudaFuncSetAttribute(product_of<1>(op), attr, kSmem)) != cudaSuccess) return e;
+            if ((e = cudaFuncSetAttribute(product_of<2>(op), attr, kSmem)) != cudaSuccess) return e;
+            for (int parts = 1; parts <= 4; parts *= 2)
+                if ((e = cudaFuncSetAttribute(narrow_of(op, parts), attr, kNarrowSmem)) != cudaSuccess) return e;
         }
-    done[*device] = true;
+        for (int i = 0; i < 3; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 1u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(sm_count >> i << i));
+            cfg.blockDim = dim3(kNarrowThreads);
+            cfg.dynamicSmemBytes = kNarrowSmem;
+            e = cudaOccupancyMaxActiveClusters(&r.clusters[i], narrow_of(kGram, 1 << i), &cfg);
+            if (e != cudaSuccess) return e;
+            if (i == 1) {
+                cfg.blockDim = dim3(kThreads);
+                cfg.dynamicSmemBytes = kSmem;
+                e = cudaOccupancyMaxActiveClusters(&r.pairs, product_of<2>(kGram), &cfg);
+                if (e != cudaSuccess) return e;
+            }
+        }
+        if (r.pairs < 1) return cudaErrorInvalidConfiguration;
+        r.singles = sm_count;
+    }
+    *out = r;
     return cudaSuccess;
+}
+
+// How a product is spread over the SMs: tiles of 128 x 128 by single CTAs, of 256 x 256 by pairs, or (parts > 0) a
+// tile of 128 x 64 by a cluster of `parts`.
+struct Plan {
+    int cg, parts;
+    int64_t workers;
+};
+Plan plan_of(bool symmetric, int64_t batch, int64_t m, int64_t n, int64_t k, const Resident& r)
+{
+    // us: a step of K (256 x 256 is bound by the tensor cores' power, the others by what an SM can read from
+    // L2), and the rest of a kernel
+    const int64_t depth = (k + kDepth - 1) / kDepth;
+    const int64_t small = batch * tiles_of<128>(symmetric, m, n), large = batch * tiles_of<256>(symmetric, m, n);
+    const int64_t narrow = batch * narrow_tiles(symmetric, m, n);
+    const double single = static_cast<double>((small + r.singles - 1) / r.singles * depth) * 0.27 + 5.0;
+    const double pair = static_cast<double>((large + r.pairs - 1) / r.pairs * depth) * 0.385 + 6.4;
+    Plan best = pair <= single ? Plan{2, 0, large < r.pairs ? large : r.pairs}
+                               : Plan{1, 0, small < r.singles ? small : r.singles};
+    double time = pair <= single ? pair : single;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t parts = int64_t(1) << i;
+        if (parts > depth || narrow > r.clusters[i]) continue;
+        const double clusters = static_cast<double>((depth + parts - 1) / parts) * 0.3 + (parts == 1 ? 3.7 : 4.3);
+        if (clusters <= time) {
+            time = clusters;
+            best = Plan{1, static_cast<int>(parts), narrow};
+        }
+    }
+    return best;
 }
 
 // A kernel behind another one of the same call; it waits for that itself.
@@ -770,9 +1173,9 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t 
 }
 
 struct Sizes {
-    int64_t m, n, x_pitch, a_pitch, state_rows, state_cols;
+    int64_t m, n, x_pitch, a_pitch, rest_rows, rest_cols;
     int parts;
-    size_t partials, state, x, a;  // bytes
+    size_t partials, rest, x, a;  // bytes
 };
 
 Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
@@ -782,14 +1185,14 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
     s.n = rows < cols ? cols : rows;
     s.x_pitch = (s.n + 63) / 64 * 64;  // rows of whole 128-byte lines
     s.a_pitch = (s.m + 63) / 64 * 64;
-    s.state_rows = (s.m + kBlock - 1) / kBlock;
-    s.state_cols = (s.n + kBlock - 1) / kBlock;
+    s.rest_rows = (s.m + kBlock - 1) / kBlock;
+    s.rest_cols = (s.n + kBlock - 1) / kBlock;
     // partial sums: 16 K values each, no more than fill the SMs several times
     int64_t parts = (rows * cols + 16383) / 16384;
     const int64_t most = batch < 592 ? 592 / batch : 1;
     s.parts = static_cast<int>(parts < most ? parts : most);
     s.partials = round256(8 * static_cast<size_t>(batch) * s.parts);
-    s.state = round256(4 * static_cast<size_t>(kStateBlock) * batch * s.state_rows * s.state_cols);
+    s.rest = round256(2 * static_cast<size_t>(kRestBlock) * batch * s.rest_rows * s.rest_cols);
     s.x = round256(2 * static_cast<size_t>(batch) * s.m * s.x_pitch);
     s.a = round256(2 * static_cast<size_t>(batch) * s.m * s.a_pitch);
     return s;
@@ -800,21 +1203,22 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
 size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols)
 {
     const Sizes s = sizes_of(batch, rows, cols);
-    return s.partials + s.state + 2 * s.x + 2 * s.a;
+    return 256 + s.partials + s.rest + 2 * s.x + 2 * s.a;
 }
 
 cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaStream_t s)
 {
-    int device = 0;
-    cudaError_t e = configure_once(&device);
+    Resident resident;
+    cudaError_t e = resident_on_device(sm_count, &resident);
     if (e != cudaSuccess) return e;
     const Sizes z = sizes_of(g.batch, g.rows, g.cols);
     const bool transposed = g.rows > g.cols;
-    uint8_t* at = static_cast<uint8_t*>(g.workspace);
+    // on a 256-byte boundary: rows are read 32 bytes at a time
+    uint8_t* at = reinterpret_cast<uint8_t*>(round256(reinterpret_cast<uintptr_t>(g.workspace)));
     double* partials = reinterpret_cast<double*>(at);
-    float* state = reinterpret_cast<float*>(at += z.partials);
+    __half* rest = reinterpret_cast<__half*>(at += z.partials);
     __half* x[2];
-    x[0] = reinterpret_cast<__half*>(at += z.state);
+    x[0] = reinterpret_cast<__half*>(at += z.rest);
     x[1] = reinterpret_cast<__half*>(at += z.x);
     __half* a = reinterpret_cast<__half*>(at += z.x);
     __half* b = reinterpret_cast<__half*>(at += z.a);
@@ -834,27 +1238,33 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     pa.transposed = transposed;
     pa.parts = z.parts;
     pa.partials = partials;
-    pa.state = state;
-    pa.state_rows = static_cast<int>(z.state_rows);
-    pa.state_cols = static_cast<int>(z.state_cols);
+    pa.rest = rest;
+    pa.rest_rows = static_cast<int>(z.rest_rows);
+    pa.rest_cols = static_cast<int>(z.rest_cols);
     pa.x = x[0];
     pa.scale = S;
     pa.eps = g.eps;
     pa.dev_status = g.dev_status;
 
-    CUtensorMap x_rows[2], x_across[2], x_store[2], a_rows, b_rows, a_store, b_store, a_turn, b_turn, out_store;
+    // left operands in boxes of 128 rows x 64 of K, right ones of 64 rows (across: of K) x 64, stores of 32 x 64
+    // or, turned, 64 x 32
+    CUtensorMap x_left[2], x_right[2], x_store[2], a_left, a_right, b_left, a_store, b_store, a_turn, b_turn, out_store;
     bool ok = true;
-    const int64_t xs = z.m * z.x_pitch, as = z.m * z.a_pitch;
-    for (int i = 0; i < 2; ++i)
-        ok = ok && make_map(&x_rows[i], x[i], z.n, z.m, g.batch, z.x_pitch, xs, kDepth, kBlock, true) &&
-             make_map(&x_across[i], x[i], z.n, z.m, g.batch, z.x_pitch, xs, 64, kDepth, true) &&
-             make_map(&x_store[i], x[i], z.n, z.m, g.batch, z.x_pitch, xs, 64, 32, true);
-    ok = ok && make_map(&a_rows, a, z.m, z.m, g.batch, z.a_pitch, as, kDepth, kBlock, true) &&
-         make_map(&b_rows, b, z.m, z.m, g.batch, z.a_pitch, as, kDepth, kBlock, true) &&
-         make_map(&a_store, a, z.m, z.m, g.batch, z.a_pitch, as, 64, 32, true) &&
-         make_map(&b_store, b, z.m, z.m, g.batch, z.a_pitch, as, 64, 32, true) &&
-         make_map(&a_turn, a, z.m, z.m, g.batch, z.a_pitch, as, 32, 64, false) &&
-         make_map(&b_turn, b, z.m, z.m, g.batch, z.a_pitch, as, 32, 64, false);
+    auto map_of = [&](CUtensorMap* map, __half* data, int64_t cols, int64_t pitch, int box_x, int box_y, bool swizzle) {
+        ok = ok && make_map(map, data, cols, z.m, g.batch, pitch, z.m * pitch, box_x, box_y, swizzle);
+    };
+    for (int i = 0; i < 2; ++i) {
+        map_of(&x_left[i], x[i], z.n, z.x_pitch, kDepth, kBlock, true);
+        map_of(&x_right[i], x[i], z.n, z.x_pitch, 64, 64, true);
+        map_of(&x_store[i], x[i], z.n, z.x_pitch, 64, 32, true);
+    }
+    map_of(&a_left, a, z.m, z.a_pitch, kDepth, kBlock, true);
+    map_of(&a_right, a, z.m, z.a_pitch, 64, 64, true);
+    map_of(&b_left, b, z.m, z.a_pitch, kDepth, kBlock, true);
+    map_of(&a_store, a, z.m, z.a_pitch, 64, 32, true);
+    map_of(&b_store, b, z.m, z.a_pitch, 64, 32, true);
+    map_of(&a_turn, a, z.m, z.a_pitch, 32, 64, false);
+    map_of(&b_turn, b, z.m, z.a_pitch, 32, 64, false);
     // tensor stores want 16-byte aligned rows, and end on 16 bytes: on B200 one that was clipped at 131 columns
     // wrote past them
     const bool by_tma = (reinterpret_cast<uintptr_t>(g.out) & 15) == 0 && g.ldo % 8 == 0 &&
@@ -870,55 +1280,53 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     if (g.f32) norm_kernel<true><<<norm_grid, kNormThreads, 0, s>>>(pa);
     else       norm_kernel<false><<<norm_grid, kNormThreads, 0, s>>>(pa);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t pieces = g.batch * ((z.m + 31) / 32) * z.state_cols;
+    const int64_t pieces = g.batch * ((z.m + 31) / 32) * z.rest_cols;
     const dim3 prepare_grid(static_cast<unsigned>(pieces < 8 * sm_count ? pieces : 8 * sm_count));
     e = launch_chained(g.f32 ? prepare_kernel<true> : prepare_kernel<false>, prepare_grid, kNormThreads, 0, 1, s, pa);
     if (e != cudaSuccess) return e;
 
     ProductArgs p = {};
     p.batch = static_cast<int>(g.batch);
-    p.addend = a;
-    p.pitch = z.a_pitch;
-    p.state = state;
-    p.state_rows = pa.state_rows;
-    p.state_cols = pa.state_cols;
-    p.out = static_cast<uint16_t*>(g.out);
-    p.ldo = g.ldo;
-    p.out_stride = g.out_stride;
+    p.rest = rest;
+    p.rest_rows = pa.rest_rows;
+    p.rest_cols = pa.rest_cols;
     p.transposed = transposed;
     p.by_tma = by_tma;
     p.dev_status = g.dev_status;
-    auto product = [&](int op, int64_t m, int64_t n, int64_t k, const CUtensorMap& ma, const CUtensorMap& mb,
-                       const CUtensorMap& md, const CUtensorMap& mt, double alpha, double beta) {
-        p.m = static_cast<int>(m);
+    auto product = [&](int op, int64_t n, int64_t k, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md,
+                       const CUtensorMap& mt, const __half* addend, int64_t pitch, __half* out, double alpha,
+                       double beta) {
+        p.m = static_cast<int>(z.m);
         p.n = static_cast<int>(n);
         p.k = static_cast<int>(k);
+        p.addend = addend;
+        p.pitch = pitch;
         p.alpha = static_cast<float>(alpha);
         p.beta = static_cast<float>(beta);
-        auto tiles = [&](int64_t side) {
-            const int64_t r = (m + side - 1) / side, c = (n + side - 1) / side;
-            return g.batch * (op == kGram || op == kSquare ? r * (r + 1) / 2 : r * c);
-        };
-        // pairs of CTAs from half a wave of their tiles on
-        const int pairs = sm_count / 2;
-        const int cg = tiles(2 * kBlock) * 2 >= pairs ? 2 : 1;
-        const int64_t t = tiles(cg * kBlock), most = cg == 2 ? pairs : sm_count;
-        const dim3 grid(static_cast<unsigned>(cg * (t < most ? t : most)));
-        return launch_chained(cg == 1 ? product_of<1>(op) : product_of<2>(op), grid, kThreads, kSmem, cg, s, ma, mb, md,
+        p.out = op == kLast ? static_cast<uint16_t*>(g.out) : reinterpret_cast<uint16_t*>(out);
+        p.ldo = op == kLast ? g.ldo : (op == kUpdate ? z.x_pitch : z.a_pitch);
+        p.out_stride = op == kLast ? g.out_stride : z.m * p.ldo;
+        const Plan plan = plan_of(op == kGram || op == kSquare, g.batch, z.m, n, k, resident);
+        if (plan.parts > 0)
+            return launch_chained(narrow_of(op, plan.parts), dim3(static_cast<unsigned>(plan.parts * plan.workers)),
+                                  kNarrowThreads, kNarrowSmem, plan.parts, s, ma, mb, p);
+        return launch_chained(plan.cg == 1 ? product_of<1>(op) : product_of<2>(op),
+                              dim3(static_cast<unsigned>(plan.cg * plan.workers)), kThreads, kSmem, plan.cg, s, ma, mb, md,
                               mt, p);
     };
     int now = 0;
     for (int i = 0; i < g.steps; ++i) {
         const double ca = g.coefficients[3 * i], cb = g.coefficients[3 * i + 1], cc = g.coefficients[3 * i + 2];
         const bool last = i + 1 == g.steps;
-        e = product(kGram, z.m, z.m, z.n, x_rows[now], x_rows[now], a_store, a_turn, 0.0, kScaleA / (S * S));
+        e = product(kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0,
+                    kScaleA / (S * S));
         if (e != cudaSuccess) return e;
-        e = product(kSquare, z.m, z.m, z.m, a_rows, a_rows, b_store, b_turn, cb * kScaleB / kScaleA,
+        e = product(kSquare, z.m, z.m, a_left, a_right, b_store, b_turn, a, z.a_pitch, b, cb * kScaleB / kScaleA,
                     cc * kScaleB / kScaleA / kScaleA);
         if (e != cudaSuccess) return e;
         const double unit = last ? 1.0 / S : 1.0;
-        e = product(last ? kLast : kUpdate, z.m, z.n, z.m, b_rows, x_across[now], last ? out_store : x_store[now ^ 1],
-                    last ? out_store : a_turn, ca * unit, unit / kScaleB);
+        e = product(last ? kLast : kUpdate, z.n, z.m, b_left, x_right[now], last ? out_store : x_store[now ^ 1],
+                    last ? out_store : a_turn, x[now], z.x_pitch, x[now ^ 1], ca * unit, unit / kScaleB);
         if (e != cudaSuccess) return e;
         now ^= 1;
     }

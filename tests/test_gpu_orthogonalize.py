@@ -187,8 +187,10 @@ def test_workspace_is_enough_and_no_state_is_kept():
     want = B.orthogonalize(g)
     for fill in (0xFF, 0, 0x7C):
         room.fill_(fill)
-        assert torch.equal(B.orthogonalize(g, workspace=room[256:256 + need]), want)
-        assert (room[:256] == fill).all() and (room[256 + need:] == fill).all()
+        for first in (256, 16, 144):  # 16-byte aligned is enough
+            assert torch.equal(B.orthogonalize(g, workspace=room[first:first + need]), want)
+            assert (room[:first] == fill).all() and (room[first + need:] == fill).all()
+            room.fill_(fill)
 
 
 def test_on_another_stream_captured_and_replayed():
