@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -38,7 +39,7 @@ class Operand(ctypes.Structure):
                 ("amax", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
-class HeadsStruct(ctypes.Structure):
+class HeadsStruct(ctypes.Structure):  # nvfp4_heads (the binding packs it into bytes: a third of the time)
     _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
@@ -202,7 +203,7 @@ def _open(path):
     L.nvfp4_qk_norm_rope_workspace_bytes.restype = sz
     L.nvfp4_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
     L.nvfp4_orthogonalize_workspace_bytes.restype = sz
-    hd = ctypes.POINTER(HeadsStruct)
+    hd = vp  # nvfp4_heads
     for name, argtypes in {
             "qk_norm_rope": [hd, hd, i32, i64, i64, vp, vp, f32, vp, vp, i64, i64, i32, hd, hd, i32, vp,
                              vp],
@@ -882,37 +883,62 @@ def rope_table(positions, rotary, base=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
-def _heads(what, t, dtypes, tokens, heads, dim):
-    """The nvfp4_heads of a tensor [tokens, heads, dim] and the reference a call takes."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) or (
-            t.shape[2] != dim) or t.stride(2) != 1:
-        raise ValueError(f"{what} must be [{tokens}, {'heads' if heads is None else heads}, {dim}] with unit "
-                         f"stride in a head, got {tuple(t.shape)} strides {t.stride()}")
-    return HeadsStruct(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1))
+_pack_heads = struct.Struct("Pqqq").pack
 
 
-def _ref(struct):
-    return None if struct is None else ctypes.byref(struct)
+def _heads(what, t, dtype, shape):
+    """The nvfp4_heads of a tensor [tokens, heads, dim], as bytes."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if t.shape != shape or stride[2] != 1:
+        raise ValueError(f"{what} must be {tuple(shape)} with unit stride in a head, got {tuple(t.shape)} strides "
+                         f"{stride}")
+    return _pack_heads(t.data_ptr(), shape[1], stride[0], stride[1])
 
 
-def _rotation(positions, table, tokens):
-    """rows and width of the table (0, 0 without one)."""
+def _head_inputs(q, k, positions, table, q_weight, k_weight):
+    """Checks what both directions take; (shape of q, shape of k or None, nvfp4_heads of both, the
+    table's rows and width)."""
+    if q.dtype not in _F32_BF16:
+        raise TypeError(f"q must be {' or '.join(str(d) for d in _F32_BF16)}, got {q.dtype}")
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens, heads, dim], got {tuple(shape)}")
+    T, _, D = shape
     if positions is not None:
-        _dense("positions", positions, torch.int32, (tokens,))
-    if table is None:
-        return 0, 0
-    _dense("table", table, torch.float32, table.shape)
-    if table.dim() != 2:
-        raise ValueError(f"table must be [positions, rotary], got {tuple(table.shape)}")
-    return table.shape
-
-
-def _head_weights(dim, **weights):
-    for name, w in weights.items():
+        _dense("positions", positions, torch.int32, (T,))
+    rows = rotary = 0
+    if table is not None:
+        rows, rotary = size = table.shape if table.dim() == 2 else (0, 0)
+        _dense("table", table, torch.float32, size)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _dense(name, w, torch.float32, (dim,))
+            _dense(name, w, torch.float32, (D,))
+    if k is None:
+        return shape, None, _heads("q", q, q.dtype, shape), None, rows, rotary
+    if k.dim() != 3:
+        raise ValueError(f"k must be [tokens, heads, dim], got {tuple(k.shape)}")
+    k_shape = (T, k.shape[1], D)
+    return shape, k_shape, _heads("q", q, q.dtype, shape), _heads("k", k, q.dtype, k_shape), rows, rotary
+
+
+def _head_outputs(names, q_out, k_out, q_shape, k_shape, dtype, device, stream):
+    """Outputs of q's and k's shape (made where they are None) and their nvfp4_heads; both have one type, that
+    of one that was given or `dtype`."""
+    if q_out is None or (k_out is None and k_shape is not None):
+        with _allocating(stream):
+            if q_out is None:
+                q_out = _poisoned(torch.empty(q_shape, dtype=dtype if k_out is None else k_out.dtype, device=device))
+            if k_out is None and k_shape is not None:
+                k_out = _poisoned(torch.empty(k_shape, dtype=q_out.dtype, device=device))
+    dtype = q_out.dtype
+    if dtype not in _F32_BF16:
+        raise TypeError(f"{names[0]} must be {' or '.join(str(d) for d in _F32_BF16)}, got {dtype}")
+    q_heads = _heads(names[0], q_out, dtype, q_shape)
+    if k_shape is None:
+        return q_out, None, q_heads, None
+    return q_out, k_out, q_heads, _heads(names[1], k_out, dtype, k_shape)
 
 
 def qk_norm_rope(q, k, positions=None, table=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -921,27 +947,15 @@ def qk_norm_rope(q, k, positions=None, table=None, q_weight=None, k_weight=None,
     """nvfp4_qk_norm_rope: every head of q [T, Hq, D] and k [T, Hk, D] (k may be None) normalised, times
     its weight, and rotated by its token's position (table: rope_table; None: no rotation).  The
     outputs' type is that of q_out and k_out when given, else out_dtype."""
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, heads, dim], got {tuple(q.shape)}")
-    T, Hq, D = q.shape
-    rows, rotary = _rotation(positions, table, T)
-    _head_weights(D, q_weight=q_weight, k_weight=k_weight)
-    xq = _heads("q", q, _F32_BF16, T, Hq, D)
-    xk = None if k is None else _heads("k", k, (q.dtype,), T, None, D)
-    with _allocating(stream):
-        if q_out is None:
-            q_out = _poisoned(torch.empty((T, Hq, D), dtype=out_dtype if k_out is None else k_out.dtype,
-                                          device=q.device))
-        if k_out is None and k is not None:
-            k_out = _poisoned(torch.empty((T, k.shape[1], D), dtype=q_out.dtype, device=q.device))
-    zq = _heads("q_out", q_out, _F32_BF16, T, Hq, D)
-    zk = None if k is None else _heads("k_out", k_out, (q_out.dtype,), T, k.shape[1], D)
-    queue = _queue("nvfp4_qk_norm_rope", stream, q, k, positions, table, q_weight, k_weight, q_out,
-                   k_out if k is not None else None, dev_status)
+    shape, k_shape, xq, xk, rows, rotary = _head_inputs(q, k, positions, table, q_weight, k_weight)
+    q_out, k_out, zq, zk = _head_outputs(("q_out", "k_out"), q_out, k_out, shape, k_shape, out_dtype, q.device,
+                                         stream)
+    queue = _queue("nvfp4_qk_norm_rope", stream, q, k, positions, table, q_weight, k_weight, q_out, k_out,
+                   dev_status)
     _check(lib().nvfp4_qk_norm_rope(
-        ctypes.byref(xq), _ref(xk), _dtype_code(q.dtype), T, D, _address(q_weight), _address(k_weight), eps,
-        _address(positions), _address(table), rows, rotary, int(bool(interleaved)), ctypes.byref(zq),
-        _ref(zk), _dtype_code(q_out.dtype), _status_word(dev_status), queue), "nvfp4_qk_norm_rope")
+        xq, xk, _dtype_code(q.dtype), shape[0], shape[2], _address(q_weight), _address(k_weight), eps,
+        _address(positions), _address(table), rows, rotary, 1 if interleaved else 0, zq, zk,
+        _dtype_code(q_out.dtype), _status_word(dev_status), queue), "nvfp4_qk_norm_rope")
     return q_out, k_out
 
 
@@ -950,45 +964,40 @@ def qk_norm_rope_backward(dq, dk, q, k, positions=None, table=None, q_weight=Non
                           dq_weight=None, dk_weight=None, workspace=None, dev_status=None, stream=None):
     """nvfp4_qk_norm_rope_backward: (dq_in, dk_in, dq_weight, dk_weight), the gradients of q, k (before
     the norm) and of the weights (float32 [D], also where a weight is None)."""
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, heads, dim], got {tuple(q.shape)}")
-    T, Hq, D = q.shape
+    shape, k_shape, xq, xk, rows, rotary = _head_inputs(q, k, positions, table, q_weight, k_weight)
     if (k is None) != (dk is None):
         raise ValueError("dk must be given with k and only with it")
-    Hk = 0 if k is None else k.shape[1]
-    rows, rotary = _rotation(positions, table, T)
-    _head_weights(D, q_weight=q_weight, k_weight=k_weight)
-    xq = _heads("q", q, _F32_BF16, T, Hq, D)
-    xk = None if k is None else _heads("k", k, (q.dtype,), T, None, D)
-    zq = _heads("dq", dq, _F32_BF16, T, Hq, D)
-    zk = None if k is None else _heads("dk", dk, (dq.dtype,), T, Hk, D)
-    with _allocating(stream):
-        if dq_in is None:
-            dq_in = _poisoned(torch.empty((T, Hq, D), dtype=dx_dtype if dk_in is None else dk_in.dtype,
-                                          device=q.device))
-        if dk_in is None and k is not None:
-            dk_in = _poisoned(torch.empty((T, Hk, D), dtype=dq_in.dtype, device=q.device))
-        if dq_weight is None:
-            dq_weight = _poisoned(_new((D,), torch.float32, q.device))
-        if dk_weight is None and k is not None:
-            dk_weight = _poisoned(_new((D,), torch.float32, q.device))
-        need = lib().nvfp4_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
-        if workspace is None:
-            workspace = _workspace(need, q.device)
+    if dq.dtype not in _F32_BF16:
+        raise TypeError(f"dq must be {' or '.join(str(d) for d in _F32_BF16)}, got {dq.dtype}")
+    T, Hq, D = shape
+    Hk = 0 if k is None else k_shape[1]
+    zq = _heads("dq", dq, dq.dtype, shape)
+    zk = None if k is None else _heads("dk", dk, dq.dtype, k_shape)
+    dq_in, dk_in, gq, gk = _head_outputs(("dq_in", "dk_in"), dq_in, dk_in, shape, k_shape, dx_dtype, q.device,
+                                         stream)
+    L = lib()
+    need = L.nvfp4_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
+    if dq_weight is None or dk_weight is None or workspace is None:
+        with _allocating(stream):
+            if dq_weight is None:
+                dq_weight = _poisoned(_new((D,), torch.float32, q.device))
+            if dk_weight is None and k is not None:
+                dk_weight = _poisoned(_new((D,), torch.float32, q.device))
+            if workspace is None:
+                workspace = _workspace(need, q.device)
     _workspace_size(workspace, need)
-    _head_weights(D, dq_weight=dq_weight, dk_weight=dk_weight)
-    gq = _heads("dq_in", dq_in, _F32_BF16, T, Hq, D)
-    gk = None if k is None else _heads("dk_in", dk_in, (dq_in.dtype,), T, Hk, D)
+    _dense("dq_weight", dq_weight, torch.float32, (D,))
     if k is None:
-        dk_in = dk_weight = None
+        dk_weight = None
+    else:
+        _dense("dk_weight", dk_weight, torch.float32, (D,))
     queue = _queue("nvfp4_qk_norm_rope_backward", stream, dq, dk, q, k, positions, table, q_weight, k_weight,
                    dq_in, dk_in, dq_weight, dk_weight, workspace, dev_status)
-    _check(lib().nvfp4_qk_norm_rope_backward(
-        ctypes.byref(zq), _ref(zk), _dtype_code(dq.dtype), ctypes.byref(xq), _ref(xk), _dtype_code(q.dtype),
-        T, D, _address(q_weight), _address(k_weight), eps, _address(positions), _address(table), rows, rotary,
-        int(bool(interleaved)), ctypes.byref(gq), _ref(gk), _dtype_code(dq_in.dtype), _address(dq_weight),
-        _address(dk_weight), _address(workspace), _status_word(dev_status), queue),
-        "nvfp4_qk_norm_rope_backward")
+    _check(L.nvfp4_qk_norm_rope_backward(
+        zq, zk, _dtype_code(dq.dtype), xq, xk, _dtype_code(q.dtype), T, D, _address(q_weight),
+        _address(k_weight), eps, _address(positions), _address(table), rows, rotary, 1 if interleaved else 0, gq,
+        gk, _dtype_code(dq_in.dtype), _address(dq_weight), _address(dk_weight), _address(workspace),
+        _status_word(dev_status), queue), "nvfp4_qk_norm_rope_backward")
     return dq_in, dk_in, dq_weight, dk_weight
 
 

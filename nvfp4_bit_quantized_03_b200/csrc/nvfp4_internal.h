@@ -216,7 +216,7 @@ cudaError_t launch_combine_backward(const CombineArgs& a, bool f32, int sm_count
 
 // Norms and rotation of queries and keys (qk_norm.cu): index 0 the queries, 1 the keys.
 constexpr int kMaxHeadDim = 512;     // a head's units of 16 values fill at most one warp
-constexpr int kMaxHeadCtas = 1776;   // CTAs of the gradient (12 per SM), i.e. rows of its partial sums
+constexpr int kMaxHeadCtas = 592;    // CTAs of the gradient (4 per SM), i.e. rows of its partial sums
 struct HeadsView {
     void* data;
     int64_t heads, token_stride, head_stride;  // strides in elements

@@ -25,19 +25,38 @@ constexpr int kWarps = 4;  // warps per CTA
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kDevIndex = 8;  // NVFP4_DEVSTAT_INDEX
 
+// 8 values as they lie in memory.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t bytes, int* status, float* f)
+struct Raw8 {
+    uint4 v[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t bytes, int* status, Raw8<F32>& r)
+{
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) r.v[i] = ld_checked(p + i, base, bytes, status);
+}
+template <bool F32>
+__device__ __forceinline__ void values(const Raw8<F32>& r, float* f)
 {
     if (F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-        const float4 a = ld_checked(p, base, bytes, status), b = ld_checked(p + 1, base, bytes, status);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(r.v[i].x);
+            f[4 * i + 1] = __uint_as_float(r.v[i].y);
+            f[4 * i + 2] = __uint_as_float(r.v[i].z);
+            f[4 * i + 3] = __uint_as_float(r.v[i].w);
+        }
     } else {
-        unpack8(ld_checked(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at), base,
-                           bytes, status), f);
+        unpack8(r.v[0], f);
     }
 }
+// A unit of a head.
+template <bool F32>
+struct Unit {
+    Raw8<F32> a, b;
+};
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -56,22 +75,6 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int64_t bytes, in
         st_checked(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at),
                    make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])),
                    base, bytes, status);
-    }
-}
-
-// 16 values of an array of one FP32 per value of a head (a weight; 1 without one).
-__device__ __forceinline__ void load_weight(const float* w, int c0, int c1, int D, int* status, float* f)
-{
-    if (!w) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = 1.0f;
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const float4 v = ldg_checked(reinterpret_cast<const float4*>(w + (h < 2 ? c0 : c1) + 4 * (h & 1)), w,
-                                     4 * D, status);
-        f[4 * h] = v.x; f[4 * h + 1] = v.y; f[4 * h + 2] = v.z; f[4 * h + 3] = v.w;
     }
 }
 
@@ -179,117 +182,159 @@ __device__ __forceinline__ int64_t extent(const HeadsView& v, const HeadsArgs& a
     return esize * ((a.tokens - 1) * v.token_stride + (v.heads - 1) * v.head_stride + a.D);
 }
 
+// The weights of queries and keys (ones without them) in shared memory.
+__device__ __forceinline__ void share_weights(float (*shared)[kMaxHeadDim], const HeadsArgs& a)
+{
+    for (int i = threadIdx.x; i < 2 * a.D; i += 32 * kWarps) {
+        const int kind = i >= a.D, d = i - kind * a.D;
+        const float* w = a.weight[kind];
+        shared[kind][d] = w ? ldg_checked(w + d, w, 4 * a.D, a.dev_status) : 1.0f;
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void unit_weights(const float* shared, const Place& p, float* w)
+{
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const float4 v = *reinterpret_cast<const float4*>(shared + (h < 2 ? p.c0 : p.c1) + 4 * (h & 1));
+        w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_unit(const HeadsView& x, const HeadsArgs& a, int64_t t, int64_t h, const Place& p,
+                                          Unit<F32>& u)
+{
+    const int64_t at = t * x.token_stride + h * x.head_stride, bytes = extent(x, a, F32 ? 4 : 2);
+    load8<F32>(x.data, at + p.c0, bytes, a.dev_status, u.a);
+    load8<F32>(x.data, at + p.c1, bytes, a.dev_status, u.b);
+}
+template <bool F32>
+__device__ __forceinline__ void store_unit(const HeadsView& z, const HeadsArgs& a, int64_t t, int64_t h, const Place& p,
+                                           const float* f)
+{
+    const int64_t at = t * z.token_stride + h * z.head_stride, bytes = extent(z, a, F32 ? 4 : 2);
+    store8<F32>(z.data, at + p.c0, bytes, a.dev_status, f);
+    store8<F32>(z.data, at + p.c1, bytes, a.dev_status, f + 8);
+}
+
+// A warp takes a token, or a slice of its heads; the values of its next heads are on their way while it works on
+// those before.  (They are read for padding too, and not used.)
 template <bool IN_F32, bool OUT_F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const HeadsArgs a)
 {
+    __shared__ __align__(16) float weights[2][kMaxHeadDim];
+    share_weights(weights, a);
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int64_t t = item / a.slices;
     if (t >= a.tokens) return;
     const Place p = place(a, INTERLEAVED, lane);
+    const int together = 32 / a.lanes;
+    const int q_steps = static_cast<int>((a.x[0].heads + together - 1) / together);
+    const int steps = q_steps + static_cast<int>((a.x[1].heads + together - 1) / together);
+    auto head = [&](int j) { return (j >= q_steps ? j - q_steps : j) * together + p.slot; };
+    auto on = [&](int j) { return p.in && j < steps && head(j) < a.x[j >= q_steps].heads; };
+    int j = static_cast<int>(item - t * a.slices);
+    Unit<IN_F32> next = {};
+    if (on(j)) load_unit<IN_F32>(a.x[j >= q_steps], a, t, head(j), p, next);
     float c[8], s[8];
     const bool there = load_angles(a, t, p, lane, c, s);
-    const int together = 32 / a.lanes;
-    const int q_steps = (a.x[0].heads + together - 1) / together;
-    const int steps = q_steps + (a.x[1].heads + together - 1) / together;
-    for (int j = static_cast<int>(item % a.slices); j < steps; j += a.slices) {
+    for (; j < steps; j += a.slices) {
         const int kind = j >= q_steps;
-        const HeadsView& x = a.x[kind];
-        const HeadsView& z = a.z[kind];
-        const int h = (kind ? j - q_steps : j) * together + p.slot;
-        const bool on = p.in && h < x.heads;
         float f[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+        values<IN_F32>(next.a, f);
+        values<IN_F32>(next.b, f + 8);
+        if (on(j + a.slices)) load_unit<IN_F32>(a.x[j + a.slices >= q_steps], a, t, head(j + a.slices), p, next);
         if (there) {
-            float w[16];
-            if (on) {
-                const int64_t at = t * x.token_stride + h * x.head_stride;
-                const int64_t bytes = extent(x, a, IN_F32 ? 4 : 2);
-                load8<IN_F32>(x.data, at + p.c0, bytes, a.dev_status, f);
-                load8<IN_F32>(x.data, at + p.c1, bytes, a.dev_status, f + 8);
-                load_weight(a.weight[kind], p.c0, p.c1, a.D, a.dev_status, w);
+            if (!on(j)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = 0.0f;
             }
             float scale;
             const float r = head_norm(f, a, scale);
-            if (on) {
+            if (on(j)) {
+                float w[16];
+                unit_weights(weights[kind], p, w);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) f[i] = f[i] * r * w[i];
                 if (p.turned) turn<INTERLEAVED, 1>(f, c, s);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = 0.0f;
         }
-        if (on) {
-            const int64_t at = t * z.token_stride + h * z.head_stride;
-            const int64_t bytes = extent(z, a, OUT_F32 ? 4 : 2);
-            store8<OUT_F32>(z.data, at + p.c0, bytes, a.dev_status, f);
-            store8<OUT_F32>(z.data, at + p.c1, bytes, a.dev_status, f + 8);
-        }
+        if (on(j)) store_unit<OUT_F32>(a.z[kind], a, t, head(j), p, f);
     }
 }
 
-// The first q_ctas CTAs take the queries, the others the keys: a warp keeps one weight and the partial
-// sums of its gradient in registers over all its tokens.  The CTA's sums go to a row of the workspace.
+// The first q_ctas CTAs take the queries, the others the keys: a warp keeps the partial sums of one weight's
+// gradient in registers over all its tokens.  The CTA's sums go to a row of the workspace.
 template <bool X_F32, bool Z_F32, bool DX_F32, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_backward_kernel(const HeadsArgs a)
+__global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(const HeadsArgs a)
 {
+    __shared__ __align__(16) float weights[2][kMaxHeadDim];
     __shared__ float part[kWarps][kMaxHeadDim];
+    share_weights(weights, a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kind = static_cast<int>(blockIdx.x) >= a.q_ctas;
     const int64_t cta = kind ? blockIdx.x - a.q_ctas : blockIdx.x;
-    const int64_t ctas = kind ? gridDim.x - a.q_ctas : a.q_ctas;
+    const int64_t warps = (kind ? gridDim.x - a.q_ctas : a.q_ctas) * kWarps;
     const HeadsView& xv = a.x[kind];
     const HeadsView& zv = a.z[kind];
-    const HeadsView& dv = a.dx[kind];
     const Place p = place(a, INTERLEAVED, lane);
     const int together = 32 / a.lanes;
-    const int64_t steps = (xv.heads + together - 1) / together;
-    float w[16], dw[16];
+    const int steps = static_cast<int>((xv.heads + together - 1) / together);
+    float dw[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = dw[i] = 0.0f;
-    if (p.in) load_weight(a.weight[kind], p.c0, p.c1, a.D, a.dev_status, w);
-    // a warp's items in order: all steps of a token before the next one
-    for (int64_t item = cta * kWarps + warp; item < a.tokens * a.slices; item += ctas * kWarps) {
+    for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+    auto on = [&](int j) { return p.in && j < steps && j * together + p.slot < xv.heads; };
+    // a warp's items in order: all steps of a token (or of its slice) before the next one
+    for (int64_t item = cta * kWarps + warp; item < a.tokens * a.slices; item += warps) {
         const int64_t t = item / a.slices;
+        int j = static_cast<int>(item - t * a.slices);
+        Unit<X_F32> x = {};
+        Unit<Z_F32> z = {};
+        if (on(j)) {
+            load_unit<X_F32>(xv, a, t, j * together + p.slot, p, x);
+            load_unit<Z_F32>(zv, a, t, j * together + p.slot, p, z);
+        }
         float c[8], s[8];
         const bool there = load_angles(a, t, p, lane, c, s);
-        for (int64_t j = item % a.slices; j < steps; j += a.slices) {
-            const int64_t h = j * together + p.slot;
-            const bool on = p.in && h < xv.heads;
+        for (; j < steps; j += a.slices) {
+            const bool now = on(j);
             float f[16], g[16];
+            values<X_F32>(x.a, f);
+            values<X_F32>(x.b, f + 8);
+            values<Z_F32>(z.a, g);
+            values<Z_F32>(z.b, g + 8);
+            if (on(j + a.slices)) {
+                load_unit<X_F32>(xv, a, t, (j + a.slices) * together + p.slot, p, x);
+                load_unit<Z_F32>(zv, a, t, (j + a.slices) * together + p.slot, p, z);
+            }
+            if (!there || !now) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = g[i] = 0.0f;
+                for (int i = 0; i < 16; ++i) f[i] = g[i] = 0.0f;
+            }
             if (there) {
-                if (on) {
-                    const int64_t at = t * xv.token_stride + h * xv.head_stride;
-                    const int64_t bytes = extent(xv, a, X_F32 ? 4 : 2);
-                    load8<X_F32>(xv.data, at + p.c0, bytes, a.dev_status, f);
-                    load8<X_F32>(xv.data, at + p.c1, bytes, a.dev_status, f + 8);
-                    const int64_t gat = t * zv.token_stride + h * zv.head_stride;
-                    const int64_t gbytes = extent(zv, a, Z_F32 ? 4 : 2);
-                    load8<Z_F32>(zv.data, gat + p.c0, gbytes, a.dev_status, g);
-                    load8<Z_F32>(zv.data, gat + p.c1, gbytes, a.dev_status, g + 8);
-                    if (p.turned) turn<INTERLEAVED, -1>(g, c, s);
-                }
+                if (p.turned) turn<INTERLEAVED, -1>(g, c, s);
                 float scale;
                 const float r = head_norm(f, a, scale);
+                float w[16];
+                if (p.in) unit_weights(weights[kind], p, w);
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     f[i] *= r;
                     dw[i] += g[i] * f[i];
-                    g[i] *= w[i];
+                    g[i] = now ? g[i] * w[i] : 0.0f;
                     dot += g[i] * f[i];
                 }
                 dot = head_sum(dot, a.lanes) * a.inv_D;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) f[i] = r * (g[i] - f[i] * dot) * scale;
             }
-            if (on) {
-                const int64_t at = t * dv.token_stride + h * dv.head_stride;
-                const int64_t bytes = extent(dv, a, DX_F32 ? 4 : 2);
-                store8<DX_F32>(dv.data, at + p.c0, bytes, a.dev_status, f);
-                store8<DX_F32>(dv.data, at + p.c1, bytes, a.dev_status, f + 8);
-            }
+            if (now) store_unit<DX_F32>(a.dx[kind], a, t, j * together + p.slot, p, f);
         }
     }
     // over the heads of a warp, then over the warps, in a fixed order

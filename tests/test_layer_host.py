@@ -61,7 +61,7 @@ def test_rope_table():
 def test_workspace_sizes():
     f = B.lib().nvfp4_qk_norm_rope_workspace_bytes
     assert f(1, 1, 0, 16) >= 2 * 16 * 4
-    assert f(1 << 20, 32, 8, 128) == 1776 * 128 * 4
+    assert 148 * 128 * 4 <= f(1 << 20, 32, 8, 128) <= 1 << 20
     for bad in ((0, 1, 1, 64), (1, 0, 1, 64), (1, 1, -1, 64), (1, 1, 1, 0), (1, 1, 1, 24), (1, 1, 1, 528),
                 (1 << 31, 1, 1, 64), (1, 1 << 21, 1, 64)):
         assert f(*bad) == 0
