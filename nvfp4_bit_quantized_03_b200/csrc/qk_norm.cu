@@ -4,10 +4,10 @@
 //   backward: dy = dz turned back,  dw = sum dy n,  dn = w dy,  dx = r (dn - n mean(dn n))
 // All in FP32; the only rounding to fewer bits is the one of the outputs to their type.
 //
-// A lane holds a unit of 16 values of a head, two chunks of 8: both halves of 8 rotated pairs
-// (chunks 8 u and rotary / 2 + 8 u, or the 16 neighbours 16 u .. when the pairs are neighbours), or 16
-// neighbours behind the rotated part.  So a pair never leaves its lane, a lane stores only where it
-// has loaded (outputs may be the inputs), and the mean is one reduction over the head's lanes.
+// A lane holds a unit of 16 values of a head, the first and the second ones of 8 rotated pairs (or 16
+// neighbours behind the rotated part).  So a pair never leaves its lane, a lane stores only where it
+// has loaded (outputs may be the inputs), and the mean is one reduction over the head's lanes.  The arithmetic
+// goes two values at a time (.f32x2): by single values the passes were bound by instruction issue.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,79 +25,133 @@ constexpr int kWarps = 4;  // warps per CTA
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kDevIndex = 8;  // NVFP4_DEVSTAT_INDEX
 
-// 8 values as they lie in memory.
+typedef uint64_t Two;  // two FP32 values
+
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Two both(float v) { return f2pack(v, v); }
+
+// 8 values as they lie in memory: a chunk.
 template <bool F32>
-struct Raw8 {
+struct Chunk {
     uint4 v[F32 ? 2 : 1];
 };
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t bytes, int* status, Raw8<F32>& r)
+__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t bytes, int* status, Chunk<F32>& r)
 {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (F32 ? 4 : 2));
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) r.v[i] = ld_checked(p + i, base, bytes, status);
 }
 template <bool F32>
-__device__ __forceinline__ void values(const Raw8<F32>& r, float* f)
+__device__ __forceinline__ void store8(void* base, int64_t at, int64_t bytes, int* status, const Chunk<F32>& r)
 {
-    if (F32) {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + at * (F32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            f[4 * i] = __uint_as_float(r.v[i].x);
-            f[4 * i + 1] = __uint_as_float(r.v[i].y);
-            f[4 * i + 2] = __uint_as_float(r.v[i].z);
-            f[4 * i + 3] = __uint_as_float(r.v[i].w);
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) st_checked(p + i, r.v[i], base, bytes, status);
+}
+__device__ __forceinline__ float raw(uint32_t v) { return __uint_as_float(v); }
+
+// The unit of two chunks: v[0..3] the first values of the 8 pairs, v[4..7] the second ones.  Pairs are
+// value i of both chunks, or neighbours.
+template <bool F32, bool INTERLEAVED>
+__device__ __forceinline__ void to_unit(const Chunk<F32>& x, const Chunk<F32>& y, Two* v)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const Chunk<F32>& c = h ? y : x;
+        float f[8];
+        if (F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4& w = c.v[F32 ? i : 0];
+                f[4 * i] = raw(w.x); f[4 * i + 1] = raw(w.y); f[4 * i + 2] = raw(w.z); f[4 * i + 3] = raw(w.w);
+            }
+        } else {
+            unpack8(c.v[0], f);
         }
-    } else {
-        unpack8(r.v[0], f);
+        if (INTERLEAVED) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[2 * h + i] = f2pack(f[4 * i], f[4 * i + 2]);
+                v[4 + 2 * h + i] = f2pack(f[4 * i + 1], f[4 * i + 3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * h + i] = f2pack(f[2 * i], f[2 * i + 1]);
+        }
     }
 }
-// A unit of a head.
-template <bool F32>
-struct Unit {
-    Raw8<F32> a, b;
-};
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-
-template <bool F32>
-__device__ __forceinline__ void store8(void* base, int64_t at, int64_t bytes, int* status, const float* f)
+template <bool F32, bool INTERLEAVED>
+__device__ __forceinline__ void from_unit(const Two* v, Chunk<F32>& x, Chunk<F32>& y)
 {
-    if (F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        st_checked(p, make_float4(f[0], f[1], f[2], f[3]), base, bytes, status);
-        st_checked(p + 1, make_float4(f[4], f[5], f[6], f[7]), base, bytes, status);
-    } else {
-        st_checked(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at),
-                   make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])),
-                   base, bytes, status);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        Chunk<F32>& c = h ? y : x;
+        float f[8];
+        if (INTERLEAVED) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[4 * i] = f2lo(v[2 * h + i]);
+                f[4 * i + 1] = f2lo(v[4 + 2 * h + i]);
+                f[4 * i + 2] = f2hi(v[2 * h + i]);
+                f[4 * i + 3] = f2hi(v[4 + 2 * h + i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = f2lo(v[4 * h + i]);
+                f[2 * i + 1] = f2hi(v[4 * h + i]);
+            }
+        }
+        if (F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                c.v[F32 ? i : 0] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                              __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+        } else {
+            c.v[0] = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+        }
     }
 }
 
 // The place of a lane: its head among those a warp takes together, its unit of that head.
 struct Place {
-    int slot, c0, c1;  // c0, c1: first values of the unit's two chunks
+    int slot, unit;
+    int c0, c1;        // first values of the unit's two chunks
     bool in, turned;   // the head has this unit; its values are rotated
 };
-__device__ __forceinline__ Place place(const HeadsArgs& a, bool interleaved, int lane)
+template <bool INTERLEAVED>
+__device__ __forceinline__ Place place(const HeadsArgs& a, int lane)
 {
-    const int u = lane & (a.lanes - 1);
     Place p;
+    p.unit = lane & (a.lanes - 1);
     p.slot = lane / a.lanes;
-    p.in = 16 * u < a.D;
-    p.turned = 16 * u < a.rotary;
-    p.c0 = interleaved || !p.turned ? 16 * u : 8 * u;
-    p.c1 = interleaved || !p.turned ? 16 * u + 8 : a.rotary / 2 + 8 * u;
+    p.in = 16 * p.unit < a.D;
+    p.turned = 16 * p.unit < a.rotary;
+    p.c0 = INTERLEAVED || !p.turned ? 16 * p.unit : 8 * p.unit;
+    p.c1 = INTERLEAVED || !p.turned ? 16 * p.unit + 8 : a.rotary / 2 + 8 * p.unit;
     return p;
+}
+// Place i (0 .. 15) of a unit's values: which value of the head it is.
+template <bool INTERLEAVED>
+__device__ __forceinline__ int value_at(const Place& p, int i)
+{
+    if (INTERLEAVED) return 16 * p.unit + 2 * (i & 7) + (i >> 3);
+    return (i < 8 ? p.c0 : p.c1) + (i & 7);
 }
 
 // Cosines and sines of the unit's 8 pairs at the token's position; false for a token without one.
-__device__ __forceinline__ bool load_angles(const HeadsArgs& a, int64_t t, const Place& p, int lane, float* c,
-                                            float* s)
+__device__ __forceinline__ bool load_angles(const HeadsArgs& a, int64_t t, const Place& p, int lane, Two* c, Two* s)
 {
     int64_t at = t;
     if (a.positions) at = ld_checked(a.positions + t, a.positions, 4 * a.tokens, a.dev_status);
@@ -107,37 +161,41 @@ __device__ __forceinline__ bool load_angles(const HeadsArgs& a, int64_t t, const
         return false;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = 1.0f;
-        s[i] = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        c[i] = both(1.0f);
+        s[i] = both(0.0f);
     }
     if (p.turned) {
-        const int u8 = 8 * (lane & (a.lanes - 1));
-        const float* row = a.table + at * a.rotary;
+        const float* row = a.table + at * a.rotary + 8 * p.unit;
         const int64_t bytes = 4 * a.table_rows * a.rotary;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float4 vc = ldg_checked(reinterpret_cast<const float4*>(row + u8) + h, a.table, bytes,
+            const float4 vc = ldg_checked(reinterpret_cast<const float4*>(row) + h, a.table, bytes, a.dev_status);
+            const float4 vs = ldg_checked(reinterpret_cast<const float4*>(row + a.rotary / 2) + h, a.table, bytes,
                                           a.dev_status);
-            const float4 vs = ldg_checked(reinterpret_cast<const float4*>(row + a.rotary / 2 + u8) + h, a.table,
-                                          bytes, a.dev_status);
-            c[4 * h] = vc.x; c[4 * h + 1] = vc.y; c[4 * h + 2] = vc.z; c[4 * h + 3] = vc.w;
-            s[4 * h] = vs.x; s[4 * h + 1] = vs.y; s[4 * h + 2] = vs.z; s[4 * h + 3] = vs.w;
+            c[2 * h] = f2pack(vc.x, vc.y);
+            c[2 * h + 1] = f2pack(vc.z, vc.w);
+            s[2 * h] = f2pack(vs.x, vs.y);
+            s[2 * h + 1] = f2pack(vs.z, vs.w);
         }
     }
     return true;
 }
 
-// f[0..15]: the unit's values, turned by the angles (SIGN +1) or back (-1).
-template <bool INTERLEAVED, int SIGN>
-__device__ __forceinline__ void turn(float* f, const float* c, const float* s)
+// The unit's pairs turned by the angles (SIGN +1) or back (-1).
+template <int SIGN>
+__device__ __forceinline__ void turn(Two* v, const Two* c, const Two* s)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int ia = INTERLEAVED ? 2 * i : i, ib = INTERLEAVED ? 2 * i + 1 : i + 8;
-        const float x = f[ia], y = f[ib], sn = SIGN > 0 ? s[i] : -s[i];
-        f[ia] = x * c[i] - y * sn;
-        f[ib] = y * c[i] + x * sn;
+    for (int i = 0; i < 4; ++i) {
+        const Two x = v[i], y = v[4 + i];
+        if (SIGN > 0) {
+            v[i] = sub2_rn(mul2_rn(x, c[i]), mul2_rn(y, s[i]));
+            v[4 + i] = fma2(x, s[i], mul2_rn(y, c[i]));
+        } else {
+            v[i] = fma2(y, s[i], mul2_rn(x, c[i]));
+            v[4 + i] = sub2_rn(mul2_rn(y, c[i]), mul2_rn(x, s[i]));
+        }
     }
 }
 
@@ -150,21 +208,21 @@ __device__ __forceinline__ float head_sum(float v, int lanes)
 // 1 / sqrt(mean x^2 + eps) of the head.  Where the squares leave FP32 the values are taken times
 // `scale` = 2^-70 (1 otherwise), in place; then the root is that of the scaled ones, so that scale r x is
 // the normalised value either way.
-__device__ __forceinline__ float head_norm(float* x, const HeadsArgs& a, float& scale)
+__device__ __forceinline__ float head_norm(Two* x, const HeadsArgs& a, float& scale)
 {
-    float ss = 0.0f;
+    Two sum = mul2_rn(x[0], x[0]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
-    ss = head_sum(ss, a.lanes);
+    for (int i = 1; i < 8; ++i) sum = fma2(x[i], x[i], sum);
+    float ss = head_sum(f2lo(sum) + f2hi(sum), a.lanes);
     scale = 1.0f;
     float eps = a.eps;
     const bool large = !(ss < INFINITY);
     if (__any_sync(kAll, large)) {
         float sl = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float v = x[i] * 0x1p-70f;
-            sl += v * v;
+        for (int i = 0; i < 8; ++i) {
+            const Two v = mul2_rn(x[i], both(0x1p-70f));
+            sl += f2lo(v) * f2lo(v) + f2hi(v) * f2hi(v);
             if (large) x[i] = v;
         }
         sl = head_sum(sl, a.lanes);
@@ -182,25 +240,38 @@ __device__ __forceinline__ int64_t extent(const HeadsView& v, const HeadsArgs& a
     return esize * ((a.tokens - 1) * v.token_stride + (v.heads - 1) * v.head_stride + a.D);
 }
 
-// The weights of queries and keys (ones without them) in shared memory.
-__device__ __forceinline__ void share_weights(float (*shared)[kMaxHeadDim], const HeadsArgs& a)
+// The weights (ones without them) of queries and keys in shared memory, four by four of a unit's places and
+// then by unit: lanes read neighbouring 16 bytes.
+constexpr int kMaxUnits = kMaxHeadDim / 16;
+typedef float4 Weights[2][4][kMaxUnits];
+template <bool INTERLEAVED>
+__device__ __forceinline__ void share_weights(Weights shared, const HeadsArgs& a)
 {
     for (int i = threadIdx.x; i < 2 * a.D; i += 32 * kWarps) {
-        const int kind = i >= a.D, d = i - kind * a.D;
+        const int kind = i >= a.D, v = i - kind * a.D;
+        const Place p = place<INTERLEAVED>(a, v / 16);  // a.lanes is at least the number of units
+        const int d = value_at<INTERLEAVED>(p, v & 15);
         const float* w = a.weight[kind];
-        shared[kind][d] = w ? ldg_checked(w + d, w, 4 * a.D, a.dev_status) : 1.0f;
+        reinterpret_cast<float*>(&shared[kind][(v & 15) / 4][v / 16])[v & 3] =
+            w ? ldg_checked(w + d, w, 4 * a.D, a.dev_status) : 1.0f;
     }
     __syncthreads();
 }
-__device__ __forceinline__ void unit_weights(const float* shared, const Place& p, float* w)
+__device__ __forceinline__ void unit_weights(const float4 (*shared)[kMaxUnits], const Place& p, Two* w)
 {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-        const float4 v = *reinterpret_cast<const float4*>(shared + (h < 2 ? p.c0 : p.c1) + 4 * (h & 1));
-        w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
+        const float4 v = shared[h][p.unit];
+        w[2 * h] = f2pack(v.x, v.y);
+        w[2 * h + 1] = f2pack(v.z, v.w);
     }
 }
 
+// The two chunks of a lane's unit of head h.
+template <bool F32>
+struct Unit {
+    Chunk<F32> a, b;
+};
 template <bool F32>
 __device__ __forceinline__ void load_unit(const HeadsView& x, const HeadsArgs& a, int64_t t, int64_t h, const Place& p,
                                           Unit<F32>& u)
@@ -209,13 +280,15 @@ __device__ __forceinline__ void load_unit(const HeadsView& x, const HeadsArgs& a
     load8<F32>(x.data, at + p.c0, bytes, a.dev_status, u.a);
     load8<F32>(x.data, at + p.c1, bytes, a.dev_status, u.b);
 }
-template <bool F32>
+template <bool F32, bool INTERLEAVED>
 __device__ __forceinline__ void store_unit(const HeadsView& z, const HeadsArgs& a, int64_t t, int64_t h, const Place& p,
-                                           const float* f)
+                                           const Two* v)
 {
     const int64_t at = t * z.token_stride + h * z.head_stride, bytes = extent(z, a, F32 ? 4 : 2);
-    store8<F32>(z.data, at + p.c0, bytes, a.dev_status, f);
-    store8<F32>(z.data, at + p.c1, bytes, a.dev_status, f + 8);
+    Unit<F32> u;
+    from_unit<F32, INTERLEAVED>(v, u.a, u.b);
+    store8<F32>(z.data, at + p.c0, bytes, a.dev_status, u.a);
+    store8<F32>(z.data, at + p.c1, bytes, a.dev_status, u.b);
 }
 
 // A warp takes a token, or a slice of its heads; the values of its next heads are on their way while it works on
@@ -223,13 +296,11 @@ __device__ __forceinline__ void store_unit(const HeadsView& z, const HeadsArgs& 
 template <bool IN_F32, bool OUT_F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const HeadsArgs a)
 {
-    __shared__ __align__(16) float weights[2][kMaxHeadDim];
-    share_weights(weights, a);
+    __shared__ Weights weights;
     const int lane = threadIdx.x & 31;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int64_t t = item / a.slices;
-    if (t >= a.tokens) return;
-    const Place p = place(a, INTERLEAVED, lane);
+    const Place p = place<INTERLEAVED>(a, lane);
     const int together = 32 / a.lanes;
     const int q_steps = static_cast<int>((a.x[0].heads + together - 1) / together);
     const int steps = q_steps + static_cast<int>((a.x[1].heads + together - 1) / together);
@@ -237,34 +308,35 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const HeadsAr
     auto on = [&](int j) { return p.in && j < steps && head(j) < a.x[j >= q_steps].heads; };
     int j = static_cast<int>(item - t * a.slices);
     Unit<IN_F32> next = {};
-    if (on(j)) load_unit<IN_F32>(a.x[j >= q_steps], a, t, head(j), p, next);
-    float c[8], s[8];
-    const bool there = load_angles(a, t, p, lane, c, s);
+    Two c[4], s[4];
+    bool there = false;
+    if (t < a.tokens) {
+        if (on(j)) load_unit<IN_F32>(a.x[j >= q_steps], a, t, head(j), p, next);
+        there = load_angles(a, t, p, lane, c, s);
+    }
+    share_weights<INTERLEAVED>(weights, a);
+    if (t >= a.tokens) return;
     for (; j < steps; j += a.slices) {
         const int kind = j >= q_steps;
-        float f[16];
-        values<IN_F32>(next.a, f);
-        values<IN_F32>(next.b, f + 8);
+        Two v[8];
+        to_unit<IN_F32, INTERLEAVED>(next.a, next.b, v);
         if (on(j + a.slices)) load_unit<IN_F32>(a.x[j + a.slices >= q_steps], a, t, head(j + a.slices), p, next);
-        if (there) {
-            if (!on(j)) {
+        if (!there || !on(j)) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = 0.0f;
-            }
+            for (int i = 0; i < 8; ++i) v[i] = 0;
+        }
+        if (there) {
             float scale;
-            const float r = head_norm(f, a, scale);
+            const Two r = both(head_norm(v, a, scale));
             if (on(j)) {
-                float w[16];
+                Two w[8];
                 unit_weights(weights[kind], p, w);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = f[i] * r * w[i];
-                if (p.turned) turn<INTERLEAVED, 1>(f, c, s);
+                for (int i = 0; i < 8; ++i) v[i] = mul2_rn(mul2_rn(v[i], r), w[i]);
+                if (p.turned) turn<1>(v, c, s);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = 0.0f;
         }
-        if (on(j)) store_unit<OUT_F32>(a.z[kind], a, t, head(j), p, f);
+        if (on(j)) store_unit<OUT_F32, INTERLEAVED>(a.z[kind], a, t, head(j), p, v);
     }
 }
 
@@ -273,21 +345,21 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const HeadsAr
 template <bool X_F32, bool Z_F32, bool DX_F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(const HeadsArgs a)
 {
-    __shared__ __align__(16) float weights[2][kMaxHeadDim];
+    __shared__ Weights weights;
     __shared__ float part[kWarps][kMaxHeadDim];
-    share_weights(weights, a);
+    share_weights<INTERLEAVED>(weights, a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int kind = static_cast<int>(blockIdx.x) >= a.q_ctas;
     const int64_t cta = kind ? blockIdx.x - a.q_ctas : blockIdx.x;
     const int64_t warps = (kind ? gridDim.x - a.q_ctas : a.q_ctas) * kWarps;
     const HeadsView& xv = a.x[kind];
     const HeadsView& zv = a.z[kind];
-    const Place p = place(a, INTERLEAVED, lane);
+    const Place p = place<INTERLEAVED>(a, lane);
     const int together = 32 / a.lanes;
     const int steps = static_cast<int>((xv.heads + together - 1) / together);
-    float dw[16];
+    Two dw[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) dw[i] = 0;
     auto on = [&](int j) { return p.in && j < steps && j * together + p.slot < xv.heads; };
     // a warp's items in order: all steps of a token (or of its slice) before the next one
     for (int64_t item = cta * kWarps + warp; item < a.tokens * a.slices; item += warps) {
@@ -299,49 +371,57 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(c
             load_unit<X_F32>(xv, a, t, j * together + p.slot, p, x);
             load_unit<Z_F32>(zv, a, t, j * together + p.slot, p, z);
         }
-        float c[8], s[8];
+        Two c[4], s[4];
         const bool there = load_angles(a, t, p, lane, c, s);
         for (; j < steps; j += a.slices) {
             const bool now = on(j);
-            float f[16], g[16];
-            values<X_F32>(x.a, f);
-            values<X_F32>(x.b, f + 8);
-            values<Z_F32>(z.a, g);
-            values<Z_F32>(z.b, g + 8);
+            Two f[8], g[8];
+            to_unit<X_F32, INTERLEAVED>(x.a, x.b, f);
+            to_unit<Z_F32, INTERLEAVED>(z.a, z.b, g);
             if (on(j + a.slices)) {
                 load_unit<X_F32>(xv, a, t, (j + a.slices) * together + p.slot, p, x);
                 load_unit<Z_F32>(zv, a, t, (j + a.slices) * together + p.slot, p, z);
             }
             if (!there || !now) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = g[i] = 0.0f;
+                for (int i = 0; i < 8; ++i) f[i] = g[i] = 0;
             }
             if (there) {
-                if (p.turned) turn<INTERLEAVED, -1>(g, c, s);
+                if (p.turned) turn<-1>(g, c, s);
                 float scale;
                 const float r = head_norm(f, a, scale);
-                float w[16];
-                if (p.in) unit_weights(weights[kind], p, w);
-                float dot = 0.0f;
+                Two w[8];
+                unit_weights(weights[kind], p, w);
+                if (!p.in) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    f[i] *= r;
-                    dw[i] += g[i] * f[i];
-                    g[i] = now ? g[i] * w[i] : 0.0f;
-                    dot += g[i] * f[i];
+                    for (int i = 0; i < 8; ++i) w[i] = 0;
                 }
-                dot = head_sum(dot, a.lanes) * a.inv_D;
+                Two sum = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = r * (g[i] - f[i] * dot) * scale;
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = mul2_rn(f[i], both(r));
+                    dw[i] = fma2(g[i], f[i], dw[i]);
+                    g[i] = mul2_rn(g[i], w[i]);
+                    sum = fma2(g[i], f[i], sum);
+                }
+                const float dot = head_sum(f2lo(sum) + f2hi(sum), a.lanes) * a.inv_D;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = mul2_rn(fma2(f[i], both(-dot), g[i]), both(r));
+                if (scale != 1.0f) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = mul2_rn(f[i], both(scale));
+                }
             }
-            if (now) store_unit<DX_F32>(a.dx[kind], a, t, j * together + p.slot, p, f);
+            if (now) store_unit<DX_F32, INTERLEAVED>(a.dx[kind], a, t, j * together + p.slot, p, f);
         }
     }
     // over the heads of a warp, then over the warps, in a fixed order
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        for (int m = a.lanes; m < 32; m <<= 1) dw[i] += __shfl_xor_sync(kAll, dw[i], m);
-        if (p.slot == 0 && p.in) part[warp][(i < 8 ? p.c0 : p.c1) + (i & 7)] = dw[i];
+        const Two two = dw[(i & 7) / 2 + 4 * (i >> 3)];
+        float v = i & 1 ? f2hi(two) : f2lo(two);
+        for (int m = a.lanes; m < 32; m <<= 1) v += __shfl_xor_sync(kAll, v, m);
+        if (p.slot == 0 && p.in) part[warp][value_at<INTERLEAVED>(p, i)] = v;
     }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
