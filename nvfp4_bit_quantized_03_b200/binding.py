@@ -977,6 +977,15 @@ def qk_norm_rope_backward(dq, dk, q, k, positions=None, table=None, q_weight=Non
                                          stream)
     L = lib()
     need = L.nvfp4_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
+    if k is None:
+        dk_weight = None
+    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if w is not None:
+            _dense(name, w, torch.float32, (D,))
+    if workspace is not None:
+        _workspace_size(workspace, need)
+    queue = _queue("nvfp4_qk_norm_rope_backward", stream, dq, dk, q, k, positions, table, q_weight, k_weight,
+                   dq_in, dk_in, dq_weight, dk_weight, workspace, dev_status)
     if dq_weight is None or dk_weight is None or workspace is None:
         with _allocating(stream):
             if dq_weight is None:
@@ -985,14 +994,6 @@ def qk_norm_rope_backward(dq, dk, q, k, positions=None, table=None, q_weight=Non
                 dk_weight = _poisoned(_new((D,), torch.float32, q.device))
             if workspace is None:
                 workspace = _workspace(need, q.device)
-    _workspace_size(workspace, need)
-    _dense("dq_weight", dq_weight, torch.float32, (D,))
-    if k is None:
-        dk_weight = None
-    else:
-        _dense("dk_weight", dk_weight, torch.float32, (D,))
-    queue = _queue("nvfp4_qk_norm_rope_backward", stream, dq, dk, q, k, positions, table, q_weight, k_weight,
-                   dq_in, dk_in, dq_weight, dk_weight, workspace, dev_status)
     _check(L.nvfp4_qk_norm_rope_backward(
         zq, zk, _dtype_code(dq.dtype), xq, xk, _dtype_code(q.dtype), T, D, _address(q_weight),
         _address(k_weight), eps, _address(positions), _address(table), rows, rotary, 1 if interleaved else 0, gq,

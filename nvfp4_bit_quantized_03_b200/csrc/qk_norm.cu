@@ -41,16 +41,16 @@ struct Chunk {
     uint4 v[F32 ? 2 : 1];
 };
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t bytes, int* status, Chunk<F32>& r)
+__device__ __forceinline__ void load8(const char* at, const void* base, int64_t bytes, int* status, Chunk<F32>& r)
 {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + at * (F32 ? 4 : 2));
+    const uint4* p = reinterpret_cast<const uint4*>(at);
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) r.v[i] = ld_checked(p + i, base, bytes, status);
 }
 template <bool F32>
-__device__ __forceinline__ void store8(void* base, int64_t at, int64_t bytes, int* status, const Chunk<F32>& r)
+__device__ __forceinline__ void store8(char* at, void* base, int64_t bytes, int* status, const Chunk<F32>& r)
 {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + at * (F32 ? 4 : 2));
+    uint4* p = reinterpret_cast<uint4*>(at);
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) st_checked(p + i, r.v[i], base, bytes, status);
 }
@@ -201,7 +201,9 @@ __device__ __forceinline__ void turn(Two* v, const Two* c, const Two* s)
 
 __device__ __forceinline__ float head_sum(float v, int lanes)
 {
-    for (int w = lanes >> 1; w; w >>= 1) v += __shfl_xor_sync(kAll, v, w);
+#pragma unroll
+    for (int w = 16; w; w >>= 1)
+        if (lanes > w) v += __shfl_xor_sync(kAll, v, w);
     return v;
 }
 
@@ -235,11 +237,6 @@ __device__ __forceinline__ float head_norm(Two* x, const HeadsArgs& a, float& sc
     return rsqrtf(ss * a.inv_D + eps);
 }
 
-__device__ __forceinline__ int64_t extent(const HeadsView& v, const HeadsArgs& a, int64_t esize)
-{
-    return esize * ((a.tokens - 1) * v.token_stride + (v.heads - 1) * v.head_stride + a.D);
-}
-
 // The weights (ones without them) of queries and keys in shared memory, four by four of a unit's places and
 // then by unit: lanes read neighbouring 16 bytes.
 constexpr int kMaxUnits = kMaxHeadDim / 16;
@@ -247,13 +244,13 @@ typedef float4 Weights[2][4][kMaxUnits];
 template <bool INTERLEAVED>
 __device__ __forceinline__ void share_weights(Weights shared, const HeadsArgs& a)
 {
-    for (int i = threadIdx.x; i < 2 * a.D; i += 32 * kWarps) {
-        const int kind = i >= a.D, v = i - kind * a.D;
+    for (int i = threadIdx.x; i < 32 * a.lanes; i += 32 * kWarps) {
+        const int kind = i >= 16 * a.lanes, v = i - kind * 16 * a.lanes;
         const Place p = place<INTERLEAVED>(a, v / 16);  // a.lanes is at least the number of units
         const int d = value_at<INTERLEAVED>(p, v & 15);
         const float* w = a.weight[kind];
         reinterpret_cast<float*>(&shared[kind][(v & 15) / 4][v / 16])[v & 3] =
-            w ? ldg_checked(w + d, w, 4 * a.D, a.dev_status) : 1.0f;
+            !p.in ? 0.0f : (w ? ldg_checked(w + d, w, 4 * a.D, a.dev_status) : 1.0f);
     }
     __syncthreads();
 }
@@ -267,34 +264,53 @@ __device__ __forceinline__ void unit_weights(const float4 (*shared)[kMaxUnits], 
     }
 }
 
-// The two chunks of a lane's unit of head h.
+// The two chunks of a lane's unit of a head.
 template <bool F32>
 struct Unit {
     Chunk<F32> a, b;
 };
+// A lane's way through the heads of a token: head slot, slot + step, ...
 template <bool F32>
-__device__ __forceinline__ void load_unit(const HeadsView& x, const HeadsArgs& a, int64_t t, int64_t h, const Place& p,
-                                          Unit<F32>& u)
+struct Walk {
+    char* at;
+    int64_t step, second;  // bytes to the next head, to the unit's second chunk
+    void* base;            // for the debug build's checks
+    int64_t bytes;
+    int* status;
+    __device__ __forceinline__ Walk(const HeadsView& v, const HeadsArgs& a, int64_t t, int64_t head, int64_t heads_on,
+                                    const Place& p)
+    {
+        constexpr int64_t size = F32 ? 4 : 2;
+        at = static_cast<char*>(v.data) + size * (t * v.token_stride + head * v.head_stride + p.c0);
+        step = size * heads_on * v.head_stride;
+        second = size * (p.c1 - p.c0);
+        base = v.data;
+        bytes = size * ((a.tokens - 1) * v.token_stride + (v.heads - 1) * v.head_stride + a.D);
+        status = a.dev_status;
+    }
+    __device__ __forceinline__ void load(Unit<F32>& u)
+    {
+        load8<F32>(at, base, bytes, status, u.a);
+        load8<F32>(at + second, base, bytes, status, u.b);
+    }
+    __device__ __forceinline__ void store(const Unit<F32>& u)
+    {
+        store8<F32>(at, base, bytes, status, u.a);
+        store8<F32>(at + second, base, bytes, status, u.b);
+    }
+};
+// Zeros for the heads of a token without a position.
+template <bool F32>
+__device__ __forceinline__ void zero_heads(Walk<F32> z, int64_t h, int64_t heads_on, int64_t heads)
 {
-    const int64_t at = t * x.token_stride + h * x.head_stride, bytes = extent(x, a, F32 ? 4 : 2);
-    load8<F32>(x.data, at + p.c0, bytes, a.dev_status, u.a);
-    load8<F32>(x.data, at + p.c1, bytes, a.dev_status, u.b);
-}
-template <bool F32, bool INTERLEAVED>
-__device__ __forceinline__ void store_unit(const HeadsView& z, const HeadsArgs& a, int64_t t, int64_t h, const Place& p,
-                                           const Two* v)
-{
-    const int64_t at = t * z.token_stride + h * z.head_stride, bytes = extent(z, a, F32 ? 4 : 2);
-    Unit<F32> u;
-    from_unit<F32, INTERLEAVED>(v, u.a, u.b);
-    store8<F32>(z.data, at + p.c0, bytes, a.dev_status, u.a);
-    store8<F32>(z.data, at + p.c1, bytes, a.dev_status, u.b);
+    const Unit<F32> zero = {};
+    for (; h < heads; h += heads_on, z.at += z.step) z.store(zero);
 }
 
 // A warp takes a token, or a slice of its heads; the values of its next heads are on their way while it works on
-// those before.  (They are read for padding too, and not used.)
+// those before.  (The first ones are read for padding too, and not used.)
 template <bool IN_F32, bool OUT_F32, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const HeadsArgs a)
+__global__ void __launch_bounds__(32 * kWarps, IN_F32 ? 6 : 7) qk_norm_rope_kernel(const HeadsArgs a)
 {
     __shared__ Weights weights;
     const int lane = threadIdx.x & 31;
@@ -303,40 +319,54 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const HeadsAr
     const Place p = place<INTERLEAVED>(a, lane);
     const int together = 32 / a.lanes;
     const int q_steps = static_cast<int>((a.x[0].heads + together - 1) / together);
-    const int steps = q_steps + static_cast<int>((a.x[1].heads + together - 1) / together);
-    auto head = [&](int j) { return (j >= q_steps ? j - q_steps : j) * together + p.slot; };
-    auto on = [&](int j) { return p.in && j < steps && head(j) < a.x[j >= q_steps].heads; };
-    int j = static_cast<int>(item - t * a.slices);
+    const int heads_on = together * a.slices;
+    // the slice's first heads of the queries, and, where those end, of the keys
+    const int slice = static_cast<int>(item - t * a.slices);
+    const int k_first = slice >= q_steps ? slice - q_steps : (a.slices - (q_steps - slice) % a.slices) % a.slices;
     Unit<IN_F32> next = {};
     Two c[4], s[4];
     bool there = false;
     if (t < a.tokens) {
-        if (on(j)) load_unit<IN_F32>(a.x[j >= q_steps], a, t, head(j), p, next);
+        if (p.in && slice * together + p.slot < a.x[0].heads)
+            Walk<IN_F32>(a.x[0], a, t, slice * together + p.slot, heads_on, p).load(next);
         there = load_angles(a, t, p, lane, c, s);
     }
     share_weights<INTERLEAVED>(weights, a);
     if (t >= a.tokens) return;
-    for (; j < steps; j += a.slices) {
-        const int kind = j >= q_steps;
-        Two v[8];
-        to_unit<IN_F32, INTERLEAVED>(next.a, next.b, v);
-        if (on(j + a.slices)) load_unit<IN_F32>(a.x[j + a.slices >= q_steps], a, t, head(j + a.slices), p, next);
-        if (!there || !on(j)) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0;
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const int all = static_cast<int>(a.x[kind].heads), heads = p.in ? all : 0;
+        const int first = (kind ? k_first : slice) * together + p.slot;
+        Walk<OUT_F32> z(a.z[kind], a, t, first, heads_on, p);
+        if (!there) {
+            zero_heads(z, first, heads_on, heads);
+            continue;
         }
-        if (there) {
+        Walk<IN_F32> x(a.x[kind], a, t, first, heads_on, p);
+        if (kind && first < heads) x.load(next);
+        // the whole warp goes on while a head of it is left (the lanes of a head reduce together)
+        int left = all - (first - p.slot);
+        for (int h = first; left > 0; left -= heads_on, h += heads_on) {
+            Two v[8];
+            to_unit<IN_F32, INTERLEAVED>(next.a, next.b, v);
+            if (h + heads_on < heads) {
+                x.at += x.step;
+                x.load(next);
+            }
             float scale;
             const Two r = both(head_norm(v, a, scale));
-            if (on(j)) {
-                Two w[8];
-                unit_weights(weights[kind], p, w);
+            Two w[8];
+            unit_weights(weights[kind], p, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = mul2_rn(mul2_rn(v[i], r), w[i]);
-                if (p.turned) turn<1>(v, c, s);
+            for (int i = 0; i < 8; ++i) v[i] = mul2_rn(mul2_rn(v[i], r), w[i]);
+            if (p.turned) turn<1>(v, c, s);
+            if (h < heads) {
+                Unit<OUT_F32> u;
+                from_unit<OUT_F32, INTERLEAVED>(v, u.a, u.b);
+                z.store(u);
+                z.at += z.step;
             }
         }
-        if (on(j)) store_unit<OUT_F32, INTERLEAVED>(a.z[kind], a, t, head(j), p, v);
     }
 }
 
@@ -352,67 +382,75 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(c
     const int kind = static_cast<int>(blockIdx.x) >= a.q_ctas;
     const int64_t cta = kind ? blockIdx.x - a.q_ctas : blockIdx.x;
     const int64_t warps = (kind ? gridDim.x - a.q_ctas : a.q_ctas) * kWarps;
-    const HeadsView& xv = a.x[kind];
-    const HeadsView& zv = a.z[kind];
     const Place p = place<INTERLEAVED>(a, lane);
     const int together = 32 / a.lanes;
-    const int steps = static_cast<int>((xv.heads + together - 1) / together);
+    const int heads_on = together * a.slices;
+    const int all = static_cast<int>(a.x[kind].heads), heads = p.in ? all : 0;
     Two dw[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[i] = 0;
-    auto on = [&](int j) { return p.in && j < steps && j * together + p.slot < xv.heads; };
-    // a warp's items in order: all steps of a token (or of its slice) before the next one
+    // a warp's items in order: all heads of a token (or of its slice) before the next one
     for (int64_t item = cta * kWarps + warp; item < a.tokens * a.slices; item += warps) {
         const int64_t t = item / a.slices;
-        int j = static_cast<int>(item - t * a.slices);
-        Unit<X_F32> x = {};
-        Unit<Z_F32> z = {};
-        if (on(j)) {
-            load_unit<X_F32>(xv, a, t, j * together + p.slot, p, x);
-            load_unit<Z_F32>(zv, a, t, j * together + p.slot, p, z);
+        const int base = static_cast<int>(item - t * a.slices) * together;
+        int h = base + p.slot;
+        Walk<X_F32> x(a.x[kind], a, t, h, heads_on, p);
+        Walk<Z_F32> z(a.z[kind], a, t, h, heads_on, p);
+        Walk<DX_F32> dx(a.dx[kind], a, t, h, heads_on, p);
+        Unit<X_F32> next_x = {};
+        Unit<Z_F32> next_z = {};
+        if (h < heads) {
+            x.load(next_x);
+            z.load(next_z);
         }
         Two c[4], s[4];
-        const bool there = load_angles(a, t, p, lane, c, s);
-        for (; j < steps; j += a.slices) {
-            const bool now = on(j);
+        if (!load_angles(a, t, p, lane, c, s)) {
+            zero_heads(dx, h, heads_on, heads);
+            continue;
+        }
+        // the whole warp goes on while a head of it is left (the lanes of a head reduce together)
+        for (int left = all - base; left > 0; left -= heads_on, h += heads_on) {
             Two f[8], g[8];
-            to_unit<X_F32, INTERLEAVED>(x.a, x.b, f);
-            to_unit<Z_F32, INTERLEAVED>(z.a, z.b, g);
-            if (on(j + a.slices)) {
-                load_unit<X_F32>(xv, a, t, (j + a.slices) * together + p.slot, p, x);
-                load_unit<Z_F32>(zv, a, t, (j + a.slices) * together + p.slot, p, z);
+            to_unit<X_F32, INTERLEAVED>(next_x.a, next_x.b, f);
+            to_unit<Z_F32, INTERLEAVED>(next_z.a, next_z.b, g);
+            if (h + heads_on < heads) {
+                x.at += x.step;
+                z.at += z.step;
+                x.load(next_x);
+                z.load(next_z);
             }
-            if (!there || !now) {
+            if (h >= heads) {  // a head before, or nothing: no part in the weight's gradient
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = g[i] = 0;
             }
-            if (there) {
-                if (p.turned) turn<-1>(g, c, s);
-                float scale;
-                const float r = head_norm(f, a, scale);
-                Two w[8];
-                unit_weights(weights[kind], p, w);
-                if (!p.in) {
+            if (p.turned) turn<-1>(g, c, s);
+            float scale;
+            const float r = head_norm(f, a, scale);
+            Two w[8];
+            unit_weights(weights[kind], p, w);
+            // with e = r dy: dw += e x, dx = w e - x r^2 mean(w e x)
+            Two sum = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = 0;
-                }
-                Two sum = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[i] = mul2_rn(f[i], both(r));
-                    dw[i] = fma2(g[i], f[i], dw[i]);
-                    g[i] = mul2_rn(g[i], w[i]);
-                    sum = fma2(g[i], f[i], sum);
-                }
-                const float dot = head_sum(f2lo(sum) + f2hi(sum), a.lanes) * a.inv_D;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = mul2_rn(fma2(f[i], both(-dot), g[i]), both(r));
-                if (scale != 1.0f) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = mul2_rn(f[i], both(scale));
-                }
+            for (int i = 0; i < 8; ++i) {
+                g[i] = mul2_rn(g[i], both(r));
+                dw[i] = fma2(g[i], f[i], dw[i]);
+                g[i] = mul2_rn(g[i], w[i]);
+                sum = fma2(g[i], f[i], sum);
             }
-            if (now) store_unit<DX_F32, INTERLEAVED>(a.dx[kind], a, t, j * together + p.slot, p, f);
+            const float dot = head_sum(f2lo(sum) + f2hi(sum), a.lanes) * a.inv_D;
+            const Two back = both(-dot * r * r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = fma2(f[i], back, g[i]);
+            if (scale != 1.0f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = mul2_rn(f[i], both(scale));
+            }
+            if (h < heads) {
+                Unit<DX_F32> u;
+                from_unit<DX_F32, INTERLEAVED>(f, u.a, u.b);
+                dx.store(u);
+                dx.at += dx.step;
+            }
         }
     }
     // over the heads of a warp, then over the warps, in a fixed order
