@@ -889,6 +889,7 @@ struct PrepareArgs {
     int64_t rows, cols, ldg, g_stride;  // of G
     int64_t m, n, pitch;                // of X (G or G^T) and of its FP16 copy
     int batch, transposed;
+    int by_fours;                       // G's rows can be read four values at a time
     int parts;                          // partial sums per matrix
     double* partials;                   // [batch][parts]
     __half* rest;
@@ -904,6 +905,18 @@ __device__ __forceinline__ float element(const PrepareArgs& a, int64_t at, int64
     if (F32) return ldg_checked(static_cast<const float*>(a.g) + at, a.g, bytes, a.dev_status);
     const uint16_t v = ldg_checked(static_cast<const uint16_t*>(a.g) + at, a.g, bytes, a.dev_status);
     return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+// Four of them (by_fours: 16-byte, bf16 8-byte aligned).
+template <bool F32>
+__device__ __forceinline__ float4 four(const PrepareArgs& a, int64_t at, int64_t bytes)
+{
+    if (F32)
+        return ldg_checked(reinterpret_cast<const float4*>(static_cast<const float*>(a.g) + at), a.g, bytes, a.dev_status);
+    const uint2 v = ldg_checked(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.g) + at), a.g, bytes,
+                                a.dev_status);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ double block_sum(double v, double* shared)
@@ -930,16 +943,30 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const PrepareArgs a)
     double sum = 0.0;
     // a warp takes rows (or pieces of 1024 values of them) in turn
     const int64_t pieces = (a.cols + 1023) / 1024;
-    const int warps = kNormThreads / 32;
+    const int warps = kNormThreads / 32, lane = threadIdx.x & 31;
     for (int64_t i = blockIdx.x * warps + (threadIdx.x >> 5); i < a.rows * pieces;
          i += static_cast<int64_t>(gridDim.x) * warps) {
         const int64_t r = i / pieces, c0 = (i - r * pieces) * 1024;
         const int64_t end = c0 + 1024 < a.cols ? c0 + 1024 : a.cols;
         const int64_t base = e * a.g_stride + r * a.ldg;
+        if (a.by_fours) {
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t c = c0 + 4 * (lane + 32 * k);
+                v[k] = c < end ? four<F32>(a, base + c, bytes) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const double x = v[k].x, y = v[k].y, z = v[k].z, w = v[k].w;
+                sum += x * x + y * y + (z * z + w * w);
+            }
+        } else {
 #pragma unroll 8
-        for (int64_t c = c0 + (threadIdx.x & 31); c < end; c += 32) {
-            const double v = element<F32>(a, base + c, bytes);
-            sum += v * v;
+            for (int64_t c = c0 + lane; c < end; c += 32) {
+                const double v = element<F32>(a, base + c, bytes);
+                sum += v * v;
+            }
         }
     }
     sum = block_sum(sum, shared);
@@ -962,7 +989,9 @@ __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs
     const int64_t per = row_pieces * col_pieces;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t have = -1;
-    double scale = 0.0;
+    // the scale as a power of two and the rest of it: no product of a value with either leaves FP32 on the way,
+    // and the result is rounded once
+    float power = 0.0f, factor = 0.0f;
     bool finite = true;
     for (int64_t i = blockIdx.x; i < per * a.batch; i += gridDim.x) {
         const int64_t e = i / per, l = i - e * per;
@@ -975,31 +1004,47 @@ __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs
             sum = block_sum(sum, shared);
             finite = sum < INFINITY;
             const double norm = sqrt(sum) + a.eps;
-            scale = norm > 0.0 ? a.scale / norm : 0.0;
+            const double scale = norm > 0.0 ? a.scale / norm : 0.0;
+            int exponent = 0;
+            const double mantissa = frexp(scale, &exponent);
+            power = ldexpf(1.0f, exponent / 2);
+            factor = static_cast<float>(ldexp(mantissa, exponent - exponent / 2));
             have = e;
             if (!finite && l == 0 && threadIdx.x == 0 && a.dev_status) atomicOr(a.dev_status, 1);  // NONFINITE
         }
         __syncthreads();  // the piece before has left the tile
+        // values that are not there, or of a matrix that is not finite, count as zeros
+        auto scaled = [&](float v, bool there) { return there && finite ? v * power * factor : 0.0f; };
         if (a.transposed) {
-            for (int c = warp; c < 128; c += kNormThreads / 32) {
-                const int64_t r = r0 + lane, cc = c0 + c;
-                float v = 0.0f;
-                if (r < a.m && cc < a.n && finite) {
-                    const double d = element<F32>(a, e * a.g_stride + cc * a.ldg + r, bytes);
-                    v = static_cast<float>(d * scale);
-                }
-                tile[lane][c] = v;
+            const int64_t r = r0 + lane;
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int64_t cc = c0 + warp + 8 * k;
+                v[k] = r < a.m && cc < a.n ? element<F32>(a, e * a.g_stride + cc * a.ldg + r, bytes) : 0.0f;
             }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) tile[lane][warp + 8 * k] = scaled(v[k], true);
+        } else if (a.by_fours) {
+            float4 v[4];
+            const int64_t cc = c0 + 4 * lane;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t r = r0 + warp + 8 * k;
+                v[k] = r < a.m && cc < a.n ? four<F32>(a, e * a.g_stride + r * a.ldg + cc, bytes)
+                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4*>(&tile[warp + 8 * k][4 * lane]) =
+                    make_float4(scaled(v[k].x, true), scaled(v[k].y, true), scaled(v[k].z, true), scaled(v[k].w, true));
         } else {
             for (int r = warp; r < 32; r += kNormThreads / 32)
 #pragma unroll
                 for (int c = lane; c < 128; c += 32) {
-                    float v = 0.0f;
-                    if (r0 + r < a.m && c0 + c < a.n && finite) {
-                        const double d = element<F32>(a, e * a.g_stride + (r0 + r) * a.ldg + c0 + c, bytes);
-                        v = static_cast<float>(d * scale);
-                    }
-                    tile[r][c] = v;
+                    const bool there = r0 + r < a.m && c0 + c < a.n;
+                    tile[r][c] = scaled(there ? element<F32>(a, e * a.g_stride + (r0 + r) * a.ldg + c0 + c, bytes) : 0.0f,
+                                        there);
                 }
         }
         __syncthreads();
@@ -1236,6 +1281,8 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     pa.pitch = z.x_pitch;
     pa.batch = static_cast<int>(g.batch);
     pa.transposed = transposed;
+    const int64_t size = g.f32 ? 4 : 2;
+    pa.by_fours = reinterpret_cast<uintptr_t>(g.g) % (4 * size) == 0 && g.cols % 4 == 0 && g.ldg % 4 == 0 && g.g_stride % 4 == 0;
     pa.parts = z.parts;
     pa.partials = partials;
     pa.rest = rest;
