@@ -1040,6 +1040,88 @@ def run_experts(args):
     return 0 if st == 0 else 1
 
 
+class QKVStep:
+    """One training step of an attention layer's QKV projection through the public binding: the NVFP4 product, the
+    head norms with the position rotation and, from gradients of the rotated heads and of the values, the way
+    back to the data and weight gradients and the weight's Newton-Schulz (Muon) update (synthetic inputs; the
+    attention itself is not part of it)."""
+
+    def __init__(self, wl, device):
+        import torch
+        from nvfp4_bit_quantized_03_b200 import binding as B
+        self.B, self.torch, self.wl = B, torch, wl
+        g = torch.Generator(device=device).manual_seed(wl.seed)
+
+        def randn(*shape, s=1.0):
+            return s * torch.randn(*shape, generator=g, device=device)
+        T, D, Hq, Hk, dim = wl.T, wl.D, wl.heads_q, wl.heads_k, wl.dim
+        self.x = randn(T, D).bfloat16()
+        self.w = randn(wl.O, D, s=0.02).bfloat16()
+        self.dq, self.dk = randn(T, Hq, dim, s=1e-3).bfloat16(), randn(T, Hk, dim, s=1e-3).bfloat16()
+        self.dv = randn(T, Hk, dim, s=1e-3).bfloat16()
+        self.q_weight, self.k_weight = 1 + randn(dim, s=0.1), 1 + randn(dim, s=0.1)
+        self.table = B.rope_table(T, dim, device=device)
+        # two packed sequences
+        self.positions = (torch.arange(T, dtype=torch.int32, device=device) % ((T + 1) // 2)).contiguous()
+        self.mask = B.sign_mask_from_seed(wl.seed)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.events = None
+
+    _timed = ExpertsStep._timed
+
+    def run(self):
+        B, torch, wl, st = self.B, self.torch, self.wl, dict(dev_status=self.dev_status)
+        Hq, Hk = wl.heads_q, wl.heads_k
+        timed, seed = self._timed, wl.seed
+        norm = (self.positions, self.table, self.q_weight, self.k_weight)
+        qkv = timed("fprop", lambda: B.linear_fprop(self.x, self.w, out_dtype=torch.bfloat16, **st))
+        heads = qkv.view(wl.T, Hq + 2 * Hk, wl.dim)
+        xq, xk = heads[:, :Hq], heads[:, Hq:Hq + Hk]
+        q, k = timed("norms", lambda: B.qk_norm_rope(xq, xk, *norm, **st))
+        dqkv = torch.empty_like(heads)
+        dqkv[:, Hq + Hk:] = self.dv
+        _, _, dqw, dkw = timed("norms backward", lambda: B.qk_norm_rope_backward(
+            self.dq, self.dk, xq, xk, *norm, dq_in=dqkv[:, :Hq], dk_in=dqkv[:, Hq:Hq + Hk], **st))
+        dy = dqkv.view(wl.T, wl.O)
+        dx = timed("dgrad", lambda: B.linear_dgrad(dy, self.w, seed, 0, out_dtype=torch.bfloat16, **st))
+        dw = timed("wgrad", lambda: B.linear_wgrad(dy, self.x, self.mask, seed, 0, **st))
+        update = timed("update", lambda: B.orthogonalize(dw, **st))
+        return dict(qkv=qkv, q=q, k=k, dqkv=dqkv, dq_weight=dqw, dk_weight=dkw, dx=dx, dw=dw, update=update)
+
+
+def run_qkv(args):
+    """The QKV projection of the 8B-class layer with its head norms, the way back and the update: one training step,
+    timed as a whole and per operator.  Prints one JSON line (not the benchmark's headline line)."""
+    import torch
+    wl = synth.qkv_layer()
+    step = QKVStep(wl, torch.device("cuda", torch.cuda.current_device()))
+    for _ in range(args.warmup):
+        step.run()
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    for _ in range(args.steps):
+        step.run()
+    e1.record()
+    torch.cuda.synchronize()
+    ms = e0.elapsed_time(e1) / args.steps
+    step.events = []
+    for _ in range(args.steps):
+        step.run()
+    torch.cuda.synchronize()
+    ops = {}
+    for name, start, end in step.events:
+        ops[name] = ops.get(name, 0.0) + start.elapsed_time(end) / args.steps
+    st = int(step.dev_status.item())
+    print(json.dumps({
+        "workload": wl.name, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms,
+        "tflops": wl.gemm_flops / (ms / 1e3) / 1e12, "ms_per_operator": ops,
+        "recipe": "NVFP4 products of the QKV projection, head norms with the position rotation and their gradient, "
+                  "the weight gradient orthogonalised; the attention itself is not part of it",
+        "data": "synthetic", "dev_status": st}), flush=True)
+    return 0 if st == 0 else 1
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -1056,9 +1138,10 @@ def main(argv=None):
                     help="quantizer bandwidth sweep over 2^n-element tensors (one line per point)")
     ap.add_argument("--sweep-min", type=int, default=20)
     ap.add_argument("--sweep-max", type=int, default=30)
-    ap.add_argument("--workload", choices=["mlp12b", "dense8b", "experts"], default="mlp12b",
+    ap.add_argument("--workload", choices=["mlp12b", "dense8b", "experts", "qkv"], default="mlp12b",
                     help="dense8b: the 8B-class layer stack (4 NVFP4 layers + 1 bf16 layer); "
-                         "experts: a mixture-of-experts layer; each on its own JSON line")
+                         "experts: a mixture-of-experts layer; qkv: a QKV projection with head norms, rotation and "
+                         "Muon update; each on its own JSON line")
     ap.add_argument("--experts-small", action="store_true",
                     help="the experts workload at 2048 tokens, 16 experts, 4 per token (profiling)")
     args = ap.parse_args(argv)
@@ -1073,6 +1156,8 @@ def main(argv=None):
         return run_dense8b(args)
     if args.workload == "experts":
         return run_experts(args)
+    if args.workload == "qkv":
+        return run_qkv(args)
     return run_ours(args)
 
 

@@ -163,3 +163,29 @@ def linear_inputs(lin: Linear, seed: int, layer_index: int = 0):
     W = weights((lin.O, lin.I), seed, tensor_id=base + 1)
     dY = gradients((lin.T, lin.O), seed, tensor_id=base + 2)
     return X, W, dY
+
+
+@dataclass(frozen=True)
+class QKVLayer:
+    """The query-key-value projection of an attention layer: T tokens of D features to heads_q + 2 heads_k heads of
+    `dim` values, with head norms and the position rotation behind it."""
+    name: str
+    seed: int
+    T: int
+    D: int
+    heads_q: int
+    heads_k: int
+    dim: int
+
+    @property
+    def O(self) -> int:  # noqa: E743
+        return (self.heads_q + 2 * self.heads_k) * self.dim
+
+    @property
+    def gemm_flops(self) -> int:
+        return 3 * 2 * self.T * self.D * self.O
+
+
+def qkv_layer() -> QKVLayer:
+    """The QKV projection of the 8B-class layer: tokens 16384, 4096 -> 6144 (32 + 8 + 8 heads of 128)."""
+    return QKVLayer("qkv_t16384_d4096_32q_8kv_128", 6, 16384, 4096, 32, 8, 128)
