@@ -601,7 +601,9 @@ constexpr int kNarrowStage = kLeftBytes + kBoxBytes;
 constexpr int kNarrowStages = 6;
 constexpr int kExchange = kBlock * kNarrow * 4; // the sums of a CTA's columns from all parts
 constexpr int kNarrowEpi = 8;                   // epilogue warps, two per lane quarter, half of the columns each
-constexpr int kNarrowThreads = 32 * (2 + kNarrowEpi);
+constexpr int kNarrowGate = 2 + kNarrowEpi;     // the issuer's gate, as in the kernel of the larger tiles
+constexpr int kNarrowThreads = 32 * (kNarrowGate + 1);
+constexpr int kNarrowBar = 2;                   // named barriers from 2: issuer and gate (1 is the epilogue's)
 constexpr int kNarrowSmem = kNarrowStages * kNarrowStage + kExchange + kBarBytes + 1024;
 static_assert(kNarrowSmem <= 232448 && (2 * kNarrowStages + 2) * 8 + 16 <= kBarBytes, "shared memory per CTA");
 
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     // the epilogue's rows and, in groups of 8, columns; what the sums are added to
     const int q = warp & 3, half = warp >= 6 ? 1 : 0;
     const int row = c.row + 32 * q + lane, col0 = c.col + rank * WIDTH + half * (WIDTH / 2);
-    const bool writes = warp >= 2 && row < p.m;
+    const bool writes = warp >= 2 && warp < kNarrowGate && row < p.m;
     uint32_t v[32];  // sums of the lane's row, 32 columns
     const int64_t plane = static_cast<int64_t>(c.e) * p.m;
     const int64_t matrix_values = static_cast<int64_t>(p.batch) * p.m * p.pitch;
@@ -737,12 +739,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA issuer ----------------
-            uint32_t fills = 0;
-            for (int d = first; d < last; ++d, ++fills) {
-                const int stage = static_cast<int>(fills % kNarrowStages);
-                if (!wait_bounded(bar(FULL + stage), fills / kNarrowStages & 1, abort_flag, p.dev_status)) break;
+        // ---------------- MMA issuer ----------------
+        uint32_t fills = 0;
+        for (int d = first; d < last; ++d, ++fills) {
+            const int stage = static_cast<int>(fills % kNarrowStages);
+            named_sync(kNarrowBar + stage, 64);
+            if (lane == 0) {
                 tc_fence_after();
                 const uint32_t at = smem_u32(smem + stage * kNarrowStage);
                 const uint64_t da = desc_sw128(at), db = ACROSS ? desc_across(at + kLeftBytes) : desc_sw128(at + kLeftBytes);
@@ -750,11 +752,23 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 for (int k = 0; k < kDepth / 16; ++k)
                     mma_f16<1>(tmem, da + 2 * k, db + (ACROSS ? 128 : 2) * k, IDESC, fills != 0 || k != 0 ? 1u : 0u);
                 mma_commit<1>(bar(EMPTY + stage));
+                if (d + 1 == last) mma_commit<1>(bar(ACC_FULL));
             }
-            mma_commit<1>(bar(ACC_FULL));  // after an abort too: the tensor memory is freed behind it
-            wait_bounded(bar(ACC_FULL), 0, abort_flag, nullptr, true);
+            __syncwarp();
         }
+        // the tensor memory is freed behind them
+        if (lane == 0) wait_bounded(bar(ACC_FULL), 0, abort_flag, nullptr, true);
         __syncwarp();
+    } else if (warp == kNarrowGate) {
+        bool ok = true;
+        uint32_t fills = 0;
+        for (int d = first; d < last; ++d, ++fills) {
+            const int stage = static_cast<int>(fills % kNarrowStages);
+            if (lane == 0 && ok)
+                ok = wait_bounded(bar(FULL + stage), fills / kNarrowStages & 1, abort_flag, p.dev_status);
+            __syncwarp();
+            named_sync(kNarrowBar + stage, 64);
+        }
     } else {
         // ---------------- sums to the CTAs that write them ----------------
 #pragma unroll
