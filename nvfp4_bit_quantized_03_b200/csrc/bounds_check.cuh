@@ -1,9 +1,9 @@
 // Debug bounds checks of the kernels' global-memory accesses.
 //
 // A library compiled with -DNVFP4_BOUNDS_CHECK (libnvfp4_checked.so) checks every global
-// load and store of the quantizers, the router, the plan and the combination, and every TMA box the
-// GEMM issues, against the extent of its buffer, which the kernel derives from the call's shape.  An access outside it is
-// skipped, and NVFP4_DEVSTAT_BOUNDS is OR-ed into the call's status word: an index mistake
+// load and store of the quantizers, the router, the plan, the combination, the head norms and the
+// orthogonalisation, and every TMA box the products issue, against the extent of its buffer, which the
+// kernel derives from the call's shape.  An access outside it is skipped, and NVFP4_DEVSTAT_BOUNDS is OR-ed into the call's status word: an index mistake
 // shows up as a status bit and a mismatch against the oracle instead of a memory fault.  In
 // the normal build kBoundsCheck is false, every check below is the constant `true`, and the
 // kernels compile to exactly the code they have without this file.

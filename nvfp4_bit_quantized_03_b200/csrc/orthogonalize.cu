@@ -7,15 +7,16 @@
 // Precision.  Every product takes FP16 operands (11 significant bits) with FP32 accumulation; X itself stays
 // in 32 bits between steps, as an FP16 value, which is the products' operand, and the rest to it in FP16 times
 // 2^11: 22 bits and more.  A, B and X are held times powers of two that keep their values inside FP16's
-// normal range: X times S ~ sqrt(columns), A times 2^12, B times 2^10.  The error of the result is then about that of its own rounding to bf16 (emulated in
-// FP64, rms of error over rms of result: 1.2e-3 .. 1.9e-3 against 1.7e-3 for the rounding).  With X
-// itself in FP16 a gradient of low rank is lost (1.5e-1: rounding noise of the directions that are not there
-// is raised like everything else), with bf16 operands the error is 1e-2 and more.
+// normal range: X times S ~ sqrt(columns), A times 2^12, B times 2^10.  The error of the result is then about
+// that of its own rounding to bf16 (emulated in FP64, rms of error over rms of result: 1.2e-3 .. 1.9e-3 against
+// 1.7e-3 for the rounding; measured with it 2.0e-3 .. 2.5e-3).  With X itself in FP16 a gradient of low rank is
+// lost (1.5e-1: rounding noise of the directions that are not there is raised like everything else), with bf16
+// operands the error is 1e-2 and more.
 //
 // Kernels: the sum of squares (FP64), the scaled copies of X, then three products per step, one
 // kernel each, chained by programmatic launches.  (One kernel that stays on the SMs for all steps, its products
-// behind a counter in memory: 512 x 512 145 against 114 us, 4096 x 4096 1.27 against 1.16 ms.  What a launch costs
-// less than the counter is the time of the fences around it.)
+// behind a counter in memory, took 145 against 114 us for 512 x 512 and 1.27 against 1.16 ms for 4096 x 4096: the
+// fences around the counter cost more than a launch.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -237,6 +238,11 @@ __device__ __forceinline__ float2 halves(uint32_t v)
 // Warp 0 loads, warp 1 issues the MMAs behind the gate warp, warps 2..9 turn accumulators into results; two
 // accumulators, so that a tile's results are written while the next one is multiplied.  In a pair
 // (cta_group::2) each CTA holds half of either operand's rows and the accumulator of its 128 rows.
+//   What bounds it (B200): a step of K of a pair's tile takes 0.385 us with all SMs at work, 1.6 PFLOP/s, which is
+// also the rate of cuBLAS's bf16 product on this GPU: the power limit (clocks fall to 1.4 .. 1.6 GHz; the tensor pipe
+// is busy 76 % of those cycles) and the 83 bytes per ns that every SM then reads from L2.  20480 x 5120: gram 370 us,
+// square 101, update 777 (4 KB of X and its rest in and out per row of a tile on top).  Single CTAs are bound by
+// the 124 bytes per ns that an SM can read: 0.27 us for a step of a quarter of that work.
 template <int CG, int OP>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -595,6 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Where larger tiles are too few for the SMs, CTAs take one of 128 x 64 each; or a cluster of 2 or 4 takes one: each
 // CTA sums a part of K, copies to every other CTA of the cluster the sums of that one's columns (bulk copies
 // between shared memories), and writes the results of its own.  The order of the additions is that of the parts.
+//   What bounds it (B200, 512 x 512, clusters of 4): latency.  Of 4.9 us per product 1.3 lie between the kernels, 1.4
+// until the sums of 2 steps of K are there, 1.2 in the exchange, 1.0 in the results.  Tiles of 128 x 128 by clusters
+// exchange twice the sums and took 6.4 us; written straight to the other CTAs' memory by the lanes the sums took
+// 2.2 us instead of 0.6 + 0.6.
 
 constexpr int kNarrow = 64;                     // columns of a tile
 constexpr int kNarrowStage = kLeftBytes + kBoxBytes;
@@ -840,14 +850,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             for (int i = 0; i < 4; ++i) {
                 float2 x = make_float2(p.beta * f[2 * i], p.beta * f[2 * i + 1]);
                 if (OP != kGram) {
-                    float2 a = halves(aw[i]);
+                    float2 to = halves(aw[i]);
                     if (ACROSS) {
                         const float2 s = halves(rw[i]);
-                        a.x += s.x * kRestUnit;
-                        a.y += s.y * kRestUnit;
+                        to.x += s.x * kRestUnit;
+                        to.y += s.y * kRestUnit;
                     }
-                    x.x += p.alpha * a.x;
-                    x.y += p.alpha * a.y;
+                    x.x += p.alpha * to.x;
+                    x.y += p.alpha * to.y;
                 }
                 o[i] = OP == kLast ? pack_bf16(x.x, x.y) : pack_half(x.x, x.y);
                 if (OP == kUpdate) {
@@ -946,7 +956,8 @@ __device__ __forceinline__ double block_sum(double v, double* shared)
     return sum;
 }
 
-// Partial sums of the squares, in FP64: no value of FP32 or bf16 leaves its range when squared.
+// Partial sums of the squares, in FP64: no value of FP32 or bf16 leaves its range when squared.  Bound by HBM: B200,
+// 20480 x 5120 FP32 69 us (6.1 TB/s).
 template <bool F32>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const PrepareArgs a)
 {
@@ -990,7 +1001,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const PrepareArgs a)
 }
 
 // X times the scale over the norm: in FP16 row by row, and the rest to it in the order of the products' epilogue.
-// A CTA takes pieces of 32 rows x 128 columns of X through shared memory (G^T: both sides stay coalesced).
+// A CTA takes pieces of 32 rows x 128 columns of X through shared memory (G^T: both sides stay coalesced), all
+// of a piece's loads in flight.  Bound by HBM and the passes between barriers: B200, 32 of 1408 x 2048 FP32 146 us
+// (5.1 TB/s), 20480 x 5120 (turned) 181 us (4.6 TB/s); with FP64 products and loads one by one 186 and 209.
 template <bool F32>
 __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs a)
 {
@@ -1181,15 +1194,19 @@ cudaError_t resident_on_device(int sm_count, Resident* out)
 }
 
 // How a product is spread over the SMs: tiles of 128 x 128 by single CTAs, of 256 x 256 by pairs, or (parts > 0) a
-// tile of 128 x 64 by a cluster of `parts`.
+// tile of 128 x 64 by a cluster of `parts` (all of which are resident at once).  Chosen by estimated time.  Whole
+// calls with one way for all three products, us (B200; singles / pairs / clusters of 1, 2, 4):
+//   512 x 512     116 / 154 / 100, 91, 81      1024 x 1024   143 / 187 / 141, 153, 291
+//   768 x 3000    184 / 229 / 222, 241, 392    2048 x 2048   270 / 279 / 558, ..
+//   16 of 256 x 512  108 / 133 / 117, ..       2816 x 2816   614 / 451 / 1346, ..
+// and with the choice 81, 124, 151, 248, 102, 440.
 struct Plan {
     int cg, parts;
     int64_t workers;
 };
 Plan plan_of(bool symmetric, int64_t batch, int64_t m, int64_t n, int64_t k, const Resident& r)
 {
-    // us: a step of K (256 x 256 is bound by the tensor cores' power, the others by what an SM can read from
-    // L2), and the rest of a kernel
+    // us: a step of K (see the kernels) and the rest of a kernel
     const int64_t depth = (k + kDepth - 1) / kDepth;
     const int64_t small = batch * tiles_of<128>(symmetric, m, n), large = batch * tiles_of<256>(symmetric, m, n);
     const int64_t narrow = batch * narrow_tiles(symmetric, m, n);

@@ -70,7 +70,8 @@ def test_against_64_bits(rows, cols, dtype):
     assert int(st) == 0
 
 
-@pytest.mark.parametrize("rows,cols", [(2500, 2300), (2304, 4608), (5000, 1900)])
+@pytest.mark.parametrize("rows,cols", [(2500, 2300), (2304, 4608), (5000, 1900), (2303, 2616), (3100, 2312),
+                                       (2300, 2601)])
 def test_sizes_that_take_pairs(rows, cols):
     g = _gradient((rows, cols), seed=1)
     _check(B.orthogonalize(g), g, (rows, cols))
@@ -142,7 +143,8 @@ def test_zeros_and_values_that_are_not_finite():
         assert not B.orthogonalize(torch.zeros(33, 20, device="cuda"), eps=eps).any()
 
 
-@pytest.mark.parametrize("rows,cols", [(96, 160), (160, 96), (75, 131), (131, 75)])
+@pytest.mark.parametrize("rows,cols", [(96, 160), (160, 96), (75, 131), (131, 75), (75, 136), (139, 72), (900, 1000),
+                                       (1200, 1001), (1201, 1000)])
 def test_strides_and_what_lies_around(rows, cols):
     base = _gradient((3, rows, cols))
     want = B.orthogonalize(base)

@@ -1,6 +1,8 @@
 """Host-side checks of the operators around a layer's products that need no GPU: the references against
 differences, sizes, and refusals before any work is queued (C ABI and binding)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -252,3 +254,17 @@ def test_orthogonalize_binding_refusals(monkeypatch):
         monkeypatch.setattr(B, "_queue", lambda *a: None)
         with pytest.raises(TypeError, match="dev_status"):
             B.orthogonalize(g, dev_status=torch.zeros(1))
+
+
+@pytest.mark.parametrize("unit", ["qk_norm.cu", "orthogonalize.cu"])
+def test_units_use_checked_accesses_only(unit):
+    """Their arrays are reached through the checked loads, stores and copies only (read from the sources, since no
+    call of a correct kernel can show a check that is missing)."""
+    text = open(os.path.join(os.path.dirname(B.__file__), "csrc", unit)).read()
+    code = re.sub(r"//[^\n]*", "", text)
+    arrays = "g|x|rest|out|partials|addend|weight|dweight|positions|table|data"
+    assert "__ldg(" not in code and "ld.global.nc" not in code
+    assert not re.findall(rf"\b[ap]\.(?:{arrays})\s*\[(?!kind\]|0\]|1\]|i\])", code)
+    assert not re.findall(rf"\*\s*[ap]\.(?:{arrays})\b(?!\s*\w)", code)
+    assert not re.findall(r"st\.global|atomicAdd", code)
+    assert len(re.findall(r"\bld\.global", code)) == (1 if unit == "orthogonalize.cu" else 0)  # load16, behind its check
