@@ -541,7 +541,7 @@ def _queue(what, stream, *tensors):
             continue
         d = t.get_device()
         if d >= 0 and here < 0:
-            here = torch.cuda.current_device()
+            here = torch._C._cuda_getDevice()
         if d < 0 or d != here:
             raise ValueError(f"{what}: every tensor must be on the current CUDA device, got {t.device}")
     return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
@@ -888,43 +888,61 @@ _pack_heads = struct.Struct("Pqqq").pack
 
 def _heads(what, t, dtype, shape):
     """The nvfp4_heads of a tensor [tokens, heads, dim], as bytes."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     stride = t.stride()
-    if t.shape != shape or stride[2] != 1:
+    if t.dtype is not dtype or t.shape != shape or stride[2] != 1:
+        if t.dtype is not dtype:
+            raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{what} must be {tuple(shape)} with unit stride in a head, got {tuple(t.shape)} strides "
                          f"{stride}")
     return _pack_heads(t.data_ptr(), shape[1], stride[0], stride[1])
 
 
+def _float_or_bf16(what, t):
+    """OUT_F32 or OUT_BF16, the type of t."""
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        return OUT_BF16
+    if dtype is torch.float32:
+        return OUT_F32
+    raise TypeError(f"{what} must be {' or '.join(str(d) for d in _F32_BF16)}, got {dtype}")
+
+
+def _vector(what, t, dtype, n):
+    """Address of a contiguous tensor of n values, None of None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        _dense(what, t, dtype, (n,))
+    return t.data_ptr()
+
+
 def _head_inputs(q, k, positions, table, q_weight, k_weight):
-    """Checks what both directions take; (shape of q, shape of k or None, nvfp4_heads of both, the
-    table's rows and width)."""
-    if q.dtype not in _F32_BF16:
-        raise TypeError(f"q must be {' or '.join(str(d) for d in _F32_BF16)}, got {q.dtype}")
+    """Checks what both directions take; shapes of q and k (or None), the nvfp4_heads of both, the type, the addresses
+    of weights and positions, and the table's address, rows and width."""
+    dtype = _float_or_bf16("q", q)
     shape = q.shape
     if len(shape) != 3:
         raise ValueError(f"q must be [tokens, heads, dim], got {tuple(shape)}")
     T, _, D = shape
-    if positions is not None:
-        _dense("positions", positions, torch.int32, (T,))
-    rows = rotary = 0
+    where = (_vector("q_weight", q_weight, torch.float32, D), _vector("k_weight", k_weight, torch.float32, D),
+             _vector("positions", positions, torch.int32, T))
+    angles = (None, 0, 0)
     if table is not None:
-        rows, rotary = size = table.shape if table.dim() == 2 else (0, 0)
-        _dense("table", table, torch.float32, size)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _dense(name, w, torch.float32, (D,))
+        size = table.shape
+        if table.dtype is not torch.float32 or len(size) != 2 or not table.is_contiguous():
+            _dense("table", table, torch.float32, size if len(size) == 2 else (0, 0))
+        angles = (table.data_ptr(), size[0], size[1])
     if k is None:
-        return shape, None, _heads("q", q, q.dtype, shape), None, rows, rotary
+        return shape, None, _heads("q", q, q.dtype, shape), None, dtype, where, angles
     if k.dim() != 3:
         raise ValueError(f"k must be [tokens, heads, dim], got {tuple(k.shape)}")
     k_shape = (T, k.shape[1], D)
-    return shape, k_shape, _heads("q", q, q.dtype, shape), _heads("k", k, q.dtype, k_shape), rows, rotary
+    return (shape, k_shape, _heads("q", q, q.dtype, shape), _heads("k", k, q.dtype, k_shape), dtype, where,
+            angles)
 
 
-def _head_outputs(names, q_out, k_out, q_shape, k_shape, dtype, device, stream):
-    """Outputs of q's and k's shape (made where they are None) and their nvfp4_heads; both have one type, that
+def _head_outputs(q_name, k_name, q_out, k_out, q_shape, k_shape, dtype, device, stream):
+    """Outputs of q's and k's shape (made where they are None), their nvfp4_heads and type; both have one type, that
     of one that was given or `dtype`."""
     if q_out is None or (k_out is None and k_shape is not None):
         with _allocating(stream):
@@ -932,13 +950,11 @@ def _head_outputs(names, q_out, k_out, q_shape, k_shape, dtype, device, stream):
                 q_out = _poisoned(torch.empty(q_shape, dtype=dtype if k_out is None else k_out.dtype, device=device))
             if k_out is None and k_shape is not None:
                 k_out = _poisoned(torch.empty(k_shape, dtype=q_out.dtype, device=device))
-    dtype = q_out.dtype
-    if dtype not in _F32_BF16:
-        raise TypeError(f"{names[0]} must be {' or '.join(str(d) for d in _F32_BF16)}, got {dtype}")
-    q_heads = _heads(names[0], q_out, dtype, q_shape)
+    code = _float_or_bf16(q_name, q_out)
+    q_heads = _heads(q_name, q_out, q_out.dtype, q_shape)
     if k_shape is None:
-        return q_out, None, q_heads, None
-    return q_out, k_out, q_heads, _heads(names[1], k_out, dtype, k_shape)
+        return q_out, None, q_heads, None, code
+    return q_out, k_out, q_heads, _heads(k_name, k_out, q_out.dtype, k_shape), code
 
 
 def qk_norm_rope(q, k, positions=None, table=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -947,15 +963,15 @@ def qk_norm_rope(q, k, positions=None, table=None, q_weight=None, k_weight=None,
     """nvfp4_qk_norm_rope: every head of q [T, Hq, D] and k [T, Hk, D] (k may be None) normalised, times
     its weight, and rotated by its token's position (table: rope_table; None: no rotation).  The
     outputs' type is that of q_out and k_out when given, else out_dtype."""
-    shape, k_shape, xq, xk, rows, rotary = _head_inputs(q, k, positions, table, q_weight, k_weight)
-    q_out, k_out, zq, zk = _head_outputs(("q_out", "k_out"), q_out, k_out, shape, k_shape, out_dtype, q.device,
-                                         stream)
+    shape, k_shape, xq, xk, x_type, (qw, kw, at), angles = _head_inputs(q, k, positions, table, q_weight,
+                                                                        k_weight)
+    q_out, k_out, zq, zk, z_type = _head_outputs("q_out", "k_out", q_out, k_out, shape, k_shape, out_dtype,
+                                                 q.device, stream)
     queue = _queue("nvfp4_qk_norm_rope", stream, q, k, positions, table, q_weight, k_weight, q_out, k_out,
                    dev_status)
-    _check(lib().nvfp4_qk_norm_rope(
-        xq, xk, _dtype_code(q.dtype), shape[0], shape[2], _address(q_weight), _address(k_weight), eps,
-        _address(positions), _address(table), rows, rotary, 1 if interleaved else 0, zq, zk,
-        _dtype_code(q_out.dtype), _status_word(dev_status), queue), "nvfp4_qk_norm_rope")
+    _check(lib().nvfp4_qk_norm_rope(xq, xk, x_type, shape[0], shape[2], qw, kw, eps, at, *angles,
+                                    1 if interleaved else 0, zq, zk, z_type, _status_word(dev_status), queue),
+           "nvfp4_qk_norm_rope")
     return q_out, k_out
 
 
@@ -964,41 +980,38 @@ def qk_norm_rope_backward(dq, dk, q, k, positions=None, table=None, q_weight=Non
                           dq_weight=None, dk_weight=None, workspace=None, dev_status=None, stream=None):
     """nvfp4_qk_norm_rope_backward: (dq_in, dk_in, dq_weight, dk_weight), the gradients of q, k (before
     the norm) and of the weights (float32 [D], also where a weight is None)."""
-    shape, k_shape, xq, xk, rows, rotary = _head_inputs(q, k, positions, table, q_weight, k_weight)
+    shape, k_shape, xq, xk, x_type, (qw, kw, at), angles = _head_inputs(q, k, positions, table, q_weight,
+                                                                        k_weight)
     if (k is None) != (dk is None):
         raise ValueError("dk must be given with k and only with it")
-    if dq.dtype not in _F32_BF16:
-        raise TypeError(f"dq must be {' or '.join(str(d) for d in _F32_BF16)}, got {dq.dtype}")
+    z_type = _float_or_bf16("dq", dq)
     T, Hq, D = shape
-    Hk = 0 if k is None else k_shape[1]
     zq = _heads("dq", dq, dq.dtype, shape)
     zk = None if k is None else _heads("dk", dk, dq.dtype, k_shape)
-    dq_in, dk_in, gq, gk = _head_outputs(("dq_in", "dk_in"), dq_in, dk_in, shape, k_shape, dx_dtype, q.device,
-                                         stream)
+    dq_in, dk_in, gq, gk, g_type = _head_outputs("dq_in", "dk_in", dq_in, dk_in, shape, k_shape, dx_dtype,
+                                                 q.device, stream)
     L = lib()
-    need = L.nvfp4_qk_norm_rope_workspace_bytes(T, Hq, Hk, D)
+    need = L.nvfp4_qk_norm_rope_workspace_bytes(T, Hq, 0 if k is None else k_shape[1], D)
     if k is None:
         dk_weight = None
-    for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if w is not None:
-            _dense(name, w, torch.float32, (D,))
+    dqw, dkw = _vector("dq_weight", dq_weight, torch.float32, D), _vector("dk_weight", dk_weight, torch.float32, D)
     if workspace is not None:
         _workspace_size(workspace, need)
     queue = _queue("nvfp4_qk_norm_rope_backward", stream, dq, dk, q, k, positions, table, q_weight, k_weight,
                    dq_in, dk_in, dq_weight, dk_weight, workspace, dev_status)
-    if dq_weight is None or dk_weight is None or workspace is None:
+    if dqw is None or dkw is None or workspace is None:
         with _allocating(stream):
-            if dq_weight is None:
+            if dqw is None:
                 dq_weight = _poisoned(_new((D,), torch.float32, q.device))
-            if dk_weight is None and k is not None:
+                dqw = dq_weight.data_ptr()
+            if dkw is None and k is not None:
                 dk_weight = _poisoned(_new((D,), torch.float32, q.device))
+                dkw = dk_weight.data_ptr()
             if workspace is None:
-                workspace = _workspace(need, q.device)
+                workspace = _poisoned(_new((need,), torch.uint8, q.device))
     _check(L.nvfp4_qk_norm_rope_backward(
-        zq, zk, _dtype_code(dq.dtype), xq, xk, _dtype_code(q.dtype), T, D, _address(q_weight),
-        _address(k_weight), eps, _address(positions), _address(table), rows, rotary, 1 if interleaved else 0, gq,
-        gk, _dtype_code(dq_in.dtype), _address(dq_weight), _address(dk_weight), _address(workspace),
-        _status_word(dev_status), queue), "nvfp4_qk_norm_rope_backward")
+        zq, zk, z_type, xq, xk, x_type, T, D, qw, kw, eps, at, *angles, 1 if interleaved else 0, gq, gk, g_type, dqw,
+        dkw, workspace.data_ptr(), _status_word(dev_status), queue), "nvfp4_qk_norm_rope_backward")
     return dq_in, dk_in, dq_weight, dk_weight
 
 
