@@ -425,13 +425,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(c
                 x.load(next_x);
                 z.load(next_z);
             }
-            if (h >= heads) {  // a head before, or nothing: no part in the weight's gradient
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = g[i] = 0;
-            }
             if (p.turned) turn<-1>(g, c, s);
             float scale;
-            const float r = head_norm(f, a, scale);
+            // lanes behind the last head hold zeros or, again, a head of this token before: no part in dw
+            const float root = head_norm(f, a, scale), r = h < heads ? root : 0.0f;
             Two w[8];
             unit_weights(weights[kind], p, w);
             // with e = r dy: dw += e x, dx = w e - x r^2 mean(w e x)
