@@ -7,11 +7,14 @@
 // Precision.  Every product takes FP16 operands (11 significant bits) with FP32 accumulation; X itself stays
 // in 32 bits between steps, as an FP16 value, which is the products' operand, and the rest to it in FP16 times
 // 2^11: 22 bits and more.  A, B and X are held times powers of two that keep their values inside FP16's
-// normal range: X times S ~ sqrt(columns), A times 2^12, B times 2^10.  The error of the result is then about
-// that of its own rounding to bf16 (emulated in FP64, rms of error over rms of result: 1.2e-3 .. 1.9e-3 against
-// 1.7e-3 for the rounding; measured with it 2.0e-3 .. 2.5e-3).  With X itself in FP16 a gradient of low rank is
-// lost (1.5e-1: rounding noise of the directions that are not there is raised like everything else), with bf16
-// operands the error is 1e-2 and more.
+// normal range: X times S ~ sqrt(columns), A times 2^12, B times 2^10.  The diagonals of A and B, which become much
+// larger than the rest of them, stay in FP32 and out of the products: with A = H + D and B = E + F (D, F diagonal)
+//   A^2 = H^2 + H D + D H + D^2,   X <- (a + F) X + E X
+// take one product each of the rest, and elements of A and X by the diagonals in the epilogue.  The error of the
+// result is then below that of its own rounding to bf16 (emulated in FP64, rms of error over rms of result: 1e-4
+// .. 1.0e-3 against 1.7e-3 for the rounding; with the diagonals in FP16 1.2e-3 .. 2.3e-3).  With X itself in FP16 a
+// gradient of low rank is lost (1.5e-1: rounding noise of the directions that are not there is raised like
+// everything else), with bf16 operands the error is 1e-2 and more.
 //
 // Kernels: the sum of squares (FP64), the scaled copies of X, then three products per step, one
 // kernel each, chained by programmatic launches.  (One kernel that stays on the SMs for all steps, its products
@@ -87,7 +90,12 @@ static_assert(kBars * 8 + 16 <= kBarBytes, "barrier area");
 struct ProductArgs {
     int m, n, k;           // rows and columns of the result, length of the products
     int batch;
-    float alpha, beta;     // result = alpha * (A or X) + beta * accumulator
+    // result = alpha * (A or X) + beta * accumulator; with the diagonals, in FP32: A's sum_i and B's d_i,
+    //   square: alpha + gamma (sum_i + sum_j), and d_i = diag_b sum_i + diag_c sum_i^2 + diag_acc accumulator_ii
+    //   update: alpha + gamma d_i
+    float alpha, beta, gamma, diag_b, diag_c, diag_acc;
+    float* sums;           // A's diagonal [batch][m]: written by gram (diag_acc accumulator_ii), read by square
+    float* diagonal;       // B's diagonal [batch][m]: written by square, read by update
     const __half* addend;  // square: A; update: X [batch][m][pitch]
     int64_t pitch;
     __half* rest;          // update: X's rest, blocks of 128 x 128 in the order of the epilogue's lanes
@@ -229,6 +237,32 @@ __device__ __forceinline__ void load16(const __half* src, const void* base, int6
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "l"(src));
+}
+// Value k (0 .. N - 1) of v, which becomes 0; 0 for another k.
+template <int N>
+__device__ __forceinline__ float take(uint32_t* v, int k)
+{
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        r = i == k ? v[i] : r;
+        v[i] = i == k ? 0u : v[i];
+    }
+    return __uint_as_float(r);
+}
+// A diagonal's value of row `row` of matrix e.
+__device__ __forceinline__ float diagonal_at(const float* d, const ProductArgs& p, int64_t e, int row)
+{
+    return row < p.m ? ld_checked(d + e * p.m + row, d, 4 * static_cast<int64_t>(p.batch) * p.m, p.dev_status) : 0.0f;
+}
+// Keeps a row's diagonal value of A (gram) or B (square) from its accumulator.
+template <int OP>
+__device__ __forceinline__ void keep_diagonal(const ProductArgs& p, int64_t e, int row, float acc, float sum)
+{
+    if (row >= p.m) return;
+    float* d = OP == kGram ? p.sums : p.diagonal;
+    const float v = OP == kGram ? p.diag_acc * acc : p.diag_b * sum + (p.diag_c * sum * sum + p.diag_acc * acc);
+    st_checked(d + e * p.m + row, v, d, 4 * static_cast<int64_t>(p.batch) * p.m, p.dev_status);
 }
 __device__ __forceinline__ float2 halves(uint32_t v)
 {
@@ -454,6 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             fetch(c0);  // on its way while the products are summed
+            // A's or B's diagonal in the lane's row, and with it the factor of what is added
+            const float own = OP == kGram ? 0.0f : diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
+            const float factor = p.alpha + p.gamma * own;
             bool ready = lane == 0 ? wait_bounded(bar(kAccFull + buf), (it >> 1) & 1, abort_flag, p.dev_status) : false;
             ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
             if (!ready) break;
@@ -477,19 +514,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     uint32_t v[32];
                     accumulator(2 * w + h, v);
+                    if (SYMMETRIC && r0 == col + 32 * h)  // the diagonal's block
+                        keep_diagonal<OP>(p, c.e, row, take<32>(v, lane), own);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int i = 16 * h + j;
                         float2 f = make_float2(p.beta * __uint_as_float(v[2 * j]), p.beta * __uint_as_float(v[2 * j + 1]));
                         if (OP != kGram) {
-                            float2 x = halves(add[i]);
+                            float2 x = halves(add[i]), by = make_float2(factor, factor);
+                            if (OP == kSquare) {  // H D + D H
+                                const int cj = col + 2 * i;
+                                by.x += p.gamma * diagonal_at(p.sums, p, c.e, cj);
+                                by.y += p.gamma * diagonal_at(p.sums, p, c.e, cj + 1);
+                            }
                             if (ACROSS) {
                                 const float2 r = halves(rest[i]);
                                 x.x += r.x * kRestUnit;
                                 x.y += r.y * kRestUnit;
                             }
-                            f.x += p.alpha * x.x;
-                            f.y += p.alpha * x.y;
+                            f.x += by.x * x.x;
+                            f.y += by.y * x.y;
                         }
                         packed[i] = OP == kLast ? pack_bf16(f.x, f.y) : pack_half(f.x, f.y);
                         if (OP == kUpdate) {
@@ -716,6 +760,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const int row = c.row + 32 * q + lane, col0 = c.col + rank * WIDTH + half * (WIDTH / 2);
     const bool writes = warp >= 2 && warp < kNarrowGate && row < p.m;
     uint32_t v[32];  // sums of the lane's row, 32 columns
+    float own = 0.0f;  // A's or B's diagonal in it
     const int64_t plane = static_cast<int64_t>(c.e) * p.m;
     const int64_t matrix_values = static_cast<int64_t>(p.batch) * p.m * p.pitch;
     uint4 add[GROUPS], rest[GROUPS];
@@ -795,6 +840,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 rest[g] = ld_checked(rest_at + 32 * g, p.rest, rest_bytes, p.dev_status);
             }
         }
+        if (OP != kGram) own = diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
         bool ready = lane == 0 ? wait_bounded(bar(ACC_FULL), 0, abort_flag, p.dev_status) : false;
         ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
         if (ready) {
@@ -843,6 +889,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                     f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
                 }
             }
+            if (SYMMETRIC && row >= col && row < col + 8) {  // the diagonal
+                uint32_t bits[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bits[i] = __float_as_uint(f[i]);
+                keep_diagonal<OP>(p, c.e, row, take<8>(bits, row - col), own);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(bits[i]);
+            }
+            const float factor = p.alpha + p.gamma * own;
             const uint32_t aw[4] = {add[g].x, add[g].y, add[g].z, add[g].w};
             const uint32_t rw[4] = {rest[g].x, rest[g].y, rest[g].z, rest[g].w};
             uint32_t o[4], r[4];
@@ -850,14 +905,18 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             for (int i = 0; i < 4; ++i) {
                 float2 x = make_float2(p.beta * f[2 * i], p.beta * f[2 * i + 1]);
                 if (OP != kGram) {
-                    float2 to = halves(aw[i]);
+                    float2 to = halves(aw[i]), by = make_float2(factor, factor);
+                    if (OP == kSquare) {  // H D + D H
+                        by.x += p.gamma * diagonal_at(p.sums, p, c.e, col + 2 * i);
+                        by.y += p.gamma * diagonal_at(p.sums, p, c.e, col + 2 * i + 1);
+                    }
                     if (ACROSS) {
                         const float2 s = halves(rw[i]);
                         to.x += s.x * kRestUnit;
                         to.y += s.y * kRestUnit;
                     }
-                    x.x += p.alpha * to.x;
-                    x.y += p.alpha * to.y;
+                    x.x += by.x * to.x;
+                    x.y += by.y * to.y;
                 }
                 o[i] = OP == kLast ? pack_bf16(x.x, x.y) : pack_half(x.x, x.y);
                 if (OP == kUpdate) {
@@ -1251,7 +1310,7 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t 
 struct Sizes {
     int64_t m, n, x_pitch, a_pitch, rest_rows, rest_cols;
     int parts;
-    size_t partials, rest, x, a;  // bytes
+    size_t partials, rest, x, a, diagonal;  // bytes
 };
 
 Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
@@ -1271,6 +1330,7 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
     s.rest = round256(2 * static_cast<size_t>(kRestBlock) * batch * s.rest_rows * s.rest_cols);
     s.x = round256(2 * static_cast<size_t>(batch) * s.m * s.x_pitch);
     s.a = round256(2 * static_cast<size_t>(batch) * s.m * s.a_pitch);
+    s.diagonal = round256(4 * static_cast<size_t>(batch) * s.m);
     return s;
 }
 
@@ -1279,7 +1339,7 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
 size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols)
 {
     const Sizes s = sizes_of(batch, rows, cols);
-    return 256 + s.partials + s.rest + 2 * s.x + 2 * s.a;
+    return 256 + s.partials + s.rest + 2 * s.x + 2 * s.a + 2 * s.diagonal;
 }
 
 cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaStream_t s)
@@ -1298,6 +1358,8 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     x[1] = reinterpret_cast<__half*>(at += z.x);
     __half* a = reinterpret_cast<__half*>(at += z.x);
     __half* b = reinterpret_cast<__half*>(at += z.a);
+    float* sums = reinterpret_cast<float*>(at += z.a);
+    float* diagonal = reinterpret_cast<float*>(at += z.diagonal);
 
     // X times S: values of about 1 where the rows of X are orthonormal
     const double S = std::ldexp(1.0, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(z.n)))));
@@ -1365,6 +1427,8 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
 
     ProductArgs p = {};
     p.batch = static_cast<int>(g.batch);
+    p.sums = sums;
+    p.diagonal = diagonal;
     p.rest = rest;
     p.rest_rows = pa.rest_rows;
     p.rest_cols = pa.rest_cols;
@@ -1373,13 +1437,14 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     p.dev_status = g.dev_status;
     auto product = [&](int op, int64_t n, int64_t k, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md,
                        const CUtensorMap& mt, const __half* addend, int64_t pitch, __half* out, double alpha,
-                       double beta) {
+                       double gamma, double beta) {
         p.m = static_cast<int>(z.m);
         p.n = static_cast<int>(n);
         p.k = static_cast<int>(k);
         p.addend = addend;
         p.pitch = pitch;
         p.alpha = static_cast<float>(alpha);
+        p.gamma = static_cast<float>(gamma);
         p.beta = static_cast<float>(beta);
         p.out = op == kLast ? static_cast<uint16_t*>(g.out) : reinterpret_cast<uint16_t*>(out);
         p.ldo = op == kLast ? g.ldo : (op == kUpdate ? z.x_pitch : z.a_pitch);
@@ -1396,15 +1461,22 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     for (int i = 0; i < g.steps; ++i) {
         const double ca = g.coefficients[3 * i], cb = g.coefficients[3 * i + 1], cc = g.coefficients[3 * i + 2];
         const bool last = i + 1 == g.steps;
-        e = product(kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0,
+        // A = X X^T from the products of S X
+        p.diag_acc = static_cast<float>(1.0 / (S * S));
+        e = product(kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0, 0.0,
                     kScaleA / (S * S));
         if (e != cudaSuccess) return e;
+        // B = b A + c A^2 with A = H + D
+        p.diag_b = static_cast<float>(cb);
+        p.diag_c = static_cast<float>(cc);
+        p.diag_acc = static_cast<float>(cc / kScaleA / kScaleA);
         e = product(kSquare, z.m, z.m, a_left, a_right, b_store, b_turn, a, z.a_pitch, b, cb * kScaleB / kScaleA,
-                    cc * kScaleB / kScaleA / kScaleA);
+                    cc * kScaleB / kScaleA, cc * kScaleB / kScaleA / kScaleA);
         if (e != cudaSuccess) return e;
+        // X <- (a + F) X + E X with B = E + F
         const double unit = last ? 1.0 / S : 1.0;
         e = product(last ? kLast : kUpdate, z.n, z.m, b_left, x_right[now], last ? out_store : x_store[now ^ 1],
-                    last ? out_store : a_turn, x[now], z.x_pitch, x[now ^ 1], ca * unit, unit / kScaleB);
+                    last ? out_store : a_turn, x[now], z.x_pitch, x[now ^ 1], ca * unit, unit, unit / kScaleB);
         if (e != cudaSuccess) return e;
         now ^= 1;
     }

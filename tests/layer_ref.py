@@ -89,8 +89,9 @@ def orthogonalize(g, steps=5, coefficients=MUON, eps=1e-7):
 
 
 def orthogonalize_rounded(g, steps=5, coefficients=MUON, eps=1e-7, seed=0):
-    """The same with every operand of a product (values that the kernels round to FP16, 11 significant bits)
-    moved up or down, at random, by the most that rounding can: half a step, 2^-11 relative."""
+    """The same with every operand of a product (values that the kernels round to FP16, 11 significant bits: X's copy,
+    A and B without their diagonals) moved up or down, at random, by the most that rounding can: half a step,
+    2^-11 relative."""
     gen = torch.Generator(device=g.device).manual_seed(seed)
 
     def off(t):
@@ -103,9 +104,14 @@ def orthogonalize_rounded(g, steps=5, coefficients=MUON, eps=1e-7, seed=0):
     x = g.double()
     x = x.mT if x.shape[-2] > x.shape[-1] else x
     x = x / (x.square().sum((-2, -1), keepdim=True).sqrt() + eps)
+
+    def apart(t):  # the diagonal stays as it is
+        d = torch.diag_embed(t.diagonal(dim1=-2, dim2=-1))
+        return d, off_symmetric(t - d)
     for i in range(steps):
         a, b, c = coefficients[i] if hasattr(coefficients[0], "__len__") else coefficients
         copy = off(x)
-        gram = off_symmetric(copy @ copy.mT)
-        x = a * x + off_symmetric(b * gram + c * gram @ gram) @ copy
+        d, h = apart(copy @ copy.mT)
+        f, e = apart(b * (d + h) + c * (d + h) @ (d + h))
+        x = a * x + f @ x + e @ copy
     return x.mT if g.shape[-2] > g.shape[-1] else x
