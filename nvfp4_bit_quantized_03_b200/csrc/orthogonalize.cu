@@ -94,8 +94,9 @@ struct ProductArgs {
     //   square: alpha + gamma (sum_i + sum_j), and d_i = diag_b sum_i + diag_c sum_i^2 + diag_acc accumulator_ii
     //   update: alpha + gamma d_i
     float alpha, beta, gamma, diag_b, diag_c, diag_acc;
-    float* sums;           // A's diagonal [batch][m]: written by gram (diag_acc accumulator_ii), read by square
-    float* diagonal;       // B's diagonal [batch][m]: written by square, read by update
+    float* sums;           // A's diagonal [batch][fours]: written by gram (diag_acc accumulator_ii), read by square
+    float* diagonal;       // B's diagonal [batch][fours]: written by square, read by update
+    int fours;             // m, rounded up to a multiple of 4
     const __half* addend;  // square: A; update: X [batch][m][pitch]
     int64_t pitch;
     __half* rest;          // update: X's rest, blocks of 128 x 128 in the order of the epilogue's lanes
@@ -253,7 +254,15 @@ __device__ __forceinline__ float take(uint32_t* v, int k)
 // A diagonal's value of row `row` of matrix e.
 __device__ __forceinline__ float diagonal_at(const float* d, const ProductArgs& p, int64_t e, int row)
 {
-    return row < p.m ? ld_checked(d + e * p.m + row, d, 4 * static_cast<int64_t>(p.batch) * p.m, p.dev_status) : 0.0f;
+    return row < p.m ? ld_checked(d + e * p.fours + row, d, 4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status)
+                     : 0.0f;
+}
+// Four of them, from row `row`, a multiple of 4 (rows behind m hold anything: nothing of them is kept).
+__device__ __forceinline__ float4 diagonal_four(const float* d, const ProductArgs& p, int64_t e, int row)
+{
+    if (row >= p.fours) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return ld_checked(reinterpret_cast<const float4*>(d + e * p.fours + row), d,
+                      4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status);
 }
 // Keeps a row's diagonal value of A (gram) or B (square) from its accumulator.
 template <int OP>
@@ -262,7 +271,7 @@ __device__ __forceinline__ void keep_diagonal(const ProductArgs& p, int64_t e, i
     if (row >= p.m) return;
     float* d = OP == kGram ? p.sums : p.diagonal;
     const float v = OP == kGram ? p.diag_acc * acc : p.diag_b * sum + (p.diag_c * sum * sum + p.diag_acc * acc);
-    st_checked(d + e * p.m + row, v, d, 4 * static_cast<int64_t>(p.batch) * p.m, p.dev_status);
+    st_checked(d + e * p.fours + row, v, d, 4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status);
 }
 __device__ __forceinline__ float2 halves(uint32_t v)
 {
@@ -516,16 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     accumulator(2 * w + h, v);
                     if (SYMMETRIC && r0 == col + 32 * h)  // the diagonal's block
                         keep_diagonal<OP>(p, c.e, row, take<32>(v, lane), own);
+                    float4 across = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // A's diagonal in four columns
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int i = 16 * h + j;
+                        if (OP == kSquare && j % 2 == 0) across = diagonal_four(p.sums, p, c.e, col + 2 * i);
                         float2 f = make_float2(p.beta * __uint_as_float(v[2 * j]), p.beta * __uint_as_float(v[2 * j + 1]));
                         if (OP != kGram) {
                             float2 x = halves(add[i]), by = make_float2(factor, factor);
                             if (OP == kSquare) {  // H D + D H
-                                const int cj = col + 2 * i;
-                                by.x += p.gamma * diagonal_at(p.sums, p, c.e, cj);
-                                by.y += p.gamma * diagonal_at(p.sums, p, c.e, cj + 1);
+                                by.x += p.gamma * (j % 2 ? across.z : across.x);
+                                by.y += p.gamma * (j % 2 ? across.w : across.y);
                             }
                             if (ACROSS) {
                                 const float2 r = halves(rest[i]);
@@ -901,14 +911,16 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             const uint32_t aw[4] = {add[g].x, add[g].y, add[g].z, add[g].w};
             const uint32_t rw[4] = {rest[g].x, rest[g].y, rest[g].z, rest[g].w};
             uint32_t o[4], r[4];
+            float4 across = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // A's diagonal in four columns
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float2 x = make_float2(p.beta * f[2 * i], p.beta * f[2 * i + 1]);
                 if (OP != kGram) {
                     float2 to = halves(aw[i]), by = make_float2(factor, factor);
                     if (OP == kSquare) {  // H D + D H
-                        by.x += p.gamma * diagonal_at(p.sums, p, c.e, col + 2 * i);
-                        by.y += p.gamma * diagonal_at(p.sums, p, c.e, col + 2 * i + 1);
+                        if (i % 2 == 0) across = diagonal_four(p.sums, p, c.e, col + 2 * i);
+                        by.x += p.gamma * (i % 2 ? across.z : across.x);
+                        by.y += p.gamma * (i % 2 ? across.w : across.y);
                     }
                     if (ACROSS) {
                         const float2 s = halves(rw[i]);
@@ -1330,7 +1342,7 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
     s.rest = round256(2 * static_cast<size_t>(kRestBlock) * batch * s.rest_rows * s.rest_cols);
     s.x = round256(2 * static_cast<size_t>(batch) * s.m * s.x_pitch);
     s.a = round256(2 * static_cast<size_t>(batch) * s.m * s.a_pitch);
-    s.diagonal = round256(4 * static_cast<size_t>(batch) * s.m);
+    s.diagonal = round256(4 * static_cast<size_t>(batch) * ((s.m + 3) / 4 * 4));
     return s;
 }
 
@@ -1429,6 +1441,7 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     p.batch = static_cast<int>(g.batch);
     p.sums = sums;
     p.diagonal = diagonal;
+    p.fours = static_cast<int>((z.m + 3) / 4 * 4);
     p.rest = rest;
     p.rest_rows = pa.rest_rows;
     p.rest_cols = pa.rest_cols;

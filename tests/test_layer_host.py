@@ -192,7 +192,7 @@ def test_orthogonalize_workspace_sizes():
         m, n = sorted((rows, cols))
         pad = -(-m // 128) * -(-n // 128) * 128 * 128
         need = batch * (2 * pad + 2 * 2 * m * n + 2 * 2 * m * m + 2 * 4 * m)
-        assert need <= f(batch, rows, cols) <= need + batch * (2 * 2 * 63 * m + 2 * 2 * 63 * m + 8 * 592) + 9 * 256
+        assert need <= f(batch, rows, cols) <= need + batch * (2 * 2 * 63 * m + 2 * 2 * 63 * m + 8 * 592 + 2 * 4 * 3) + 9 * 256
     for bad in ((0, 4, 4), (65536, 4, 4), (1, 0, 4), (1, 4, 0), (1, (1 << 18) + 1, 4), (1, 4, (1 << 18) + 1),
                 (2, 1 << 18, 1 << 18), (-1, 4, 4)):
         assert f(*bad) == 0
