@@ -1,5 +1,6 @@
 """NVFP4 training hot path on B200 (sm_100a): quantizers and block-scaled FP4 GEMMs for the
-three GEMMs of a linear layer or of a layer of experts, behind the C ABI of libnvfp4.so
+three GEMMs of a linear layer or of a layer of experts, head norms with the position rotation behind
+a QKV projection, and the Newton-Schulz update of weight gradients, behind the C ABI of libnvfp4.so
 (include/nvfp4.h).
 
 The Python surface is the ctypes binding in ``binding``; it loads the in-tree
