@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kBoundsCheck && !(gemm::tma_box_start_ok(d * kDepth, ya, 2, p.dev_status) &&
                                       gemm::tma_box_start_ok(yb, d * kDepth, 2, p.dev_status) &&
                                       c.e < p.batch)) {
+                    record_bounds_error(p.dev_status);
                     *abort_flag = 1;
                     ok = false;
                     break;

@@ -1,5 +1,9 @@
 """GPU parity of the Newton-Schulz orthogonalisation against the steps in 64 bits; every test through
 both libraries."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -10,6 +14,8 @@ nv = pytest.importorskip("nvfp4_bit_quantized_03_b200")
 B = nv.binding
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(params=["release", "checked"], autouse=True)
@@ -226,3 +232,36 @@ def test_two_calls_at_once():
         got = B.orthogonalize(a, stream=streams[0]), B.orthogonalize(b, stream=streams[1])
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    code = """
+import torch
+from nvfp4_bit_quantized_03_b200 import binding as B
+for shape in ((300, 200), (2304, 2304)):
+    g = torch.randn(shape, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = B.orthogonalize(g)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, B.orthogonalize(g))
+    del graph
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=300)
+
+
+def test_gradients_with_an_exact_answer():
+    """A permutation times a power of two: every step maps its singular values to one number."""
+    n = 256
+    g = torch.zeros(n, n, device="cuda")
+    g[torch.arange(n), torch.randperm(n, device="cuda")] = 0.25
+    s = 1 / n ** 0.5
+    for a, b, c in [R.MUON] * 5:
+        s = a * s + b * s ** 3 + c * s ** 5
+    out = B.orthogonalize(g, eps=0.0)
+    assert torch.equal(out != 0, g != 0)
+    # A and B are diagonal, so all that moves a value is in 32 bits or X's 22.  2^-22 at each factor of the
+    # terms b s^3 and c s^5, carried on by each step's slope s p'(s) / p(s), adds up to 69 * 2^-22 < 2^-12
+    # over the five steps.  The answer is rounded to bf16: half a step is 2^-8.
+    assert ((out[g != 0].double() - s).abs() <= (2.0 ** -8 + 2.0 ** -12) * s).all()
