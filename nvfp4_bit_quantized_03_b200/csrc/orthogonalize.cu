@@ -1272,18 +1272,24 @@ cudaError_t resident_on_device(int sm_count, Resident* out)
 //   768 x 3000    184 / 229 / 222, 241, 392    2048 x 2048   270 / 279 / 558, ..
 //   16 of 256 x 512  108 / 133 / 117, ..       2816 x 2816   614 / 451 / 1346, ..
 // and with the choice 81, 124, 151, 248, 102, 440.
+// Over 46 sizes from 128 x 512 to 2688 x 4096, in batches of 1 to 64, no other way for one of the products was more
+// than 4 % faster than the choice (1536 x 4096: updates by pairs 331, by singles 350; 16 of 768 x 2048: gram by pairs 569, by
+// singles 599).
 struct Plan {
     int cg, parts;
     int64_t workers;
 };
 Plan plan_of(bool symmetric, int64_t batch, int64_t m, int64_t n, int64_t k, const Resident& r)
 {
-    // us: a step of K (see the kernels) and the rest of a kernel
+    // us: a step of K (see the kernels), what a wave of single tiles adds, and the rest of a kernel.  A pair's tile takes
+    // at least its results' 5 us, which lie under the next one's products
     const int64_t depth = (k + kDepth - 1) / kDepth;
     const int64_t small = batch * tiles_of<128>(symmetric, m, n), large = batch * tiles_of<256>(symmetric, m, n);
     const int64_t narrow = batch * narrow_tiles(symmetric, m, n);
-    const double single = static_cast<double>((small + r.singles - 1) / r.singles * depth) * 0.27 + 5.0;
-    const double pair = static_cast<double>((large + r.pairs - 1) / r.pairs * depth) * 0.385 + 6.4;
+    const double single = static_cast<double>((small + r.singles - 1) / r.singles) *
+                              (static_cast<double>(depth) * 0.27 + 1.0) + 4.0;
+    const double tile = static_cast<double>(depth) * 0.385;
+    const double pair = static_cast<double>((large + r.pairs - 1) / r.pairs - 1) * (tile > 5.0 ? tile : 5.0) + tile + 6.4;
     Plan best = pair <= single ? Plan{2, 0, large < r.pairs ? large : r.pairs}
                                : Plan{1, 0, small < r.singles ? small : r.singles};
     double time = pair <= single ? pair : single;
