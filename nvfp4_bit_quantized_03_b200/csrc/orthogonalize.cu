@@ -467,13 +467,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r0 = c.row + rank * kBlock + 32 * q;  // the warp's rows (one per lane)
             const int row = r0 + lane;
             const int c0 = c.col + half * SLICE;            // its columns
-            // what the accumulator is added to, 64 columns at a time: A or X of the lane's row, and X's rest
+            // what the accumulator is added to, 32 columns (half h of 64) at a time: A or X of the lane's row, and X's rest
             uint32_t add[OP == kGram ? 1 : 32], rest[ACROSS ? 32 : 1];
-            __half* rest_at = nullptr;
-            auto fetch = [&](int col) {
+            auto rest_at = [&](int col) -> __half* {
+                const int br = r0 / kBlock, bc = col / kBlock;
+                if (br >= p.rest_rows || bc >= p.rest_cols) return nullptr;
+                return p.rest + ((static_cast<int64_t>(c.e) * p.rest_rows + br) * p.rest_cols + bc) * kRestBlock +
+                       ((q * 16 + (col % kBlock) / 8) * 32 + lane) * 8;
+            };
+            auto fetch = [&](int col, int h) {
                 if (OP != kGram) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
+                    for (int g = 2 * h; g < 2 * h + 2; ++g) {
                         if (row < p.m && col + 16 * g < p.pitch)
                             load16(p.addend + (static_cast<int64_t>(c.e) * p.m + row) * p.pitch + col + 16 * g, p.addend,
                                    addend_bytes, p.dev_status, add + 8 * g);
@@ -483,21 +488,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (ACROSS) {
-                    const int br = r0 / kBlock, bc = col / kBlock;
-                    rest_at = nullptr;
-                    if (br < p.rest_rows && bc < p.rest_cols)
-                        rest_at = p.rest + ((static_cast<int64_t>(c.e) * p.rest_rows + br) * p.rest_cols + bc) * kRestBlock +
-                                  ((q * 16 + (col % kBlock) / 8) * 32 + lane) * 8;
+                    const __half* const at = rest_at(col);
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
+                    for (int g = 4 * h; g < 4 * h + 4; ++g) {
                         uint4 v = make_uint4(0, 0, 0, 0);
-                        if (rest_at)
-                            v = ld_checked(reinterpret_cast<const uint4*>(rest_at) + 32 * g, p.rest, rest_bytes, p.dev_status);
+                        if (at)
+                            v = ld_checked(reinterpret_cast<const uint4*>(at) + 32 * g, p.rest, rest_bytes, p.dev_status);
                         rest[4 * g] = v.x; rest[4 * g + 1] = v.y; rest[4 * g + 2] = v.z; rest[4 * g + 3] = v.w;
                     }
                 }
             };
-            fetch(c0);  // on its way while the products are summed
+            fetch(c0, 0);  // on its way while the products are summed
+            fetch(c0, 1);
             // A's or B's diagonal in the lane's row, and with it the factor of what is added
             const float own = OP == kGram ? 0.0f : diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
             const float factor = p.alpha + p.gamma * own;
@@ -519,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < SLICE / 64; ++w) {
                 const int col = c0 + 64 * w;
                 uint32_t packed[32];
-                __half* const rest_out = rest_at;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t v[32];
@@ -552,15 +553,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             rest[i] = pack_half((f.x - o.x) * (1.0f / kRestUnit), (f.y - o.y) * (1.0f / kRestUnit));
                         }
                     }
-                }
-                if (OP == kUpdate && rest_out) {
+                    if (OP == kUpdate) {
+                        __half* const at = rest_at(col);
 #pragma unroll
-                    for (int g = 0; g < 8; ++g)
-                        st_checked(reinterpret_cast<uint4*>(rest_out) + 32 * g,
-                                   make_uint4(rest[4 * g], rest[4 * g + 1], rest[4 * g + 2], rest[4 * g + 3]), p.rest,
-                                   rest_bytes, p.dev_status);
+                        for (int g = 4 * h; at && g < 4 * h + 4; ++g)
+                            st_checked(reinterpret_cast<uint4*>(at) + 32 * g,
+                                       make_uint4(rest[4 * g], rest[4 * g + 1], rest[4 * g + 2], rest[4 * g + 3]), p.rest,
+                                       rest_bytes, p.dev_status);
+                    }
+                    if (w + 1 < SLICE / 64) fetch(col + 64, h);  // under the other half's work
                 }
-                if (w + 1 < SLICE / 64) fetch(col + 64);
                 const bool inside = r0 < p.m && col < p.n;
                 const bool direct = OP != kLast || !p.transposed;
                 // a symmetric result's other half; a tile on the diagonal holds both
