@@ -1105,7 +1105,8 @@ __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs
             sum = block_sum(sum, shared);
             finite = sum < INFINITY;
             const double norm = sqrt(sum) + a.eps;
-            const double scale = norm > 0.0 ? a.scale / norm : 0.0;
+            // zeros stay zeros, whatever eps: its inverse may leave FP32
+            const double scale = sum > 0.0 ? a.scale / norm : 0.0;
             int exponent = 0;
             const double mantissa = frexp(scale, &exponent);
             power = ldexpf(1.0f, exponent / 2);
