@@ -639,9 +639,9 @@ size_t nvfp4_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t 
  *                 copies, otherwise value by value.  It may be G itself if that is bf16 with the same strides.
  *   workspace   : nvfp4_orthogonalize_workspace_bytes(...) device bytes.
  * Products take FP16 operands (11 significant bits) and FP32 accumulators.  Between steps X is held in two
- * FP16 parts (22 bits), and the diagonals of A and B in FP32, apart from the products: the error is about
- * that of the final rounding to bf16.  A matrix of zeros gives zeros, one with NaN or Inf
- * too (and sets NVFP4_DEVSTAT_NONFINITE).
+ * FP16 parts (22 bits), times a power of two of the matrix's own where |G|_F is below eps, and the diagonals of
+ * A and B in FP32, apart from the products: the error is about that of the final rounding to bf16.  A matrix
+ * of zeros gives zeros, one with NaN or Inf too (and sets NVFP4_DEVSTAT_NONFINITE).
  * Limits: rows, cols <= 2^18, batch <= 65535, batch * rows * cols <= 2^36, 1 <= steps <= 32,
  * 0 <= eps <= 1e30, |coefficients| <= 1e6.
  */

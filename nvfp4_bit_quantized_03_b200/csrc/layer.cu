@@ -109,7 +109,6 @@ nvfp4_status head_args(HeadsArgs& a, const HeadsPair* in, HeadsView* const* view
 constexpr int64_t kMaxSide = 1 << 18;     // FP16 copies times ~ sqrt(side) stay far inside their range
 constexpr int64_t kMaxBatch = 65535;
 constexpr int64_t kMaxValues = int64_t(1) << 36;
-constexpr int kMaxSteps = 32;
 
 bool matrices_ok(int64_t batch, int64_t rows, int64_t cols)
 {
@@ -185,7 +184,7 @@ nvfp4_status nvfp4_orthogonalize(const void* G, int g_dtype, int64_t batch, int6
     if (!G || !coefficients || !out_bf16 || !workspace) return NVFP4_ERR_NULL;
     if (!known_type(g_dtype)) return NVFP4_ERR_ARG;
     if (!matrices_ok(batch, rows, cols)) return NVFP4_ERR_SHAPE;
-    if (steps < 1 || steps > kMaxSteps || !(eps >= 0.0) || !(eps <= 1e30)) return NVFP4_ERR_ARG;
+    if (steps < 1 || steps > kMaxOrthogonalizeSteps || !(eps >= 0.0) || !(eps <= 1e30)) return NVFP4_ERR_ARG;
     for (int i = 0; i < 3 * steps; ++i)
         if (!(std::fabs(coefficients[i]) <= 1e6f)) return NVFP4_ERR_ARG;
     // a single row's or matrix's stride is never used

@@ -245,6 +245,7 @@ cudaError_t launch_qk_norm_rope_backward(HeadsArgs a, bool x_f32, bool z_f32, bo
                                          cudaStream_t s);
 
 // Newton-Schulz orthogonalisation (orthogonalize.cu).
+constexpr int kMaxOrthogonalizeSteps = 32;
 struct OrthogonalizeArgs {
     const void* g;            // batch matrices rows x cols
     bool f32;                 // FP32, otherwise bf16

@@ -16,6 +16,12 @@
 // gradient of low rank is lost (1.5e-1: rounding noise of the directions that are not there is raised like
 // everything else), with bf16 operands the error is 1e-2 and more.
 //
+// Where |G|_F is below eps, X = t G / |G|_F with a t that the steps raise by a factor of about a each.  What is then
+// held is X 2^-l, with an l of the matrix's own before every step, from the bound t prod (|a| + |b| s^2 + |c| s^4) of
+// the singular values, that keeps it at 1 / 2 .. 1 until they get there; and B over a power of two that keeps the larger
+// of b 4^l and c 16^l at 1 / 2 .. 1.  So X keeps its 22 bits however small t is, and a step without a its
+// product's.  (Held as it is, X was off by 1 % at |G|_F = 1e-8 eps and lost from 1e-10 eps on.)
+//
 // Kernels: the sum of squares (FP64), the scaled copies of X, then three products per step, one
 // kernel each, chained by programmatic launches.  (One kernel that stays on the SMs for all steps, its products
 // behind a counter in memory, took 145 against 114 us for 512 x 512 and 1.27 against 1.16 ms for 4096 x 4096: the
@@ -90,10 +96,13 @@ static_assert(kBars * 8 + 16 <= kBarBytes, "barrier area");
 struct ProductArgs {
     int m, n, k;           // rows and columns of the result, length of the products
     int batch;
-    // result = alpha * (A or X) + beta * accumulator; with the diagonals, in FP32: A's sum_i and B's d_i,
-    //   square: alpha + gamma (sum_i + sum_j), and d_i = diag_b sum_i + diag_c sum_i^2 + diag_acc accumulator_ii
-    //   update: alpha + gamma d_i
-    float alpha, beta, gamma, diag_b, diag_c, diag_acc;
+    const float4* factors; // this step's of every matrix, kMaxOrthogonalizeSteps apart
+    // result = alpha * (A or X) + beta * accumulator, with the matrix's factors (a, unit, b, c) and powers of two
+    // `on_x` (the addend) and `on_acc`; with the diagonals, in FP32: A's sum_i and B's d_i,
+    //   gram:   on_acc accumulator; sum_i = diag_acc accumulator_ii
+    //   square: on_x (b + c (sum_i + sum_j)) A + on_acc c accumulator; d_i = b sum_i + c (sum_i^2 + diag_acc accumulator_ii)
+    //   update: on_x (a + unit d_i) X + on_acc unit accumulator
+    float on_x, on_acc, diag_acc;
     float* sums;           // A's diagonal [batch][fours]: written by gram (diag_acc accumulator_ii), read by square
     float* diagonal;       // B's diagonal [batch][fours]: written by square, read by update
     int fours;             // m, rounded up to a multiple of 4
@@ -251,6 +260,31 @@ __device__ __forceinline__ float take(uint32_t* v, int k)
     }
     return __uint_as_float(r);
 }
+// What a product's lane takes its row's values times: the addend (its diagonal's part included), the accumulator, and
+// (square) A's diagonal in the value's column.
+struct Weights {
+    float alpha, beta, gamma;
+    float b, c;  // square: of the diagonal
+};
+template <int OP>
+__device__ __forceinline__ Weights weights_of(const ProductArgs& p, int64_t e, float own)
+{
+    Weights w = {0.0f, p.on_acc, 0.0f, 0.0f, 0.0f};
+    if (OP == kGram) return w;
+    const float4 f = ld_checked(p.factors + e * kMaxOrthogonalizeSteps, p.factors,
+                                16 * ((static_cast<int64_t>(p.batch) - 1) * kMaxOrthogonalizeSteps + 1), p.dev_status);
+    if (OP == kSquare) {
+        w.b = f.z;
+        w.c = f.w;
+        w.gamma = p.on_x * f.w;
+        w.alpha = fmaf(w.gamma, own, p.on_x * f.z);
+        w.beta = p.on_acc * f.w;
+    } else {
+        w.alpha = fmaf(p.on_x * f.y, own, p.on_x * f.x);
+        w.beta = p.on_acc * f.y;
+    }
+    return w;
+}
 // A diagonal's value of row `row` of matrix e.
 __device__ __forceinline__ float diagonal_at(const float* d, const ProductArgs& p, int64_t e, int row)
 {
@@ -266,11 +300,12 @@ __device__ __forceinline__ float4 diagonal_four(const float* d, const ProductArg
 }
 // Keeps a row's diagonal value of A (gram) or B (square) from its accumulator.
 template <int OP>
-__device__ __forceinline__ void keep_diagonal(const ProductArgs& p, int64_t e, int row, float acc, float sum)
+__device__ __forceinline__ void keep_diagonal(const ProductArgs& p, int64_t e, int row, float acc, float sum,
+                                              const Weights& w)
 {
     if (row >= p.m) return;
     float* d = OP == kGram ? p.sums : p.diagonal;
-    const float v = OP == kGram ? p.diag_acc * acc : p.diag_b * sum + (p.diag_c * sum * sum + p.diag_acc * acc);
+    const float v = OP == kGram ? p.diag_acc * acc : fmaf(w.b, sum, fmaf(w.c * sum, sum, w.c * p.diag_acc * acc));
     st_checked(d + e * p.fours + row, v, d, 4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status);
 }
 __device__ __forceinline__ float2 halves(uint32_t v)
@@ -500,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             fetch(c0, 0);  // on its way while the products are summed
             fetch(c0, 1);
-            // A's or B's diagonal in the lane's row, and with it the factor of what is added
+            // A's or B's diagonal in the lane's row, and with it the factors of what is added
             const float own = OP == kGram ? 0.0f : diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
-            const float factor = p.alpha + p.gamma * own;
+            const Weights by_row = weights_of<OP>(p, c.e, own);
             bool ready = lane == 0 ? wait_bounded(bar(kAccFull + buf), (it >> 1) & 1, abort_flag, p.dev_status) : false;
             ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
             if (!ready) break;
@@ -526,18 +561,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     accumulator(2 * w + h, v);
                     if (SYMMETRIC && r0 == col + 32 * h)  // the diagonal's block
-                        keep_diagonal<OP>(p, c.e, row, take<32>(v, lane), own);
+                        keep_diagonal<OP>(p, c.e, row, take<32>(v, lane), own, by_row);
                     float4 across = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // A's diagonal in four columns
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int i = 16 * h + j;
                         if (OP == kSquare && j % 2 == 0) across = diagonal_four(p.sums, p, c.e, col + 2 * i);
-                        float2 f = make_float2(p.beta * __uint_as_float(v[2 * j]), p.beta * __uint_as_float(v[2 * j + 1]));
+                        float2 f = make_float2(by_row.beta * __uint_as_float(v[2 * j]), by_row.beta * __uint_as_float(v[2 * j + 1]));
                         if (OP != kGram) {
-                            float2 x = halves(add[i]), by = make_float2(factor, factor);
+                            float2 x = halves(add[i]), by = make_float2(by_row.alpha, by_row.alpha);
                             if (OP == kSquare) {  // H D + D H
-                                by.x += p.gamma * (j % 2 ? across.z : across.x);
-                                by.y += p.gamma * (j % 2 ? across.w : across.y);
+                                by.x += by_row.gamma * (j % 2 ? across.z : across.x);
+                                by.y += by_row.gamma * (j % 2 ? across.w : across.y);
                             }
                             if (ACROSS) {
                                 const float2 r = halves(rest[i]);
@@ -774,6 +809,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const bool writes = warp >= 2 && warp < kNarrowGate && row < p.m;
     uint32_t v[32];  // sums of the lane's row, 32 columns
     float own = 0.0f;  // A's or B's diagonal in it
+    Weights by_row = {};
     const int64_t plane = static_cast<int64_t>(c.e) * p.m;
     const int64_t matrix_values = static_cast<int64_t>(p.batch) * p.m * p.pitch;
     uint4 add[GROUPS], rest[GROUPS];
@@ -854,6 +890,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             }
         }
         if (OP != kGram) own = diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
+        by_row = weights_of<OP>(p, c.e, own);
         bool ready = lane == 0 ? wait_bounded(bar(ACC_FULL), 0, abort_flag, p.dev_status) : false;
         ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
         if (ready) {
@@ -906,24 +943,23 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 uint32_t bits[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) bits[i] = __float_as_uint(f[i]);
-                keep_diagonal<OP>(p, c.e, row, take<8>(bits, row - col), own);
+                keep_diagonal<OP>(p, c.e, row, take<8>(bits, row - col), own, by_row);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(bits[i]);
             }
-            const float factor = p.alpha + p.gamma * own;
             const uint32_t aw[4] = {add[g].x, add[g].y, add[g].z, add[g].w};
             const uint32_t rw[4] = {rest[g].x, rest[g].y, rest[g].z, rest[g].w};
             uint32_t o[4], r[4];
             float4 across = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // A's diagonal in four columns
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float2 x = make_float2(p.beta * f[2 * i], p.beta * f[2 * i + 1]);
+                float2 x = make_float2(by_row.beta * f[2 * i], by_row.beta * f[2 * i + 1]);
                 if (OP != kGram) {
-                    float2 to = halves(aw[i]), by = make_float2(factor, factor);
+                    float2 to = halves(aw[i]), by = make_float2(by_row.alpha, by_row.alpha);
                     if (OP == kSquare) {  // H D + D H
                         if (i % 2 == 0) across = diagonal_four(p.sums, p, c.e, col + 2 * i);
-                        by.x += p.gamma * (i % 2 ? across.z : across.x);
-                        by.y += p.gamma * (i % 2 ? across.w : across.y);
+                        by.x += by_row.gamma * (i % 2 ? across.z : across.x);
+                        by.y += by_row.gamma * (i % 2 ? across.w : across.y);
                     }
                     if (ACROSS) {
                         const float2 s = halves(rw[i]);
@@ -994,6 +1030,9 @@ struct PrepareArgs {
     int rest_rows, rest_cols;
     __half* x;
     double scale, eps;
+    float4* factors;                    // [batch][kMaxOrthogonalizeSteps]
+    int steps;
+    float coefficients[3 * kMaxOrthogonalizeSteps];
     int* dev_status;
 };
 
@@ -1074,6 +1113,37 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const PrepareArgs a)
                    8 * static_cast<int64_t>(a.batch) * a.parts, a.dev_status);
 }
 
+// The steps' factors (a, unit, b, c) of a matrix whose X starts as X 2^-low with singular values up to t.
+__device__ void write_factors(const PrepareArgs& a, int64_t e, double t, int low)
+{
+    const int64_t bytes = 16 * static_cast<int64_t>(a.batch) * kMaxOrthogonalizeSteps;
+    float4* const factors = a.factors + e * kMaxOrthogonalizeSteps;
+    if (low == 0) {  // as most are
+        const int i = threadIdx.x;
+        if (i < a.steps)
+            st_checked(factors + i, make_float4(a.coefficients[3 * i], 1.0f, a.coefficients[3 * i + 1], a.coefficients[3 * i + 2]),
+                       a.factors, bytes, a.dev_status);
+        return;
+    }
+    if (threadIdx.x != 0) return;
+    double bound = t;
+    for (int i = 0; i < a.steps; ++i) {
+        const double ca = a.coefficients[3 * i], cb = a.coefficients[3 * i + 1], cc = a.coefficients[3 * i + 2];
+        const double square = bound * bound;
+        bound *= fabs(ca) + square * (fabs(cb) + square * fabs(cc));
+        int next = 0;  // X 2^-next behind the step; behind the last one X itself
+        if (low < 0 && i + 1 < a.steps && bound > 0.0 && bound < 0.5) frexp(bound, &next);
+        const double b = ldexp(cb, 2 * low), c = ldexp(cc, 4 * low);
+        int unit = 0;  // B is held times 2^-unit
+        if (low < 0) frexp(fmax(fabs(b), fabs(c)), &unit);
+        st_checked(factors + i,
+                   make_float4(static_cast<float>(ldexp(ca, low - next)), static_cast<float>(ldexp(1.0, unit + low - next)),
+                               static_cast<float>(ldexp(b, -unit)), static_cast<float>(ldexp(c, -unit))),
+                   a.factors, bytes, a.dev_status);
+        low = next;
+    }
+}
+
 // X times the scale over the norm: in FP16 row by row, and the rest to it in the order of the products' epilogue.
 // A CTA takes pieces of 32 rows x 128 columns of X through shared memory (G^T: both sides stay coalesced), all
 // of a piece's loads in flight.  Bound by HBM and the passes between barriers: B200, 32 of 1408 x 2048 FP32 146 us
@@ -1104,9 +1174,15 @@ __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs
                                   8 * static_cast<int64_t>(a.batch) * a.parts, a.dev_status);
             sum = block_sum(sum, shared);
             finite = sum < INFINITY;
-            const double norm = sqrt(sum) + a.eps;
+            const double root = sqrt(sum), norm = root + a.eps;
             // zeros stay zeros, whatever eps: its inverse may leave FP32
-            const double scale = sum > 0.0 ? a.scale / norm : 0.0;
+            double scale = sum > 0.0 ? a.scale / norm : 0.0;
+            int low = 0;
+            if (root < a.eps && root > 0.0) {  // root / norm is below 1 / 2
+                frexp(root / norm, &low);
+                scale = ldexp(scale, -low);
+            }
+            if (l == 0) write_factors(a, e, root / norm, low);
             int exponent = 0;
             const double mantissa = frexp(scale, &exponent);
             power = ldexpf(1.0f, exponent / 2);
@@ -1332,7 +1408,7 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t 
 struct Sizes {
     int64_t m, n, x_pitch, a_pitch, rest_rows, rest_cols;
     int parts;
-    size_t partials, rest, x, a, diagonal;  // bytes
+    size_t partials, factors, rest, x, a, diagonal;  // bytes
 };
 
 Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
@@ -1349,6 +1425,7 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
     const int64_t most = batch < 592 ? 592 / batch : 1;
     s.parts = static_cast<int>(parts < most ? parts : most);
     s.partials = round256(8 * static_cast<size_t>(batch) * s.parts);
+    s.factors = round256(sizeof(float4) * static_cast<size_t>(batch) * kMaxOrthogonalizeSteps);
     s.rest = round256(2 * static_cast<size_t>(kRestBlock) * batch * s.rest_rows * s.rest_cols);
     s.x = round256(2 * static_cast<size_t>(batch) * s.m * s.x_pitch);
     s.a = round256(2 * static_cast<size_t>(batch) * s.m * s.a_pitch);
@@ -1361,7 +1438,7 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
 size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols)
 {
     const Sizes s = sizes_of(batch, rows, cols);
-    return 256 + s.partials + s.rest + 2 * s.x + 2 * s.a + 2 * s.diagonal;
+    return 256 + s.partials + s.factors + s.rest + 2 * s.x + 2 * s.a + 2 * s.diagonal;
 }
 
 cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaStream_t s)
@@ -1374,7 +1451,8 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     // on a 256-byte boundary: rows are read 32 bytes at a time
     uint8_t* at = reinterpret_cast<uint8_t*>(round256(reinterpret_cast<uintptr_t>(g.workspace)));
     double* partials = reinterpret_cast<double*>(at);
-    __half* rest = reinterpret_cast<__half*>(at += z.partials);
+    float4* factors = reinterpret_cast<float4*>(at += z.partials);
+    __half* rest = reinterpret_cast<__half*>(at += z.factors);
     __half* x[2];
     x[0] = reinterpret_cast<__half*>(at += z.rest);
     x[1] = reinterpret_cast<__half*>(at += z.x);
@@ -1406,6 +1484,9 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     pa.x = x[0];
     pa.scale = S;
     pa.eps = g.eps;
+    pa.factors = factors;
+    pa.steps = g.steps;
+    for (int i = 0; i < 3 * g.steps; ++i) pa.coefficients[i] = g.coefficients[i];
     pa.dev_status = g.dev_status;
 
     // left operands in boxes of 128 rows x 64 of K, right ones of 64 rows (across: of K) x 64, stores of 32 x 64
@@ -1459,16 +1540,16 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     p.by_tma = by_tma;
     p.dev_status = g.dev_status;
     auto product = [&](int op, int64_t n, int64_t k, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md,
-                       const CUtensorMap& mt, const __half* addend, int64_t pitch, __half* out, double alpha,
-                       double gamma, double beta) {
+                       const CUtensorMap& mt, const __half* addend, int64_t pitch, __half* out, double on_x,
+                       double on_acc, double diag_acc) {
         p.m = static_cast<int>(z.m);
         p.n = static_cast<int>(n);
         p.k = static_cast<int>(k);
         p.addend = addend;
         p.pitch = pitch;
-        p.alpha = static_cast<float>(alpha);
-        p.gamma = static_cast<float>(gamma);
-        p.beta = static_cast<float>(beta);
+        p.on_x = static_cast<float>(on_x);
+        p.on_acc = static_cast<float>(on_acc);
+        p.diag_acc = static_cast<float>(diag_acc);
         p.out = op == kLast ? static_cast<uint16_t*>(g.out) : reinterpret_cast<uint16_t*>(out);
         p.ldo = op == kLast ? g.ldo : (op == kUpdate ? z.x_pitch : z.a_pitch);
         p.out_stride = op == kLast ? g.out_stride : z.m * p.ldo;
@@ -1482,24 +1563,20 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     };
     int now = 0;
     for (int i = 0; i < g.steps; ++i) {
-        const double ca = g.coefficients[3 * i], cb = g.coefficients[3 * i + 1], cc = g.coefficients[3 * i + 2];
         const bool last = i + 1 == g.steps;
+        p.factors = factors + i;
         // A = X X^T from the products of S X
-        p.diag_acc = static_cast<float>(1.0 / (S * S));
-        e = product(kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0, 0.0,
-                    kScaleA / (S * S));
+        e = product(kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0,
+                    kScaleA / (S * S), 1.0 / (S * S));
         if (e != cudaSuccess) return e;
         // B = b A + c A^2 with A = H + D
-        p.diag_b = static_cast<float>(cb);
-        p.diag_c = static_cast<float>(cc);
-        p.diag_acc = static_cast<float>(cc / kScaleA / kScaleA);
-        e = product(kSquare, z.m, z.m, a_left, a_right, b_store, b_turn, a, z.a_pitch, b, cb * kScaleB / kScaleA,
-                    cc * kScaleB / kScaleA, cc * kScaleB / kScaleA / kScaleA);
+        e = product(kSquare, z.m, z.m, a_left, a_right, b_store, b_turn, a, z.a_pitch, b, kScaleB / kScaleA,
+                    kScaleB / kScaleA / kScaleA, 1.0 / kScaleA / kScaleA);
         if (e != cudaSuccess) return e;
         // X <- (a + F) X + E X with B = E + F
         const double unit = last ? 1.0 / S : 1.0;
         e = product(last ? kLast : kUpdate, z.n, z.m, b_left, x_right[now], last ? out_store : x_store[now ^ 1],
-                    last ? out_store : a_turn, x[now], z.x_pitch, x[now ^ 1], ca * unit, unit, unit / kScaleB);
+                    last ? out_store : a_turn, x[now], z.x_pitch, x[now ^ 1], unit, unit / kScaleB, 0.0);
         if (e != cudaSuccess) return e;
         now ^= 1;
     }
