@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(c
             const float root = head_norm(f, a, scale), r = h < heads ? root : 0.0f;
             Two w[8];
             unit_weights(weights[kind], p, w);
-            // with e = r dy: dw += e x, dx = w e - x r^2 mean(w e x)
+            // with e = r dy: dw += e x, dx = w e - (r x) (r mean(w e x)); r^2 by itself may leave FP32
             Two sum = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -441,9 +441,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(c
                 sum = fma2(g[i], f[i], sum);
             }
             const float dot = head_sum(f2lo(sum) + f2hi(sum), a.lanes) * a.inv_D;
-            const Two back = both(-dot * r * r);
+            const Two back = both(-dot * r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = fma2(f[i], back, g[i]);
+            for (int i = 0; i < 8; ++i) f[i] = fma2(mul2_rn(f[i], both(r)), back, g[i]);
             if (scale != 1.0f) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = mul2_rn(f[i], both(scale));

@@ -1,0 +1,49 @@
+"""The gradient of the head norms at the ends of its range, against the formulas in 64 bits; every test
+through both libraries."""
+import pytest
+import torch
+
+import layer_ref as R
+from nvfp4_testlib import need_gpu
+
+nv = pytest.importorskip("nvfp4_bit_quantized_03_b200")
+B = nv.binding
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24      # half a step of FP32
+TINY = 2.0 ** -126  # below the normal range values come as subnormals or zero
+
+
+@pytest.fixture(params=["release", "checked"], autouse=True)
+def _library(request):
+    need_gpu()
+    if request.param == "release":
+        yield
+    else:
+        with B.bounds_checked():
+            yield
+
+
+# In half-steps of FP32: the root 16 (21 for the sum of squares, 2 for mean and eps, of which half, and 4 of its
+# own), dz turned back and times the weight 4, e = r dy 17 on top; n 17; the mean of their products 4 + 17 + 1 + 21 +
+# 1, times r 17 and times n 18 more: 24 for dx's first part, 84 for its second.  dw: 22 for each product, and its sum
+# 64 in a lane, 5 + 3 over heads and warps, 56 + 5 over the CTAs.
+@pytest.mark.parametrize("size,gradient,eps", [(1e18, 1e-6, 1e-6), (1e17, 1e-6, 1e-6), (1e17, 1e-9, 1e-6),
+                                               (1e16, 1e-9, 1e-6), (1e17, 1.0, 1e-6), (1e-14, 1e12, 1e-30),
+                                               (1e-10, 1e15, 1e-30)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_gradients_far_from_their_heads_in_size(size, gradient, eps, interleaved):
+    g = torch.Generator(device="cuda").manual_seed(7)
+    T, H, D = 11, 5, 64
+    x = size * torch.randn(T, H, D, generator=g, device="cuda")
+    d = gradient * torch.randn(T, H, D, generator=g, device="cuda")
+    w = 1 + 0.3 * torch.randn(D, generator=g, device="cuda")
+    table = B.rope_table(T, 32)
+    dx, _, dw, _ = B.qk_norm_rope_backward(d, None, x, None, None, table, w, eps=eps, interleaved=interleaved,
+                                           dx_dtype=torch.float32)
+    ref, dwr, (first, second, dsize) = R.qk_backward(d.cpu(), x.cpu(), w.cpu(), eps, None, table.cpu(), interleaved)
+    tol = U * (ref.abs() * (1 + 2.0 ** -7) + 24 * first + 84 * second) + TINY
+    off = (dx.double().cpu() - ref).abs()
+    assert (off <= tol).all(), float((off / tol).max())
+    assert ((dw.double().cpu() - dwr).abs() <= (22 + 133) * U * dsize + TINY).all()
