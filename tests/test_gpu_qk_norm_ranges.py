@@ -47,3 +47,26 @@ def test_gradients_far_from_their_heads_in_size(size, gradient, eps, interleaved
     off = (dx.double().cpu() - ref).abs()
     assert (off <= tol).all(), float((off / tol).max())
     assert ((dw.double().cpu() - dwr).abs() <= (22 + 133) * U * dsize + TINY).all()
+
+
+@pytest.mark.parametrize("H,D", [(20, 64), (3, 128), (7, 32), (5, 80)])
+@pytest.mark.parametrize("value,dtype", [(float("inf"), torch.bfloat16), (float("-inf"), torch.bfloat16),
+                                         (float("inf"), torch.float32)])
+def test_an_infinite_gradient_stays_with_its_value_of_the_weight(H, D, value, dtype):
+    """In the last head, and in every head before it, of a token among so many that a warp takes all heads of one: lanes
+    behind the last head have worked on another one before."""
+    T = 2600
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, H, D, generator=g, device="cuda").to(dtype)
+    d = torch.randn(T, H, D, generator=g, device="cuda").to(dtype)
+    w = 1 + 0.3 * torch.randn(D, generator=g, device="cuda")
+    clean, _, dw_clean, _ = B.qk_norm_rope_backward(d, None, x, None, q_weight=w)
+    for h in range(H):
+        hit = d.clone()
+        hit[100 * h, h, h + 3] = value
+        dx, _, dw, _ = B.qk_norm_rope_backward(hit, None, x, None, q_weight=w)
+        want = dw_clean.clone()
+        want[h + 3] = value * float(x[100 * h, h, h + 3])
+        assert torch.equal(dw, want), (h, dw[h + 3])
+        dx[100 * h, h] = clean[100 * h, h]
+        assert torch.equal(dx, clean)
