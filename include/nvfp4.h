@@ -643,7 +643,7 @@ size_t nvfp4_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t 
  * A and B in FP32, apart from the products: the error is about that of the final rounding to bf16.  A matrix
  * of zeros gives zeros, one with NaN or Inf too (and sets NVFP4_DEVSTAT_NONFINITE).
  * Limits: rows, cols <= 2^18, batch <= 65535, batch * rows * cols <= 2^36, 1 <= steps <= 32,
- * 0 <= eps <= 1e30, |coefficients| <= 1e6.
+ * 0 <= eps <= 1e30, |coefficients| <= 1e6, strides <= 2^38 (those of a single row or matrix are not used).
  */
 nvfp4_status nvfp4_orthogonalize(const void* G, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
                                  int64_t g_stride, int steps, const float* coefficients, double eps, void* out_bf16,

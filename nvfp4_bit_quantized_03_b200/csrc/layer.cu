@@ -14,7 +14,8 @@ namespace {
 
 constexpr int64_t kMaxHeads = 1 << 20;
 constexpr int64_t kMaxTokens = 1 << 30;
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+// beyond any GPU's memory; the output's tensor map takes strides below 2^40 bytes
+constexpr int64_t kMaxStride = int64_t(1) << 38;
 
 bool known_type(int dtype) { return dtype == NVFP4_OUT_F32 || dtype == NVFP4_OUT_BF16; }
 
