@@ -16,6 +16,7 @@ constexpr int64_t kMaxHeads = 1 << 20;
 constexpr int64_t kMaxTokens = 1 << 30;
 // beyond any GPU's memory; the output's tensor map takes strides below 2^40 bytes
 constexpr int64_t kMaxStride = int64_t(1) << 38;
+constexpr int64_t kMaxExtent = int64_t(1) << 48;
 
 bool known_type(int dtype) { return dtype == NVFP4_OUT_F32 || dtype == NVFP4_OUT_BF16; }
 
@@ -32,6 +33,9 @@ nvfp4_status check_heads(const nvfp4_heads& v, int64_t heads, int64_t tokens, in
     if (!v.data) return NVFP4_ERR_NULL;
     if (v.heads != heads || v.token_stride < 0 || v.head_stride < 0 || v.token_stride > kMaxStride ||
         v.head_stride > kMaxStride)
+        return NVFP4_ERR_SHAPE;
+    // from the first token or head to the last one
+    if ((tokens > 1 && v.token_stride > kMaxExtent / (tokens - 1)) || (heads > 1 && v.head_stride > kMaxExtent / (heads - 1)))
         return NVFP4_ERR_SHAPE;
     const int64_t per16 = dtype == NVFP4_OUT_F32 ? 4 : 8;
     if (!aligned16(v.data) || (tokens > 1 && v.token_stride % per16) || (heads > 1 && v.head_stride % per16))
