@@ -562,8 +562,10 @@ nvfp4_status nvfp4_combine_backward(const void* dout, int dout_dtype, int64_t ld
 /* Heads of a batch of tokens: value d of head h of token t is data[t * token_stride + h *
  * head_stride + d] (strides in elements), whatever lies between: a part of the product's output
  * rows, or an array by token or by head.  Device pointers, 16-byte aligned; strides multiples of 16
- * bytes.  Heads that are written must not overlap; those that are read may (a stride of 0).  The stride
- * of a single token or head is not used. */
+ * bytes.  Heads that are read may overlap (a stride of 0).  Those that are written share no value with one
+ * another or with any that are read, except that they may be the heads of their own in place (the
+ * same address, strides and type); calls where they do are refused (NVFP4_ERR_SHAPE).  The stride of a
+ * single token or head is not used. */
 typedef struct {
     void* data;
     int64_t heads;

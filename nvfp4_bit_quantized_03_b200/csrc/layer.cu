@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "api_common.h"
+#include "heads_overlap.h"
 
 using namespace nvfp4;
 
@@ -77,6 +78,32 @@ nvfp4_status take_heads(const HeadsPair& in, int64_t heads_q, int64_t heads_k, i
     return NVFP4_OK;
 }
 
+// No head that is written (views[n - 1]) shares a byte with another one of the call's, except that it may be
+// the head of its own that is read, at the same place.
+nvfp4_status check_apart(const HeadsPair* in, const HeadsView* const* views, int n, int64_t tokens, int64_t D)
+{
+    auto runs = [&](int i, int kind) {
+        const HeadsView& v = views[i][kind];
+        const int64_t size = in[i].dtype == NVFP4_OUT_F32 ? 4 : 2;
+        return Runs(v.data, v.heads, tokens, size * D, size * v.head_stride, size * v.token_stride);
+    };
+    auto same = [&](int i, int j, int kind) {
+        const HeadsView &a = views[i][kind], &b = views[j][kind];
+        return in[i].dtype == in[j].dtype && a.data == b.data && a.token_stride == b.token_stride &&
+               a.head_stride == b.head_stride;
+    };
+    for (int kind = 0; kind < 2; ++kind) {
+        if (views[n - 1][kind].heads == 0) continue;
+        const Runs out = runs(n - 1, kind);
+        for (int i = 0; i < n; ++i)
+            for (int other = 0; other < 2; ++other) {
+                if (views[i][other].heads == 0 || (other == kind && (i == n - 1 || same(i, n - 1, kind)))) continue;
+                if (runs_meet(out, runs(i, other))) return NVFP4_ERR_SHAPE;
+            }
+    }
+    return NVFP4_OK;
+}
+
 // What both directions share; in[0] is x.
 nvfp4_status head_args(HeadsArgs& a, const HeadsPair* in, HeadsView* const* views, int n, int64_t tokens,
                        int64_t D, const float* q_weight, const float* k_weight, float eps,
@@ -139,6 +166,7 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, int 
     if (st != NVFP4_OK) return st;
     int sms = 0;
     if ((st = current_device(&sms)) != NVFP4_OK) return st;
+    if ((st = check_apart(in, views, 2, tokens, head_dim)) != NVFP4_OK) return st;
     return from_cuda(launch_qk_norm_rope(a, in_dtype == NVFP4_OUT_F32, out_dtype == NVFP4_OUT_F32,
                                          interleaved != 0, sms, static_cast<cudaStream_t>(stream)));
 }
@@ -172,6 +200,7 @@ nvfp4_status nvfp4_qk_norm_rope_backward(const nvfp4_heads* dq, const nvfp4_head
     a.dweight[1] = dk_weight;
     int sms = 0;
     if ((st = current_device(&sms)) != NVFP4_OK) return st;
+    if ((st = check_apart(in, views, 3, tokens, head_dim)) != NVFP4_OK) return st;
     return from_cuda(launch_qk_norm_rope_backward(a, in_dtype == NVFP4_OUT_F32, grad_dtype == NVFP4_OUT_F32,
                                                   dx_dtype == NVFP4_OUT_F32, interleaved != 0,
                                                   static_cast<cudaStream_t>(stream)));

@@ -70,3 +70,35 @@ def test_an_infinite_gradient_stays_with_its_value_of_the_weight(H, D, value, dt
         assert torch.equal(dw, want), (h, dw[h + 3])
         dx[100 * h, h] = clean[100 * h, h]
         assert torch.equal(dx, clean)
+
+
+def test_outputs_over_other_heads_are_refused():
+    T, D = 40, 64
+    buf = torch.randn(T, 12, D, device="cuda").bfloat16()
+    q, k = buf[:, :4], buf[:, 4:8]
+    table = B.rope_table(T, D)
+    before = buf.clone()
+    wide = buf.view(torch.float32)  # [T, 12, D / 2]
+
+    def refused(f, *a, **kw):
+        with pytest.raises(B.NVFP4Error) as e:
+            f(*a, **kw)
+        assert e.value.status == B.ERR_SHAPE
+        torch.cuda.synchronize()
+        assert torch.equal(buf, before)
+    d = torch.randn(T, 4, D, device="cuda").bfloat16()
+    for out in (k, buf[:, 3:7], buf[:, 1:5], buf.flatten()[:T * 4 * D].view(T, 4, D), buf[1:].flatten()[:T * 4 * D].view(T, 4, D)):
+        refused(B.qk_norm_rope, q, k, None, table, q_out=out)
+        refused(B.qk_norm_rope_backward, d, d, q, k, None, table, dq_in=out)
+    refused(B.qk_norm_rope, q, k, None, table, q_out=buf[:, 8:], k_out=buf[:, 8:])
+    refused(B.qk_norm_rope, q, k, None, table, k_out=q)
+    refused(B.qk_norm_rope, q, q, None, table, k_out=q)  # read as queries too
+    refused(B.qk_norm_rope_backward, q, k, d, d, None, table, dq_in=k, dk_in=q)
+    two = torch.randn(T, 2, D, device="cuda").bfloat16()
+    refused(B.qk_norm_rope, q[:, :2], None, None, table, q_out=wide.as_strided((T, 2, D), (12 * D // 2, D, 1)))
+    refused(B.qk_norm_rope_backward, two, None, q[:, :2], None, None, table,
+            dq_in=wide.as_strided((T, 2, D), (12 * D // 2, D, 1)))
+    # beside them in the same rows, and in place
+    B.qk_norm_rope(q, k, None, table, q_out=q, k_out=buf[:, 8:])
+    B.qk_norm_rope_backward(d, buf[:, 8:], q, k, None, table, dq_in=d, dk_in=buf[:, 8:])
+    assert torch.equal(buf[:, 4:8], before[:, 4:8]) and not torch.equal(buf[:, 8:], before[:, 8:])
