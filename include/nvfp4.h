@@ -651,6 +651,11 @@ nvfp4_status nvfp4_orthogonalize(const void* G, int g_dtype, int64_t batch, int6
                                  int64_t g_stride, int steps, const float* coefficients, double eps, void* out_bf16,
                                  int64_t ldo, int64_t out_stride, void* workspace, int* dev_status, void* stream);
 
+/* For tests: how nvfp4_orthogonalize spreads A, A^2 and B X of these sizes on the current device (ways: HOST memory,
+ * 3 values): 256 or 128 for tiles of 256 x 256 by pairs of CTAs or 128 x 128 by single ones, 1, 2 or 4 for
+ * tiles of 128 x 64 by clusters of so many.  Queues nothing. */
+nvfp4_status nvfp4_selftest_orthogonalize_ways(int64_t batch, int64_t rows, int64_t cols, int* ways);
+
 #ifdef __cplusplus
 }
 #endif

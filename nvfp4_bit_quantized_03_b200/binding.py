@@ -203,6 +203,8 @@ def _open(path):
     L.nvfp4_qk_norm_rope_workspace_bytes.restype = sz
     L.nvfp4_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
     L.nvfp4_orthogonalize_workspace_bytes.restype = sz
+    L.nvfp4_selftest_orthogonalize_ways.argtypes = [i64, i64, i64, vp]
+    L.nvfp4_selftest_orthogonalize_ways.restype = i32
     hd = vp  # nvfp4_heads
     for name, argtypes in {
             "qk_norm_rope": [hd, hd, i32, i64, i64, vp, vp, f32, vp, vp, i64, i64, i32, hd, hd, i32, vp,
@@ -445,6 +447,13 @@ def selftest_bounds(dev_status, stream=None):
     end; after it the device status word has NVFP4_DEVSTAT_BOUNDS set."""
     _check(lib().nvfp4_selftest_bounds(_status(dev_status), _stream(stream)),
            "nvfp4_selftest_bounds")
+
+
+def selftest_orthogonalize_ways(batch, rows, cols):
+    """nvfp4_selftest_orthogonalize_ways: how the products of these sizes are spread on the current device."""
+    ways = (ctypes.c_int * 3)()
+    _check(lib().nvfp4_selftest_orthogonalize_ways(batch, rows, cols, ways), "nvfp4_selftest_orthogonalize_ways")
+    return tuple(ways)
 
 
 def linear_fprop(X, W, out=None, out_dtype=torch.float32, workspace=None, dev_status=None,

@@ -211,6 +211,15 @@ size_t nvfp4_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t 
     return matrices_ok(batch, rows, cols) ? orthogonalize_workspace(batch, rows, cols) : 0;
 }
 
+nvfp4_status nvfp4_selftest_orthogonalize_ways(int64_t batch, int64_t rows, int64_t cols, int* ways)
+{
+    if (!ways) return NVFP4_ERR_NULL;
+    if (!matrices_ok(batch, rows, cols)) return NVFP4_ERR_SHAPE;
+    int sms = 0;
+    const nvfp4_status st = current_device(&sms);
+    return st == NVFP4_OK ? from_cuda(orthogonalize_ways(batch, rows, cols, sms, ways)) : st;
+}
+
 nvfp4_status nvfp4_orthogonalize(const void* G, int g_dtype, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
                                  int64_t g_stride, int steps, const float* coefficients, double eps, void* out_bf16,
                                  int64_t ldo, int64_t out_stride, void* workspace, int* dev_status, void* stream)

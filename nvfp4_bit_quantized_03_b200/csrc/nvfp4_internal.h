@@ -259,6 +259,7 @@ struct OrthogonalizeArgs {
     int* dev_status;
 };
 size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);
+cudaError_t orthogonalize_ways(int64_t batch, int64_t rows, int64_t cols, int sm_count, int* ways);
 cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaStream_t s);
 
 cudaError_t launch_gemm_grouped(const GroupedGemmArgs& g, int sm_count, cudaStream_t s);

@@ -1441,6 +1441,18 @@ size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols)
     return 256 + s.partials + s.factors + s.rest + 2 * s.x + 2 * s.a + 2 * s.diagonal;
 }
 
+cudaError_t orthogonalize_ways(int64_t batch, int64_t rows, int64_t cols, int sm_count, int* ways)
+{
+    Resident resident;
+    const cudaError_t e = resident_on_device(sm_count, &resident);
+    if (e != cudaSuccess) return e;
+    const Sizes z = sizes_of(batch, rows, cols);
+    const Plan plans[3] = {plan_of(true, batch, z.m, z.m, z.n, resident), plan_of(true, batch, z.m, z.m, z.m, resident),
+                           plan_of(false, batch, z.m, z.n, z.m, resident)};
+    for (int i = 0; i < 3; ++i) ways[i] = plans[i].parts > 0 ? plans[i].parts : plans[i].cg * kBlock;
+    return cudaSuccess;
+}
+
 cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaStream_t s)
 {
     Resident resident;

@@ -111,3 +111,11 @@ def test_views_as_calls_have_them(meet):
     assert meet((0, 32, T, 2 * D, 2 * D, 64 * D), (0, 32, T, D, D, 32 * D))
     # rows of unlike strides that never meet, too many to try: they count as apart
     assert not meet((0, 1, T, 16, 0, 64), (32, 1, T, 16, 0, 128))
+
+
+def test_ways_of_orthogonalize_refusals():
+    f = B.lib().nvfp4_selftest_orthogonalize_ways
+    ways = (ctypes.c_int * 3)()
+    assert f(1, 4, 4, None) == B.ERR_NULL
+    for bad in ((0, 4, 4), (1, 0, 4), (1, 4, (1 << 18) + 1)):
+        assert f(*bad, ways) == B.ERR_SHAPE
