@@ -18,7 +18,7 @@
 //
 // Where |G|_F is below eps, X = t G / |G|_F with a t that the steps raise by a factor of about a each.  What is then
 // held is X 2^-l, with an l of the matrix's own before every step, from the bound t prod (|a| + |b| s^2 + |c| s^4) of
-// the singular values, that keeps it at 1 / 2 .. 1 until they get there; and B over a power of two that keeps the larger
+// the singular values, that keeps it at 1 / 4 .. 1 until they get there; and B over a power of two that keeps the larger
 // of b 4^l and c 16^l at 1 / 2 .. 1.  So X keeps its 22 bits however small t is, and a step without a its
 // product's.  (Held as it is, X was off by 1 % at |G|_F = 1e-8 eps and lost from 1e-10 eps on.)
 //
@@ -62,7 +62,7 @@ constexpr float kScaleB = 1024.0f;  // B times this
 
 // ---- the steps ---------------------------------------------------------------------------
 
-enum Product { kGram = 0, kSquare = 1, kUpdate = 2, kLast = 3 };
+enum Product { kGram = 0, kSquare = 1, kUpdate = 2, kLast = 3, kFirst = 4 };  // kFirst: the first step's gram
 
 constexpr int kBlock = 128;                    // rows of a CTA's left operand; its tensor-memory lanes
 constexpr int kDepth = 64;                     // K per pipeline stage (128 bytes of FP16)
@@ -96,7 +96,10 @@ static_assert(kBars * 8 + 16 <= kBarBytes, "barrier area");
 struct ProductArgs {
     int m, n, k;           // rows and columns of the result, length of the products
     int batch;
-    const float4* factors; // this step's of every matrix, kMaxOrthogonalizeSteps apart
+    float4* factors;       // this step's of every matrix, kMaxOrthogonalizeSteps apart
+    const double2* starts; // |G|_F of every matrix, and with eps
+    int steps;
+    float coefficients[3 * kMaxOrthogonalizeSteps];
     // result = alpha * (A or X) + beta * accumulator, with the matrix's factors (a, unit, b, c) and powers of two
     // `on_x` (the addend) and `on_acc`; with the diagonals, in FP32: A's sum_i and B's d_i,
     //   gram:   on_acc accumulator; sum_i = diag_acc accumulator_ii
@@ -104,7 +107,7 @@ struct ProductArgs {
     //   update: on_x (a + unit d_i) X + on_acc unit accumulator
     float on_x, on_acc, diag_acc;
     float* sums;           // A's diagonal [batch][fours]: written by gram (diag_acc accumulator_ii), read by square
-    float* diagonal;       // B's diagonal [batch][fours]: written by square, read by update
+    float2* diagonal;      // with B's diagonal d_i (a + unit d_i, unit) [batch][fours]: written by square, read by update
     int fours;             // m, rounded up to a multiple of 4
     const __half* addend;  // square: A; update: X [batch][m][pitch]
     int64_t pitch;
@@ -260,53 +263,96 @@ __device__ __forceinline__ float take(uint32_t* v, int k)
     }
     return __uint_as_float(r);
 }
+// The l of a matrix's first X 2^-l: 0 where |G|_F / (|G|_F + eps) is 1 / 2 or more, otherwise (by the exponents)
+// what leaves 1 / 4 .. 1 of it.
+__device__ __forceinline__ int start_power(double root, double norm)
+{
+    return root > 0.0 && root < 0.5 * norm ? (__double2hiint(root) >> 20) - (__double2hiint(norm) >> 20) + 1 : 0;
+}
+// The steps' factors (a, unit, b, c) of the matrices, a lane for each, by the loading warp of every CTA of the first
+// gram when its loads are on their way: nothing waits for it there (in prepare_kernel they took 3 % of a step of 1024
+// of 128 x 512 in registers, a matrix after the other 1 %).
+__device__ __forceinline__ void write_factors(const ProductArgs& p, int lane)
+{
+    const int64_t bytes = 16 * static_cast<int64_t>(p.batch) * kMaxOrthogonalizeSteps;
+    const int64_t ctas = gridDim.x;
+    for (int64_t e = blockIdx.x + lane * ctas; e < p.batch; e += 32 * ctas) {
+        const double2 start = ld_checked(p.starts + e, p.starts, 16 * static_cast<int64_t>(p.batch), p.dev_status);
+        float4* const factors = p.factors + e * kMaxOrthogonalizeSteps;
+        int low = start_power(start.x, start.y);
+        if (low == 0) {  // as for most
+            for (int i = 0; i < p.steps; ++i)
+                st_checked(factors + i, make_float4(p.coefficients[3 * i], 1.0f, p.coefficients[3 * i + 1],
+                                                    p.coefficients[3 * i + 2]),
+                           p.factors, bytes, p.dev_status);
+            continue;
+        }
+        double bound = start.x / start.y;
+        for (int i = 0; i < p.steps; ++i) {
+            const double ca = p.coefficients[3 * i], cb = p.coefficients[3 * i + 1], cc = p.coefficients[3 * i + 2];
+            const double square = bound * bound;
+            bound *= fabs(ca) + square * (fabs(cb) + square * fabs(cc));
+            int next = 0;  // X 2^-next behind the step; behind the last one X itself
+            if (low < 0 && i + 1 < p.steps && bound > 0.0 && bound < 0.5) frexp(bound, &next);
+            const double b = ldexp(cb, 2 * low), c = ldexp(cc, 4 * low);
+            int unit = 0;  // B is held times 2^-unit
+            if (low < 0) frexp(fmax(fabs(b), fabs(c)), &unit);
+            st_checked(factors + i,
+                       make_float4(static_cast<float>(ldexp(ca, low - next)), static_cast<float>(ldexp(1.0, unit + low - next)),
+                                   static_cast<float>(ldexp(b, -unit)), static_cast<float>(ldexp(c, -unit))),
+                       p.factors, bytes, p.dev_status);
+            low = next;
+        }
+    }
+}
 // What a product's lane takes its row's values times: the addend (its diagonal's part included), the accumulator, and
 // (square) A's diagonal in the value's column.
 struct Weights {
     float alpha, beta, gamma;
-    float b, c;  // square: of the diagonal
+    float own;  // square: A's diagonal in the row
+    float4 f;   // square: the matrix's factors
 };
 template <int OP>
-__device__ __forceinline__ Weights weights_of(const ProductArgs& p, int64_t e, float own)
+__device__ __forceinline__ Weights weights_of(const ProductArgs& p, int64_t e, int row)
 {
-    Weights w = {0.0f, p.on_acc, 0.0f, 0.0f, 0.0f};
-    if (OP == kGram) return w;
-    const float4 f = ld_checked(p.factors + e * kMaxOrthogonalizeSteps, p.factors,
-                                16 * ((static_cast<int64_t>(p.batch) - 1) * kMaxOrthogonalizeSteps + 1), p.dev_status);
+    Weights w = {0.0f, p.on_acc, 0.0f, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
     if (OP == kSquare) {
-        w.b = f.z;
-        w.c = f.w;
-        w.gamma = p.on_x * f.w;
-        w.alpha = fmaf(w.gamma, own, p.on_x * f.z);
-        w.beta = p.on_acc * f.w;
-    } else {
-        w.alpha = fmaf(p.on_x * f.y, own, p.on_x * f.x);
-        w.beta = p.on_acc * f.y;
+        const int64_t rows = static_cast<int64_t>(p.batch) * p.fours;
+        w.own = row < p.m ? ld_checked(p.sums + e * p.fours + row, p.sums, 4 * rows, p.dev_status) : 0.0f;
+        w.f = ld_checked(p.factors + e * kMaxOrthogonalizeSteps, p.factors,
+                         16 * ((static_cast<int64_t>(p.batch) - 1) * kMaxOrthogonalizeSteps + 1), p.dev_status);
+        w.gamma = p.on_x * w.f.w;
+        w.alpha = fmaf(w.gamma, w.own, p.on_x * w.f.z);
+        w.beta = p.on_acc * w.f.w;
+    } else if (OP != kGram) {
+        const int64_t rows = static_cast<int64_t>(p.batch) * p.fours;
+        const float2 d = row < p.m ? ld_checked(p.diagonal + e * p.fours + row, p.diagonal, 8 * rows, p.dev_status)
+                                   : make_float2(0.0f, 0.0f);
+        w.alpha = p.on_x * d.x;
+        w.beta = p.on_acc * d.y;
     }
     return w;
 }
-// A diagonal's value of row `row` of matrix e.
-__device__ __forceinline__ float diagonal_at(const float* d, const ProductArgs& p, int64_t e, int row)
-{
-    return row < p.m ? ld_checked(d + e * p.fours + row, d, 4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status)
-                     : 0.0f;
-}
-// Four of them, from row `row`, a multiple of 4 (rows behind m hold anything: nothing of them is kept).
+// A's diagonal in four rows from `row` on, a multiple of 4 (rows behind m hold anything: nothing of them is kept).
 __device__ __forceinline__ float4 diagonal_four(const float* d, const ProductArgs& p, int64_t e, int row)
 {
     if (row >= p.fours) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     return ld_checked(reinterpret_cast<const float4*>(d + e * p.fours + row), d,
                       4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status);
 }
-// Keeps a row's diagonal value of A (gram) or B (square) from its accumulator.
+// Keeps a row's diagonal value of A (gram), or what update makes of B's (square), from its accumulator.
 template <int OP>
-__device__ __forceinline__ void keep_diagonal(const ProductArgs& p, int64_t e, int row, float acc, float sum,
-                                              const Weights& w)
+__device__ __forceinline__ void keep_diagonal(const ProductArgs& p, int64_t e, int row, float acc, const Weights& w)
 {
     if (row >= p.m) return;
-    float* d = OP == kGram ? p.sums : p.diagonal;
-    const float v = OP == kGram ? p.diag_acc * acc : fmaf(w.b, sum, fmaf(w.c * sum, sum, w.c * p.diag_acc * acc));
-    st_checked(d + e * p.fours + row, v, d, 4 * static_cast<int64_t>(p.batch) * p.fours, p.dev_status);
+    const int64_t rows = static_cast<int64_t>(p.batch) * p.fours;
+    if (OP == kGram) {
+        st_checked(p.sums + e * p.fours + row, p.diag_acc * acc, p.sums, 4 * rows, p.dev_status);
+    } else {
+        const float d = fmaf(w.f.z, w.own, fmaf(w.f.w * w.own, w.own, w.f.w * p.diag_acc * acc));
+        st_checked(p.diagonal + e * p.fours + row, make_float2(fmaf(w.f.y, d, w.f.x), w.f.y), p.diagonal, 8 * rows,
+                   p.dev_status);
+    }
 }
 __device__ __forceinline__ float2 halves(uint32_t v)
 {
@@ -321,7 +367,7 @@ __device__ __forceinline__ float2 halves(uint32_t v)
 // is busy 76 % of those cycles) and the 83 bytes per ns that every SM then reads from L2.  20480 x 5120: gram 370 us,
 // square 101, update 777 (4 KB of X and its rest in and out per row of a tile on top).  Single CTAs are bound by
 // the 124 bytes per ns that an SM can read: 0.27 us for a step of a quarter of that work.
-template <int CG, int OP>
+template <int CG, int OP, bool FIRST>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_t,
@@ -535,9 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             fetch(c0, 0);  // on its way while the products are summed
             fetch(c0, 1);
-            // A's or B's diagonal in the lane's row, and with it the factors of what is added
-            const float own = OP == kGram ? 0.0f : diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
-            const Weights by_row = weights_of<OP>(p, c.e, own);
+            // what the lane's row takes, A's or B's diagonal in it included
+            const Weights by_row = weights_of<OP>(p, c.e, row);
             bool ready = lane == 0 ? wait_bounded(bar(kAccFull + buf), (it >> 1) & 1, abort_flag, p.dev_status) : false;
             ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
             if (!ready) break;
@@ -561,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     accumulator(2 * w + h, v);
                     if (SYMMETRIC && r0 == col + 32 * h)  // the diagonal's block
-                        keep_diagonal<OP>(p, c.e, row, take<32>(v, lane), own, by_row);
+                        keep_diagonal<OP>(p, c.e, row, take<32>(v, lane), by_row);
                     float4 across = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // A's diagonal in four columns
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -672,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) bulk_wait_all();
     }
+    if (FIRST && warp == 0) write_factors(p, lane);
 
     tc_fence_before();
     __syncthreads();
@@ -748,7 +794,7 @@ __device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t
         : "memory");
 }
 
-template <int OP, int PARTS>
+template <int OP, int PARTS, bool FIRST>
 __global__ void __launch_bounds__(kNarrowThreads, 1)
     narrow_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const ProductArgs p)
@@ -808,7 +854,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const int row = c.row + 32 * q + lane, col0 = c.col + rank * WIDTH + half * (WIDTH / 2);
     const bool writes = warp >= 2 && warp < kNarrowGate && row < p.m;
     uint32_t v[32];  // sums of the lane's row, 32 columns
-    float own = 0.0f;  // A's or B's diagonal in it
     Weights by_row = {};
     const int64_t plane = static_cast<int64_t>(c.e) * p.m;
     const int64_t matrix_values = static_cast<int64_t>(p.batch) * p.m * p.pitch;
@@ -842,6 +887,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 }
         }
         __syncwarp();
+        if (FIRST) write_factors(p, lane);
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
         uint32_t fills = 0;
@@ -889,8 +935,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 rest[g] = ld_checked(rest_at + 32 * g, p.rest, rest_bytes, p.dev_status);
             }
         }
-        if (OP != kGram) own = diagonal_at(OP == kSquare ? p.sums : p.diagonal, p, c.e, row);
-        by_row = weights_of<OP>(p, c.e, own);
+        by_row = weights_of<OP>(p, c.e, row);
         bool ready = lane == 0 ? wait_bounded(bar(ACC_FULL), 0, abort_flag, p.dev_status) : false;
         ready = __shfl_sync(0xFFFFFFFFu, ready ? 1 : 0, 0) != 0;
         if (ready) {
@@ -943,7 +988,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 uint32_t bits[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) bits[i] = __float_as_uint(f[i]);
-                keep_diagonal<OP>(p, c.e, row, take<8>(bits, row - col), own, by_row);
+                keep_diagonal<OP>(p, c.e, row, take<8>(bits, row - col), by_row);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(bits[i]);
             }
@@ -1030,9 +1075,7 @@ struct PrepareArgs {
     int rest_rows, rest_cols;
     __half* x;
     double scale, eps;
-    float4* factors;                    // [batch][kMaxOrthogonalizeSteps]
-    int steps;
-    float coefficients[3 * kMaxOrthogonalizeSteps];
+    double2* starts;                    // [batch]: |G|_F, and with eps
     int* dev_status;
 };
 
@@ -1113,37 +1156,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const PrepareArgs a)
                    8 * static_cast<int64_t>(a.batch) * a.parts, a.dev_status);
 }
 
-// The steps' factors (a, unit, b, c) of a matrix whose X starts as X 2^-low with singular values up to t.
-__device__ void write_factors(const PrepareArgs& a, int64_t e, double t, int low)
-{
-    const int64_t bytes = 16 * static_cast<int64_t>(a.batch) * kMaxOrthogonalizeSteps;
-    float4* const factors = a.factors + e * kMaxOrthogonalizeSteps;
-    if (low == 0) {  // as most are
-        const int i = threadIdx.x;
-        if (i < a.steps)
-            st_checked(factors + i, make_float4(a.coefficients[3 * i], 1.0f, a.coefficients[3 * i + 1], a.coefficients[3 * i + 2]),
-                       a.factors, bytes, a.dev_status);
-        return;
-    }
-    if (threadIdx.x != 0) return;
-    double bound = t;
-    for (int i = 0; i < a.steps; ++i) {
-        const double ca = a.coefficients[3 * i], cb = a.coefficients[3 * i + 1], cc = a.coefficients[3 * i + 2];
-        const double square = bound * bound;
-        bound *= fabs(ca) + square * (fabs(cb) + square * fabs(cc));
-        int next = 0;  // X 2^-next behind the step; behind the last one X itself
-        if (low < 0 && i + 1 < a.steps && bound > 0.0 && bound < 0.5) frexp(bound, &next);
-        const double b = ldexp(cb, 2 * low), c = ldexp(cc, 4 * low);
-        int unit = 0;  // B is held times 2^-unit
-        if (low < 0) frexp(fmax(fabs(b), fabs(c)), &unit);
-        st_checked(factors + i,
-                   make_float4(static_cast<float>(ldexp(ca, low - next)), static_cast<float>(ldexp(1.0, unit + low - next)),
-                               static_cast<float>(ldexp(b, -unit)), static_cast<float>(ldexp(c, -unit))),
-                   a.factors, bytes, a.dev_status);
-        low = next;
-    }
-}
-
 // X times the scale over the norm: in FP16 row by row, and the rest to it in the order of the products' epilogue.
 // A CTA takes pieces of 32 rows x 128 columns of X through shared memory (G^T: both sides stay coalesced), all
 // of a piece's loads in flight.  Bound by HBM and the passes between barriers: B200, 32 of 1408 x 2048 FP32 146 us
@@ -1175,14 +1187,14 @@ __global__ void __launch_bounds__(kNormThreads) prepare_kernel(const PrepareArgs
             sum = block_sum(sum, shared);
             finite = sum < INFINITY;
             const double root = sqrt(sum), norm = root + a.eps;
+            if (l == 0 && threadIdx.x == 0)
+                st_checked(a.starts + e, make_double2(root, norm), a.starts, 16 * static_cast<int64_t>(a.batch),
+                           a.dev_status);
+            // norm 2^l, in its exponent (an ldexp behind the division took 40 registers instead of 32)
+            const double divisor = __hiloint2double(__double2hiint(norm) + start_power(root, norm) * (1 << 20),
+                                                    __double2loint(norm));
             // zeros stay zeros, whatever eps: its inverse may leave FP32
-            double scale = sum > 0.0 ? a.scale / norm : 0.0;
-            int low = 0;
-            if (root < a.eps && root > 0.0) {  // root / norm is below 1 / 2
-                frexp(root / norm, &low);
-                scale = ldexp(scale, -low);
-            }
-            if (l == 0) write_factors(a, e, root / norm, low);
+            const double scale = sum > 0.0 ? a.scale / divisor : 0.0;
             int exponent = 0;
             const double mantissa = frexp(scale, &exponent);
             power = ldexpf(1.0f, exponent / 2);
@@ -1274,20 +1286,22 @@ template <int CG>
 auto product_of(int op)
 {
     switch (op) {
-        case kGram: return product_kernel<CG, kGram>;
-        case kSquare: return product_kernel<CG, kSquare>;
-        case kUpdate: return product_kernel<CG, kUpdate>;
-        default: return product_kernel<CG, kLast>;
+        case kFirst: return product_kernel<CG, kGram, true>;
+        case kGram: return product_kernel<CG, kGram, false>;
+        case kSquare: return product_kernel<CG, kSquare, false>;
+        case kUpdate: return product_kernel<CG, kUpdate, false>;
+        default: return product_kernel<CG, kLast, false>;
     }
 }
 template <int PARTS>
 auto narrow_of(int op)
 {
     switch (op) {
-        case kGram: return narrow_kernel<kGram, PARTS>;
-        case kSquare: return narrow_kernel<kSquare, PARTS>;
-        case kUpdate: return narrow_kernel<kUpdate, PARTS>;
-        default: return narrow_kernel<kLast, PARTS>;
+        case kFirst: return narrow_kernel<kGram, PARTS, true>;
+        case kGram: return narrow_kernel<kGram, PARTS, false>;
+        case kSquare: return narrow_kernel<kSquare, PARTS, false>;
+        case kUpdate: return narrow_kernel<kUpdate, PARTS, false>;
+        default: return narrow_kernel<kLast, PARTS, false>;
     }
 }
 auto narrow_of(int op, int parts)
@@ -1310,7 +1324,7 @@ cudaError_t resident_on_device(int sm_count, Resident* out)
     Resident& r = known[device];
     if (r.singles == 0) {
         cudaError_t e = cudaSuccess;
-        for (int op = 0; op < 4; ++op) {
+        for (int op = kGram; op <= kFirst; ++op) {
             const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
             if ((e = cudaFuncSetAttribute(product_of<1>(op), attr, kSmem)) != cudaSuccess) return e;
             if ((e = cudaFuncSetAttribute(product_of<2>(op), attr, kSmem)) != cudaSuccess) return e;
@@ -1408,7 +1422,7 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, int threads, size_t 
 struct Sizes {
     int64_t m, n, x_pitch, a_pitch, rest_rows, rest_cols;
     int parts;
-    size_t partials, factors, rest, x, a, diagonal;  // bytes
+    size_t partials, starts, factors, rest, x, a, sums, diagonal;  // bytes
 };
 
 Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
@@ -1425,11 +1439,13 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
     const int64_t most = batch < 592 ? 592 / batch : 1;
     s.parts = static_cast<int>(parts < most ? parts : most);
     s.partials = round256(8 * static_cast<size_t>(batch) * s.parts);
+    s.starts = round256(sizeof(double2) * static_cast<size_t>(batch));
     s.factors = round256(sizeof(float4) * static_cast<size_t>(batch) * kMaxOrthogonalizeSteps);
     s.rest = round256(2 * static_cast<size_t>(kRestBlock) * batch * s.rest_rows * s.rest_cols);
     s.x = round256(2 * static_cast<size_t>(batch) * s.m * s.x_pitch);
     s.a = round256(2 * static_cast<size_t>(batch) * s.m * s.a_pitch);
-    s.diagonal = round256(4 * static_cast<size_t>(batch) * ((s.m + 3) / 4 * 4));
+    s.sums = round256(4 * static_cast<size_t>(batch) * ((s.m + 3) / 4 * 4));
+    s.diagonal = round256(8 * static_cast<size_t>(batch) * ((s.m + 3) / 4 * 4));
     return s;
 }
 
@@ -1438,7 +1454,7 @@ Sizes sizes_of(int64_t batch, int64_t rows, int64_t cols)
 size_t orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols)
 {
     const Sizes s = sizes_of(batch, rows, cols);
-    return 256 + s.partials + s.factors + s.rest + 2 * s.x + 2 * s.a + 2 * s.diagonal;
+    return 256 + s.partials + s.starts + s.factors + s.rest + 2 * s.x + 2 * s.a + s.sums + s.diagonal;
 }
 
 cudaError_t orthogonalize_ways(int64_t batch, int64_t rows, int64_t cols, int sm_count, int* ways)
@@ -1463,7 +1479,8 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     // on a 256-byte boundary: rows are read 32 bytes at a time
     uint8_t* at = reinterpret_cast<uint8_t*>(round256(reinterpret_cast<uintptr_t>(g.workspace)));
     double* partials = reinterpret_cast<double*>(at);
-    float4* factors = reinterpret_cast<float4*>(at += z.partials);
+    double2* starts = reinterpret_cast<double2*>(at += z.partials);
+    float4* factors = reinterpret_cast<float4*>(at += z.starts);
     __half* rest = reinterpret_cast<__half*>(at += z.factors);
     __half* x[2];
     x[0] = reinterpret_cast<__half*>(at += z.rest);
@@ -1471,7 +1488,7 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     __half* a = reinterpret_cast<__half*>(at += z.x);
     __half* b = reinterpret_cast<__half*>(at += z.a);
     float* sums = reinterpret_cast<float*>(at += z.a);
-    float* diagonal = reinterpret_cast<float*>(at += z.diagonal);
+    float2* diagonal = reinterpret_cast<float2*>(at += z.sums);
 
     // X times S: values of about 1 where the rows of X are orthonormal
     const double S = std::ldexp(1.0, static_cast<int>(std::lround(0.5 * std::log2(static_cast<double>(z.n)))));
@@ -1496,9 +1513,7 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     pa.x = x[0];
     pa.scale = S;
     pa.eps = g.eps;
-    pa.factors = factors;
-    pa.steps = g.steps;
-    for (int i = 0; i < 3 * g.steps; ++i) pa.coefficients[i] = g.coefficients[i];
+    pa.starts = starts;
     pa.dev_status = g.dev_status;
 
     // left operands in boxes of 128 rows x 64 of K, right ones of 64 rows (across: of K) x 64, stores of 32 x 64
@@ -1551,6 +1566,9 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
     p.transposed = transposed;
     p.by_tma = by_tma;
     p.dev_status = g.dev_status;
+    p.starts = starts;
+    p.steps = g.steps;
+    for (int i = 0; i < 3 * g.steps; ++i) p.coefficients[i] = g.coefficients[i];
     auto product = [&](int op, int64_t n, int64_t k, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md,
                        const CUtensorMap& mt, const __half* addend, int64_t pitch, __half* out, double on_x,
                        double on_acc, double diag_acc) {
@@ -1565,7 +1583,7 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
         p.out = op == kLast ? static_cast<uint16_t*>(g.out) : reinterpret_cast<uint16_t*>(out);
         p.ldo = op == kLast ? g.ldo : (op == kUpdate ? z.x_pitch : z.a_pitch);
         p.out_stride = op == kLast ? g.out_stride : z.m * p.ldo;
-        const Plan plan = plan_of(op == kGram || op == kSquare, g.batch, z.m, n, k, resident);
+        const Plan plan = plan_of(op != kUpdate && op != kLast, g.batch, z.m, n, k, resident);
         if (plan.parts > 0)
             return launch_chained(narrow_of(op, plan.parts), dim3(static_cast<unsigned>(plan.parts * plan.workers)),
                                   kNarrowThreads, kNarrowSmem, plan.parts, s, ma, mb, p);
@@ -1578,7 +1596,7 @@ cudaError_t launch_orthogonalize(const OrthogonalizeArgs& g, int sm_count, cudaS
         const bool last = i + 1 == g.steps;
         p.factors = factors + i;
         // A = X X^T from the products of S X
-        e = product(kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0,
+        e = product(i == 0 ? kFirst : kGram, z.m, z.n, x_left[now], x_right[now], a_store, a_turn, nullptr, z.a_pitch, a, 0.0,
                     kScaleA / (S * S), 1.0 / (S * S));
         if (e != cudaSuccess) return e;
         // B = b A + c A^2 with A = H + D
