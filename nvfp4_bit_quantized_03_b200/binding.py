@@ -971,7 +971,8 @@ def qk_norm_rope(q, k, positions=None, table=None, q_weight=None, k_weight=None,
                  stream=None):
     """nvfp4_qk_norm_rope: every head of q [T, Hq, D] and k [T, Hk, D] (k may be None) normalised, times
     its weight, and rotated by its token's position (table: rope_table; None: no rotation).  The
-    outputs' type is that of q_out and k_out when given, else out_dtype."""
+    outputs' type is that of q_out and k_out when given, else out_dtype.  They may be q and k themselves, and
+    share no value with other heads of the call otherwise."""
     shape, k_shape, xq, xk, x_type, (qw, kw, at), angles = _head_inputs(q, k, positions, table, q_weight,
                                                                         k_weight)
     q_out, k_out, zq, zk, z_type = _head_outputs("q_out", "k_out", q_out, k_out, shape, k_shape, out_dtype,
@@ -1038,7 +1039,8 @@ def _coefficient_array(coefficients, steps):
 def orthogonalize(g, steps=5, coefficients=MUON_COEFFICIENTS, eps=1e-7, out=None, workspace=None,
                   dev_status=None, stream=None):
     """nvfp4_orthogonalize: the Newton-Schulz update (bf16) of a weight gradient [rows, cols], or of each
-    matrix of a batch [batch, rows, cols].  coefficients: (a, b, c), or a triple for each step."""
+    matrix of a batch [batch, rows, cols].  coefficients: (a, b, c), or a triple for each step.  A matrix with
+    NaN or Inf gives zeros; dev_status is what tells them from those of a zero gradient (DEVSTAT_NONFINITE)."""
     if g.dtype not in _F32_BF16:
         raise TypeError(f"g must be float32 or bfloat16, got {g.dtype}")
     if g.dim() not in (2, 3) or (g.shape[-1] > 1 and g.stride(-1) != 1):

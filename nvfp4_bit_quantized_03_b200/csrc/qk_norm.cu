@@ -309,8 +309,9 @@ __device__ __forceinline__ void zero_heads(Walk<F32> z, int64_t h, int64_t heads
 
 // A warp takes a token, or a slice of its heads; the values of its next heads are on their way while it works on
 // those before.  (The first ones are read for padding too, and not used.)  Bound by HBM: B200, 16384 tokens, 32 + 8
-// heads of 128, bf16 64 us (5.4 TB/s, issue slots 58 % busy); without the next heads under way 72, with the weights
-// read from memory for every head instead of from shared memory 70.
+// heads of 128, bf16 64 us (5.4 TB/s, issue slots 58 % busy), FP32 109 (6.2 TB/s); without the next heads under way 72,
+// with the weights read from memory for every head instead of from shared memory 70.  The bounds of 7 and 6 CTAs
+// (72 and 80 registers) make three of the eight variants spill, bf16 and FP32 to bf16 with halves paired 20 bytes each.
 template <bool IN_F32, bool OUT_F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps, IN_F32 ? 6 : 7) qk_norm_rope_kernel(const HeadsArgs a)
 {
@@ -374,10 +375,11 @@ __global__ void __launch_bounds__(32 * kWarps, IN_F32 ? 6 : 7) qk_norm_rope_kern
 
 // The first q_ctas CTAs take the queries, the others the keys: a warp keeps the partial sums of one weight's
 // gradient in registers over all its tokens.  The CTA's sums go to a row of the workspace.  B200, 16384 tokens, 32 +
-// 8 heads of 128, bf16 110 us with the second kernel (4.6 TB/s): 16 warps of 126 registers per SM leave the issue
-// slots 44 % busy and wait for the chain norm, dot, result.  One value at a time 130 us; more warps of fewer
-// registers spill (20 warps 141); a ring of copies in shared memory ahead of the warp changes nothing (110, and 54
-// against 42 us for 4096 tokens, 16 + 4 heads of 256, FP32); the next token's first heads and angles under way 137.
+// 8 heads of 128, bf16 111 us with the second kernel (4.6 TB/s), FP32 173 (5.8 TB/s): 16 warps of 125 to 128 registers
+// per SM leave the issue slots 44 % busy and wait for the chain norm, dot, result.  The bf16 variants spill nothing, those
+// with FP32 on one side up to 16 bytes; 20 warps spill more (141 us).  One value at a time 130 us; a ring of copies in
+// shared memory ahead of the warp changes nothing (110, and 54 against 42 us for 4096 tokens, 16 + 4 heads of 256,
+// FP32); the next token's first heads and angles under way 137.
 template <bool X_F32, bool Z_F32, bool DX_F32, bool INTERLEAVED>
 __global__ void __launch_bounds__(32 * kWarps, 4) qk_norm_rope_backward_kernel(const HeadsArgs a)
 {
